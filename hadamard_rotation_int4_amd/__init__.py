@@ -1,7 +1,7 @@
 """Python binding of libhr.so (ctypes): randomized Hadamard rotation, fused
 int4 / int8 quantization, HARP-style butterfly and mixed-radix processor, int4
-dequant, the W4A4 / W4A8 / W8A8 GEMMs and the online-rotation decode GEMM on
-MI355X (gfx950).
+dequant, the W4A4 / W4A8 / W8A8 GEMMs, the online-rotation decode GEMM, and the
+4-bit key/value cache with the attention over it, on MI355X (gfx950).
 
 Argument marshalling only: every step runs in the library's HIP kernels on
 torch's current stream.  Every tensor argument is checked (dtype, shape,
@@ -24,6 +24,7 @@ __all__ = ["HRError", "rotate", "rotate_quant_int4", "rotate_quant_int8", "quant
            "butterfly_coeffs", "butterfly_apply", "harp_blocks", "harp_apply", "harp_n_params", "harp_table_size",
            "dequant_int4", "w4a4_gemm", "w4a8_gemm", "w8a8_gemm", "rotate_quant_w4a4_gemm",
            "fp6_rows", "w4a4_to_fp6", "rotate_quant_fp6", "w4a4_gemm_fp6",
+           "KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_attention",
            "lib", "LIB_PATH", "SYMBOLS",
            "HR_OK", "HR_EINVAL", "HR_EUNSUPPORTED", "HR_EDEVICE", "HR_F32", "HR_BF16", "HR_F16"]
 
@@ -32,7 +33,15 @@ LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libhr.so")
 HR_OK, HR_EINVAL, HR_EUNSUPPORTED, HR_EDEVICE = 0, 1, 2, 3
 HR_F32, HR_BF16, HR_F16 = 0, 1, 2
 
-_i32, _i64, _vp = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+_i32, _i64, _vp, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p, ctypes.c_float
+
+
+class _CacheStruct(ctypes.Structure):
+    """hr_kv4_cache of include/hr.h."""
+    _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp), ("signs", _vp),
+                ("pages", _i64), ("heads", _i32), ("dim", _i32), ("page", _i32), ("group", _i32),
+                ("rotate", _i32)]
+
 
 # name -> (restype, argtypes); mirrors include/hr.h
 SYMBOLS = {
@@ -58,6 +67,11 @@ SYMBOLS = {
     "hr_w4a4_to_fp6": (_i32, [_vp, _vp, _i32, _i64, _i64, _i32, _vp, _vp, _vp]),
     "hr_rotate_quant_fp6": (_i32, [_vp, _i32, _vp, _i64, _i32, _i32, _i32, _vp, _vp, _vp]),
     "hr_w4a4_gemm_fp6": (_i32, [_vp, _vp, _vp, _vp, _i32, _i64, _i64, _i64, _i32, _vp, _vp, _vp]),
+    "hr_kv4_append": (_i32, [_vp, _vp, _vp, _i32, _i64, _i64, _vp, _i64, _vp]),
+    "hr_kv4_read": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp]),
+    "hr_kv4_attention": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i64, _f32,
+                                _i32, _i32, _vp, _vp, _i64, _vp]),
+    "hr_kv4_attention_workspace": (_i64, [_i32, _i32, _i64, _i32, _i32, _i32, _i64, _i32]),
 }
 
 
@@ -94,7 +108,7 @@ def _check(status: int, fn: str) -> None:
 
 
 _DT_NAME = {torch.float32: "float32", torch.bfloat16: "bfloat16", torch.float16: "float16",
-            torch.int8: "int8", torch.uint8: "uint8", torch.int32: "int32"}
+            torch.int8: "int8", torch.uint8: "uint8", torch.int32: "int32", torch.int64: "int64"}
 
 
 def _arg(t, name: str, dtypes, shape):
@@ -616,3 +630,190 @@ def w4a4_gemm_fp6(a_f6: torch.Tensor, a_scales: torch.Tensor, w_f6: torch.Tensor
     _check(lib.hr_w4a4_gemm_fp6(pa, psa, pw, psw, _dtype_code(sd), M, N, K, g, pc, pacc, _stream(dev)),
            "hr_w4a4_gemm_fp6")
     return (c, acc) if group_acc else c
+
+
+# ------------------------------------------------------------------ 4-bit key/value cache
+
+class KV4Cache:
+    """A paged 4-bit key/value cache (hr_kv4_cache): codes uint8
+    [pages][heads][page][dim/2] and scales fp16 [pages][heads][dim/group][page]
+    of the keys and of the values, and the rotation its vectors are held in
+    (rotate; signs: int8 [dim] of +-1, or None for all +1).  Checks the tensors
+    and keeps them; the calls below take it as their first argument."""
+
+    def __init__(self, k_codes: torch.Tensor, k_scales: torch.Tensor, v_codes: torch.Tensor,
+                 v_scales: torch.Tensor, rotate: bool = True, signs: torch.Tensor | None = None):
+        for t, name, nd in ((k_codes, "k_codes", 4), (k_scales, "k_scales", 4)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+            if t.dim() != nd:
+                raise ValueError(f"{name}: expected a {nd}-D tensor, got shape {tuple(t.shape)}")
+        pages, heads, page, half = (int(v) for v in k_codes.shape)
+        dim, groups = 2 * half, int(k_scales.shape[2])
+        if dim not in (64, 128, 256):
+            raise ValueError(f"dim={dim} not in (64, 128, 256)")
+        if groups < 1 or dim % groups or dim // groups not in (32, 64, 128, 256):
+            raise ValueError(f"k_scales: {groups} groups do not make groups of 32, 64, 128 or 256 of dim={dim}")
+        if page & (page - 1) or not 16 <= page <= 1 << 20:
+            raise ValueError(f"page={page} is not a power of two in [16, 2^20]")
+        if signs is not None and not rotate:
+            raise ValueError("signs go with rotate")
+        cshape, sshape = (pages, heads, page, half), (pages, heads, groups, page)
+        args = [_arg(k_codes, "k_codes", torch.uint8, cshape), _arg(k_scales, "k_scales", torch.float16, sshape),
+                _arg(v_codes, "v_codes", torch.uint8, cshape), _arg(v_scales, "v_scales", torch.float16, sshape),
+                _arg(signs, "signs", torch.int8, (dim,))]
+        if v_codes is None or v_scales is None:
+            raise TypeError("v_codes and v_scales must be tensors")
+        self.k_codes, self.k_scales, self.v_codes, self.v_scales, self.signs = (t for _, t in args)
+        self.pages, self.heads, self.page, self.dim, self.group = pages, heads, page, dim, dim // groups
+        self.rotate = bool(rotate)
+        self.device = k_codes.device
+        self._struct = _CacheStruct(*_ptrs(*args), pages, heads, dim, page, self.group, int(self.rotate))
+        self._ref = ctypes.addressof(self._struct)
+
+
+def kv4_cache(pages: int, heads: int, dim: int, page: int = 64, group: int | None = None, rotate: bool = True,
+              signs: torch.Tensor | None = None, device="cuda") -> KV4Cache:
+    """An empty KV4Cache (all zeros); group defaults to dim, one scale a vector."""
+    g = _group(dim if group is None else group, dim)
+    codes = torch.zeros((2, pages, heads, page, dim // 2), dtype=torch.uint8, device=device)
+    scales = torch.zeros((2, pages, heads, dim // g, page), dtype=torch.float16, device=device)
+    return KV4Cache(codes[0], scales[0], codes[1], scales[1], rotate=rotate, signs=signs)
+
+
+_KV4_TYPES = {torch.bfloat16: HR_BF16, torch.float16: HR_F16, torch.float32: HR_F32}
+
+
+def _kv4(cache, *named):
+    """Device and pointers of (name, tensor) pairs that a call on `cache` takes (None -> NULL)."""
+    dev = cache.device
+    out = []
+    for name, t in named:
+        if t is None:
+            out.append(None)
+            continue
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensor must live on the GPU")
+        if t.device != dev:
+            raise ValueError(f"{name}: on {t.device}, expected {dev}")
+        out.append(t.data_ptr())
+    return out
+
+
+def _kv4_rows(cache, t, name: str, heads: int | None, dtype=None):
+    """Check token rows [tokens][heads][dim] whose tokens may be strided (slices
+    of a fused projection); returns (tokens, heads, row stride)."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype not in _KV4_TYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name}: dtype {t.dtype} not in "
+                        f"{[_DT_NAME[d] for d in (_KV4_TYPES if dtype is None else (dtype,))]}")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.dim or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [tokens][{'heads' if heads is None else heads}]"
+                         f"[{cache.dim}]")
+    stride = t.stride()
+    row = shape[1] * cache.dim
+    if shape[0] and (stride[2] != 1 or (stride[1] != cache.dim and shape[1] != 1)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    step = stride[0] if shape[0] > 1 else row
+    if step < row or step * t.element_size() % 16:
+        raise ValueError(f"{name}: tokens {step} elements apart; they must not overlap and be a multiple of 16 bytes apart")
+    return shape[0], shape[1], step
+
+
+def _kv4_index(t, name: str, dtype, shape):
+    """Check an index tensor: dtype, shape (an int is any size where negative), contiguous."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: dtype {t.dtype} not in {[_DT_NAME[dtype]]}")
+    if t.dim() != len(shape) or any(w >= 0 and v != w for v, w in zip(t.shape, shape)):
+        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if w < 0 else w for w in shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: tensor must be contiguous")
+    return t
+
+
+def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
+    """Quantize keys and values into the cache (hr_kv4_append).  k, v: [tokens]
+    [heads][dim] bf16, fp16 or fp32, of one dtype, tokens may be strided; slots:
+    int64 [tokens], page * cache.page + place, all different, a slot outside the
+    cache writes nothing."""
+    tokens, _, ks = _kv4_rows(cache, k, "k", getattr(cache, "heads", None))
+    vt, _, vs = _kv4_rows(cache, v, "v", cache.heads, k.dtype)
+    if vt != tokens:
+        raise ValueError(f"v: {vt} tokens, but k has {tokens}")
+    _kv4_index(slots, "slots", torch.int64, (tokens,))
+    pk, pv, psl = _kv4(cache, ("k", k), ("v", v), ("slots", slots))
+    _check(lib.hr_kv4_append(cache._ref, pk, pv, _KV4_TYPES[k.dtype], ks, vs, psl, tokens, _stream(cache.device)),
+           "hr_kv4_append")
+
+
+def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
+             v: torch.Tensor | None = None):
+    """The keys and values that slots of the cache stand for (hr_kv4_read):
+    (k, v), each [tokens][heads][dim] of dtype; zeros for a slot outside it."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
+    _kv4_index(slots, "slots", torch.int64, (-1,))
+    if dtype not in _KV4_TYPES:
+        raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
+    shape = (slots.shape[0], cache.heads, cache.dim)
+    _arg(k, "k", dtype, shape)
+    _arg(v, "v", dtype, shape)
+    if k is None:
+        k = torch.empty(shape, dtype=dtype, device=cache.device)
+    if v is None:
+        v = torch.empty(shape, dtype=dtype, device=cache.device)
+    psl, pk, pv = _kv4(cache, ("slots", slots), ("k", k), ("v", v))
+    _check(lib.hr_kv4_read(cache._ref, psl, shape[0], _KV4_TYPES[dtype], pk, pv, _stream(cache.device)),
+           "hr_kv4_read")
+    return k, v
+
+
+def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
+                  starts: torch.Tensor | None = None, max_new: int = 1, max_len: int | None = None,
+                  scale: float | None = None, causal: bool = True, window: int = 0,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of query rows over the cache (hr_kv4_attention).  q: [total]
+    [q_heads][dim] bf16, fp16 or fp32, rows may be strided; table: int32
+    [batch][width] page ids; lens: int32 [batch] cached tokens of each sequence,
+    its new ones among them; starts: int32 [batch + 1] first row of each
+    sequence in q, or None when each has max_new rows.  max_new and max_len
+    (width * page if None) bound the rows and the lengths; scale defaults to
+    1/sqrt(dim); window > 0 sees only that many tokens back.  workspace: uint8,
+    kept by a caller that captures the call in a graph; allocated when None.
+    Returns out [total][q_heads][dim] of q's dtype, 0 in a row that sees no
+    token."""
+    total, q_heads, step = _kv4_rows(cache, q, "q", None)
+    _kv4_index(table, "table", torch.int32, (-1, -1))
+    batch, width = table.shape
+    _kv4_index(lens, "lens", torch.int32, (batch,))
+    if starts is not None:
+        _kv4_index(starts, "starts", torch.int32, (batch + 1,))
+    if q_heads < 1 or q_heads % cache.heads:
+        raise ValueError(f"q: {q_heads} heads are not a multiple of the cache's {cache.heads}")
+    if max_len is None:
+        max_len = min(width * cache.page, 1 << 30)
+    if scale is None:
+        scale = cache.dim ** -0.5
+    _arg(out, "out", q.dtype, (total, q_heads, cache.dim))
+    if out is None:
+        out = torch.empty((total, q_heads, cache.dim), dtype=q.dtype, device=cache.device)
+    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, total, batch, q_heads, max_new, max_len, window)
+    if workspace is not None:
+        _kv4_index(workspace, "workspace", torch.uint8, (-1,))
+        if workspace.shape[0] < need:
+            raise ValueError(f"workspace: {workspace.shape[0]} bytes, {need} needed")
+    elif need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    pq, pt, pl, pst, po, pw = _kv4(cache, ("q", q), ("table", table), ("lens", lens), ("starts", starts),
+                                   ("out", out), ("workspace", workspace))
+    _check(lib.hr_kv4_attention(cache._ref, pq, _KV4_TYPES[q.dtype], step, total, pst, pt, width, pl, batch,
+                                q_heads, max_new, max_len, scale, int(causal), window, po, pw,
+                                0 if workspace is None else workspace.shape[0], _stream(cache.device)),
+           "hr_kv4_attention")
+    return out

@@ -553,4 +553,180 @@ int32_t hr_w4a4_gemm_fp6(const uint8_t* a_f6, const void* a_scales, const uint8_
   return from_hip(hr::launch_gemm_fp6(a, static_cast<hipStream_t>(stream)), fn);
 }
 
+// Checks a cache description and fills the internal one.  The arrays may be
+// NULL only when no token is touched (`need` false).
+static int32_t kv4_cache(const char* fn, const hr_kv4_cache* c, bool need, hr::Kv4Cache* out) {
+  if (!c) return fail(HR_EINVAL, "%s: cache is NULL", fn);
+  if (c->pages < 0) return fail(HR_EINVAL, "%s: pages < 0", fn);
+  if (c->rotate != 0 && c->rotate != 1) return fail(HR_EINVAL, "%s: rotate must be 0 or 1", fn);
+  if (need && c->pages > 0 && (!c->k_codes || !c->k_scales || !c->v_codes || !c->v_scales))
+    return fail(HR_EINVAL, "%s: the cache's codes and scales are required", fn);
+  if (!aligned16(c->k_codes) || !aligned16(c->k_scales) || !aligned16(c->v_codes) || !aligned16(c->v_scales) ||
+      !aligned16(c->signs))
+    return fail(HR_EINVAL, "%s: the cache's pointers must be 16-byte aligned", fn);
+  if (c->dim != 64 && c->dim != 128 && c->dim != 256)
+    return fail(HR_EUNSUPPORTED, "%s: dim=%d not in {64,128,256}", fn, c->dim);
+  if (!valid_group(c->group) || c->dim % c->group)
+    return fail(HR_EUNSUPPORTED, "%s: group=%d invalid for dim=%d", fn, c->group, c->dim);
+  if (!pow2(c->page) || c->page < 16 || c->page > (1 << 20))
+    return fail(HR_EUNSUPPORTED, "%s: page=%d is not a power of two in [16, 2^20]", fn, c->page);
+  if (c->heads < 1 || c->heads > 65535)
+    return fail(HR_EUNSUPPORTED, "%s: heads=%d outside [1, 65535]", fn, c->heads);
+  if (c->pages > INT32_MAX) return fail(HR_EUNSUPPORTED, "%s: more than 2^31 - 1 pages", fn);
+  *out = hr::Kv4Cache{};
+  out->codes[0] = c->k_codes;
+  out->codes[1] = c->v_codes;
+  out->scales[0] = static_cast<_Float16*>(c->k_scales);
+  out->scales[1] = static_cast<_Float16*>(c->v_scales);
+  out->signs = c->rotate ? c->signs : nullptr;
+  out->pages = c->pages;
+  out->heads = c->heads;
+  out->dim = c->dim;
+  out->group = c->group;
+  out->page_log2 = ilog2(c->page);
+  out->rotate = c->rotate;
+  return HR_OK;
+}
+
+static bool kv4_dtype(int32_t dt) { return dt == HR_F32 || dt == HR_BF16 || dt == HR_F16; }
+
+// Rows `stride` elements apart: long enough and 16-byte aligned.
+static bool kv4_stride(int64_t stride, int64_t row, int32_t dtype) {
+  return stride >= row && stride % (dtype == HR_F32 ? 4 : 8) == 0;
+}
+
+int32_t hr_kv4_append(const hr_kv4_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                      int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream) {
+  const char* fn = "hr_kv4_append";
+  if (tokens < 0) return fail(HR_EINVAL, "%s: tokens < 0", fn);
+  if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  hr::Kv4AppendArgs a{};
+  const int32_t st = kv4_cache(fn, cache, tokens > 0, &a.c);
+  if (st) return st;
+  if (tokens > 0 && (!k || !v || !slots)) return fail(HR_EINVAL, "%s: k, v and slots are required", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(HR_EINVAL, "%s: k and v must be 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(HR_EINVAL, "%s: slots must be 8-byte aligned", fn);
+  const int64_t row = (int64_t)cache->heads * cache->dim;
+  if (!kv4_stride(k_stride, row, dtype) || !kv4_stride(v_stride, row, dtype))
+    return fail(HR_EINVAL, "%s: k_stride and v_stride must be at least heads * dim and multiples of 16 bytes", fn);
+  if (tokens > INT32_MAX / cache->heads)
+    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^31 - 1", fn);
+  if (tokens == 0 || cache->pages == 0) return ok();
+  a.x[0] = k;
+  a.x[1] = v;
+  a.stride[0] = k_stride;
+  a.stride[1] = v_stride;
+  a.dtype = dtype;
+  a.slots = slots;
+  a.tokens = tokens;
+  return from_hip(hr::launch_kv4_append(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tokens, int32_t dtype, void* k,
+                    void* v, void* stream) {
+  const char* fn = "hr_kv4_read";
+  if (tokens < 0) return fail(HR_EINVAL, "%s: tokens < 0", fn);
+  if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  hr::Kv4ReadArgs a{};
+  const int32_t st = kv4_cache(fn, cache, tokens > 0, &a.c);
+  if (st) return st;
+  if (tokens > 0 && (!k || !v || !slots)) return fail(HR_EINVAL, "%s: k, v and slots are required", fn);
+  if (!aligned16(k) || !aligned16(v)) return fail(HR_EINVAL, "%s: k and v must be 16-byte aligned", fn);
+  if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(HR_EINVAL, "%s: slots must be 8-byte aligned", fn);
+  if (tokens > INT32_MAX / cache->heads)
+    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^31 - 1", fn);
+  if (tokens == 0) return ok();
+  a.y[0] = k;
+  a.y[1] = v;
+  a.dtype = dtype;
+  a.slots = slots;
+  a.tokens = tokens;
+  return from_hip(hr::launch_kv4_read(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// Workspace of a planned call: partial sums, then (max, sum) pairs.
+static int64_t kv4_workspace(const hr::Kv4AttnArgs& a) {
+  return a.nsplit > 1 ? a.total * a.q_heads * a.nsplit * (4 * (int64_t)a.c.dim + 8) : 0;
+}
+
+int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int64_t total, int32_t batch, int32_t q_heads,
+                                   int32_t max_new, int64_t max_len, int32_t window) {
+  if (heads < 1 || dim < 1 || total < 1 || batch < 1 || q_heads < heads || max_new < 1 || max_len < 0 || window < 0)
+    return 0;
+  hr::Kv4AttnArgs a{};
+  a.c.heads = heads;
+  a.c.dim = dim;
+  a.total = total;
+  a.batch = batch;
+  a.q_heads = q_heads;
+  a.rep = q_heads / heads;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.window = window;
+  hr::kv4_attention_plan(&a);
+  return kv4_workspace(a);
+}
+
+int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype, int64_t q_stride, int64_t total,
+                         const int32_t* starts, const int32_t* table, int64_t width, const int32_t* lens,
+                         int32_t batch, int32_t q_heads, int32_t max_new, int64_t max_len, float scale,
+                         int32_t causal, int32_t window, void* out, void* workspace, int64_t workspace_bytes,
+                         void* stream) {
+  const char* fn = "hr_kv4_attention";
+  if (total < 0 || batch < 0 || width < 0 || max_new < 0 || max_len < 0 || window < 0 || workspace_bytes < 0)
+    return fail(HR_EINVAL, "%s: negative size", fn);
+  if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  if (causal != 0 && causal != 1) return fail(HR_EINVAL, "%s: causal must be 0 or 1", fn);
+  if (!(scale > 0.0f) || !(scale <= 3.4028235e38f)) return fail(HR_EINVAL, "%s: scale must be positive and finite", fn);
+  hr::Kv4AttnArgs a{};
+  const bool some = total > 0 && batch > 0;
+  const int32_t st = kv4_cache(fn, cache, some, &a.c);
+  if (st) return st;
+  if (some && (!q || !lens || !out || (!table && width > 0)))
+    return fail(HR_EINVAL, "%s: q, table, lens and out are required", fn);
+  if (!aligned16(q) || !aligned16(out) || !aligned16(workspace))
+    return fail(HR_EINVAL, "%s: q, out and workspace must be 16-byte aligned", fn);
+  if ((reinterpret_cast<uintptr_t>(starts) | reinterpret_cast<uintptr_t>(table) | reinterpret_cast<uintptr_t>(lens)) & 3u)
+    return fail(HR_EINVAL, "%s: starts, table and lens must be 4-byte aligned", fn);
+  if (q_heads < 1 || q_heads % cache->heads)
+    return fail(HR_EUNSUPPORTED, "%s: q_heads=%d is not a multiple of heads=%d", fn, q_heads, cache->heads);
+  if (!kv4_stride(q_stride, (int64_t)q_heads * cache->dim, dtype))
+    return fail(HR_EINVAL, "%s: q_stride must be at least q_heads * dim and a multiple of 16 bytes", fn);
+  if (!starts && (int64_t)batch * max_new != total)
+    return fail(HR_EINVAL, "%s: without starts, total must be batch * max_new", fn);
+  if (total > INT32_MAX / q_heads || max_new > INT32_MAX / q_heads)
+    return fail(HR_EUNSUPPORTED, "%s: rows * q_heads above 2^31 - 1", fn);
+  if (batch > 65535) return fail(HR_EUNSUPPORTED, "%s: batch=%d above 65535", fn, batch);
+  if (max_len > hr::kKv4MaxLen) return fail(HR_EUNSUPPORTED, "%s: max_len above 2^30", fn);
+  if (!some || max_new == 0) return ok();
+  a.q = q;
+  a.q_stride = q_stride;
+  a.dtype = dtype;
+  a.total = total;
+  a.starts = starts;
+  a.table = table;
+  a.width = cache->pages > 0 ? width : 0;
+  a.lens = lens;
+  a.batch = batch;
+  a.q_heads = q_heads;
+  a.rep = q_heads / cache->heads;
+  a.max_new = max_new;
+  a.max_len = max_len;
+  a.scale = scale;
+  a.causal = causal;
+  a.window = window;
+  a.out = out;
+  hr::kv4_attention_plan(&a);
+  if ((int64_t)cache->heads * a.tiles * a.nsplit > INT32_MAX)
+    return fail(HR_EUNSUPPORTED, "%s: too many rows for one launch", fn);
+  const int64_t need = kv4_workspace(a);
+  if (need > 0) {
+    if (!workspace || workspace_bytes < need)
+      return fail(HR_EINVAL, "%s: workspace of %lld bytes needed", fn, (long long)need);
+    a.part_o = static_cast<float*>(workspace);
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + total * q_heads * a.nsplit * cache->dim);
+  }
+  return from_hip(hr::launch_kv4_attention(a, static_cast<hipStream_t>(stream)), fn);
+}
+
 }  // extern "C"

@@ -1,7 +1,8 @@
 /*
  * hr.h -- C ABI of libhr.so: randomized Hadamard rotation, fused int4 (and
- * int8) quantization, HARP-style butterfly, int4 dequant and the W4A4 (and
- * W4A8) GEMM on AMD Instinct MI355X (gfx950).
+ * int8) quantization, HARP-style butterfly, int4 dequant, the W4A4 (and
+ * W4A8) GEMM, and the 4-bit key/value cache with the attention over it, on AMD
+ * Instinct MI355X (gfx950).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -479,6 +480,109 @@ int32_t hr_rotate_quant_w4a4_gemm(const void* x, int32_t x_dtype, const int8_t* 
                                   const uint8_t* w_codes, const void* w_scales, int32_t scale_dtype,
                                   int64_t M, int64_t N, int64_t K, float* c, uint8_t* a_codes,
                                   void* a_scales, void* stream);
+
+/*
+ * The 4-bit key/value cache: keys and values of a transformer's attention,
+ * rotated per head and held as int4 codes with fp16 group scales in pages of
+ * `page` tokens.
+ *
+ * Defines: the quantizer and the rotation are those of "Experiment -- Hadamard
+ * rotation for int4 (W4A4) accuracy" (Hypothesis and Method), per head of dim
+ * elements; the random sign diagonal is HARP's incoherence processing.
+ *
+ *   k_codes, v_codes    [pages][heads][page][dim / 2] packed int4.
+ *   k_scales, v_scales  [pages][heads][dim / group][page] fp16.
+ *   signs   [dim] int8 +-1, or NULL (all +1); only read with rotate.
+ *   rotate  1: y = H_dim (d * x) / sqrt(dim) is what the codes hold; 0: x.
+ *   heads   key/value heads, >= 1;  dim in {64, 128, 256}.
+ *   page    tokens of a page, a power of two in [16, 2^20].
+ *   group   in {32, 64, 128, 256}, dividing dim.
+ * A token's slot is page_id * page + its place in the page.  The struct itself
+ * is host memory, read during the call; its arrays are device memory, 16-byte
+ * aligned.
+ */
+typedef struct {
+  uint8_t* k_codes;
+  void* k_scales;
+  uint8_t* v_codes;
+  void* v_scales;
+  const int8_t* signs;
+  int64_t pages;
+  int32_t heads, dim, page, group, rotate;
+} hr_kv4_cache;
+
+/*
+ * hr_kv4_append -- quantize the keys and values of some tokens into the cache.
+ *
+ * For the key and the value x of every (token, head): y = x or its rotation;
+ * per group a = max |y|, s = fp16(a / 7) (stored), k = 1 / s (0 when s == 0),
+ * q = clamp(rint(y k), -7, 7), each step one fp32 operation rounded to nearest
+ * even (with the rotation, k and 1 / sqrt(dim) are one factor).
+ * A (token, head) whose key or value is not finite, or needs a scale above the
+ * fp16 range, is stored with zero codes and NaN scales in both: reading it, or
+ * attending to it, gives NaN.
+ *
+ *   k, v      [tokens] rows of [heads][dim] of dtype (HR_F32, HR_BF16 or
+ *             HR_F16), rows k_stride / v_stride elements apart (at least
+ *             heads * dim; a multiple of 16 bytes).
+ *   slots     [tokens] int64, all different; a slot outside
+ *             [0, pages * page) writes nothing.
+ */
+int32_t hr_kv4_append(const hr_kv4_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride,
+                      int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream);
+
+/*
+ * hr_kv4_read -- the keys and values that slots of the cache stand for:
+ * x_hat = d * H_dim (q s) / sqrt(dim) (q s without the rotation), rounded once
+ * to dtype.
+ *
+ *   slots     [tokens] int64; a slot outside [0, pages * page) reads zeros.
+ *   k, v      [tokens][heads][dim] of dtype (HR_F32, HR_BF16 or HR_F16).
+ */
+int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tokens, int32_t dtype, void* k,
+                    void* v, void* stream);
+
+/*
+ * hr_kv4_attention -- softmax attention of query rows over the cache, in its
+ * 4-bit form: queries are rotated and outputs rotated back inside.
+ *
+ * Sequence b has lens[b] cached tokens; token j of it is at place j % page of
+ * page table[b][j / page].  Its query rows are starts[b] .. starts[b + 1] - 1
+ * (its newest tokens, whose keys and values are cached already), row i of its
+ * `new` at position pos = lens[b] - new + i.  Query head h attends to
+ * key/value head h / (q_heads / heads):
+ *   out = sum_j softmax_j(scale q . k_j) v_j
+ * over the tokens j < lens[b] with j <= pos (causal) and j > pos - window
+ * (window > 0); 0 for a row that sees none.
+ *
+ *   q         [total] rows of [q_heads][dim] of dtype (HR_F32, HR_BF16 or
+ *             HR_F16), rows q_stride elements apart (at least q_heads * dim; a
+ *             multiple of 16 bytes).
+ *   starts    [batch + 1] int32, not decreasing, or NULL: max_new rows each
+ *             (total = batch * max_new).
+ *   table     [batch][width] int32 page ids; only entries of cached tokens are
+ *             used.  An id outside [0, pages) is read as 0.
+ *   lens      [batch] int32 (device), at most width * page.
+ *   q_heads   a multiple of heads.
+ *   max_new, max_len  upper bounds of a sequence's query rows and cached
+ *             length, for the launch; rows past max_new are not computed.  A
+ *             max_len below a sequence's length costs time only.
+ *   scale     multiplies q . k; 1 / sqrt(dim) usually.
+ *   causal    0 or 1;  window >= 0 (0: none).
+ *   out       [total][q_heads][dim] of dtype; rows of no sequence are left.
+ *   workspace device memory of at least hr_kv4_attention_workspace(...) bytes
+ *             (NULL when that is 0), in use until the stream has run the call.
+ */
+int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype, int64_t q_stride, int64_t total,
+                         const int32_t* starts, const int32_t* table, int64_t width, const int32_t* lens,
+                         int32_t batch, int32_t q_heads, int32_t max_new, int64_t max_len, float scale,
+                         int32_t causal, int32_t window, void* out, void* workspace, int64_t workspace_bytes,
+                         void* stream);
+
+/* Bytes of workspace of an hr_kv4_attention call of these sizes (0: none;
+ * negative sizes give 0). */
+int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int64_t total, int32_t batch, int32_t q_heads,
+                                   int32_t max_new, int64_t max_len, int32_t window);
 
 #ifdef __cplusplus
 }

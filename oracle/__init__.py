@@ -29,4 +29,4 @@ Modules and the passages they follow:
 
 Readings of points the pages leave open are stated where they are used.
 """
-from . import hadamard, mixed_radix, butterfly, quant, gemm, probe, harp  # noqa: F401
+from . import hadamard, mixed_radix, butterfly, quant, gemm, probe, harp, kv4  # noqa: F401
