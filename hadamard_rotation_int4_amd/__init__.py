@@ -801,8 +801,6 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     if scale is None:
         scale = cache.dim ** -0.5
     _arg(out, "out", q.dtype, (total, q_heads, cache.dim))
-    if out is None:
-        out = torch.empty((total, q_heads, cache.dim), dtype=q.dtype, device=cache.device)
     need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, total, batch, q_heads, max_new, max_len, window)
     if workspace is not None:
         _kv4_index(workspace, "workspace", torch.uint8, (-1,))
@@ -810,6 +808,8 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
             raise ValueError(f"workspace: {workspace.shape[0]} bytes, {need} needed")
     elif need:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    if out is None:
+        out = torch.empty((total, q_heads, cache.dim), dtype=q.dtype, device=cache.device)
     pq, pt, pl, pst, po, pw = _kv4(cache, ("q", q), ("table", table), ("lens", lens), ("starts", starts),
                                    ("out", out), ("workspace", workspace))
     _check(lib.hr_kv4_attention(cache._ref, pq, _KV4_TYPES[q.dtype], step, total, pst, pt, width, pl, batch,
