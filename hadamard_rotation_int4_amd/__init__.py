@@ -71,7 +71,7 @@ SYMBOLS = {
     "hr_kv4_read": (_i32, [_vp, _vp, _i64, _i32, _vp, _vp, _vp]),
     "hr_kv4_attention": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i64, _f32,
                                 _i32, _i32, _vp, _vp, _i64, _vp]),
-    "hr_kv4_attention_workspace": (_i64, [_i32, _i32, _i64, _i32, _i32, _i32, _i64, _i32]),
+    "hr_kv4_attention_workspace": (_i64, [_i32, _i32, _i32, _i64, _i32, _i32, _i32, _i64, _i32]),
 }
 
 
@@ -801,7 +801,8 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     if scale is None:
         scale = cache.dim ** -0.5
     _arg(out, "out", q.dtype, (total, q_heads, cache.dim))
-    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, total, batch, q_heads, max_new, max_len, window)
+    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, _KV4_TYPES[q.dtype], total, batch, q_heads,
+                                          max_new, max_len, window)
     if workspace is not None:
         _kv4_index(workspace, "workspace", torch.uint8, (-1,))
         if workspace.shape[0] < need:

@@ -649,13 +649,14 @@ static int64_t kv4_workspace(const hr::Kv4AttnArgs& a) {
   return a.nsplit > 1 ? a.total * a.q_heads * a.nsplit * (4 * (int64_t)a.c.dim + 8) : 0;
 }
 
-int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int64_t total, int32_t batch, int32_t q_heads,
-                                   int32_t max_new, int64_t max_len, int32_t window) {
+int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, int64_t total, int32_t batch,
+                                   int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window) {
   if (heads < 1 || dim < 1 || total < 1 || batch < 1 || q_heads < heads || max_new < 1 || max_len < 0 || window < 0)
     return 0;
   hr::Kv4AttnArgs a{};
   a.c.heads = heads;
   a.c.dim = dim;
+  a.dtype = dtype;
   a.total = total;
   a.batch = batch;
   a.q_heads = q_heads;

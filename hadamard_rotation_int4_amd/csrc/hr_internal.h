@@ -125,6 +125,9 @@ constexpr int kDtF32 = 0, kDtBf16 = 1, kDtF16 = 2;
 // Largest cached length: token indices of a sequence stay in 32 bits.
 constexpr int kKv4MaxLen = 1 << 30;
 
+// Query rows of a workgroup of the prompt kernel.
+constexpr int kPromptRows = 128;
+
 // A 4-bit key/value cache after host validation (layout: kv4_device.h).
 struct Kv4Cache {
   uint8_t* codes[2];     // keys, values
@@ -173,14 +176,16 @@ struct Kv4AttnArgs {
   float2* part_ml;       // [total * q_heads][nsplit] (running max in log2 units, sum)
   int nsplit;            // parts of the token axis (kv4_attention_plan)
   int chunk;             // tokens of a part
-  int tiles;             // 16-row tiles of a (sequence, head)
+  int tiles;             // row tiles of a (sequence, key/value head)
+  int prompt;            // 1: tiles of kPromptRows rows (kv4_prompt.hip), 0: of 16
 };
 
 hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s);
 hipError_t launch_kv4_read(const Kv4ReadArgs& a, hipStream_t s);
-// Fills nsplit, chunk and tiles from the sizes.
+// Fills prompt, nsplit, chunk and tiles from the sizes and types.
 void kv4_attention_plan(Kv4AttnArgs* a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t s);
+void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s);   // its part when a.prompt
 
 hipError_t launch_harp_blocks(const HarpSchedule& sc, const float* theta, const float* fallbacks,
                               float* blocks, hipStream_t s);

@@ -28,11 +28,6 @@ namespace hr {
 constexpr int kKv4Threads = 256;
 constexpr int kKv4Waves = kKv4Threads / 64;
 
-template <int D>
-constexpr float kv4_norm() {
-  return D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
-}
-
 // Group absmax over the group's lanes (non-negative floats and NaN compare as
 // integers, NaN above all).
 __device__ __forceinline__ uint32_t group_max(uint32_t a, int group) {

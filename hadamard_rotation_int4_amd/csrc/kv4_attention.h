@@ -1,0 +1,110 @@
+// What the kernels of attention over the 4-bit key/value cache share: which
+// tokens a query row sees, matrix instructions, codes to fp16, the last steps
+// of an output row.
+#pragma once
+
+#include "kv4_device.h"
+
+namespace hr {
+
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kMaxSlack = 8.0f;    // log2 units the scores may pass the running maximum by
+
+// The query rows of one sequence, and the tokens they see.  Row and token
+// indices fit 32 bits (the host checks); offsets into the cache do not.
+struct Kv4Seq {
+  int len, s0, news, rows;
+  int window, causal;
+
+  __device__ __forceinline__ Kv4Seq(const Kv4AttnArgs& p, int b) : window(p.window), causal(p.causal) {
+    const int64_t cap = p.width << p.c.page_log2;
+    const int cap32 = cap < kKv4MaxLen ? (int)cap : kKv4MaxLen;
+    len = p.lens[b];
+    len = len < 0 ? 0 : len > cap32 ? cap32 : len;
+    s0 = b * p.max_new;
+    int s1 = s0 + p.max_new;
+    if (p.starts) {
+      s0 = p.starts[b];
+      s1 = p.starts[b + 1];
+    }
+    if (s0 < 0) s0 = 0;
+    if (s1 > (int)p.total) s1 = (int)p.total;
+    news = s1 - s0;
+    rows = news * p.rep;
+  }
+  // new token n sees tokens [lo(n), hi(n)); both grow with n
+  __device__ __forceinline__ int lo(int n) const {
+    const int v = len - news + n - window + 1;
+    return window > 0 && v > 0 ? v : 0;
+  }
+  __device__ __forceinline__ int hi(int n) const {
+    const int v = len - news + n + 1;
+    return !causal || v > len ? len : v < 0 ? 0 : v;
+  }
+};
+
+__device__ __forceinline__ f32x4 mma(half8v a, half8v b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(bf16x8v a, bf16x8v b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// nibbles 0 and 4 (low half, high half) of x as codes in fp16; x's nibbles are two's complement
+__device__ __forceinline__ half2v codes_lo(uint32_t x) {
+  const half2v h = __builtin_bit_cast(half2v, (x & 0x000F000Fu) ^ 0x64086408u);     // 1024 + 8 + q
+  return h - (half2v){(_Float16)1032.0f, (_Float16)1032.0f};
+}
+// nibbles 1 and 5
+__device__ __forceinline__ half2v codes_hi(uint32_t x) {
+  const half2v h = __builtin_bit_cast(half2v, (x & 0x00F000F0u) ^ 0x64806480u);     // 1024 + 16 (8 + q)
+  const half2v s = {(_Float16)0.0625f, (_Float16)0.0625f}, o = {(_Float16)-72.0f, (_Float16)-72.0f};
+  return __builtin_elementwise_fma(h, s, o);
+}
+
+// eight codes of a dword in the order nibble 0, 4, 1, 5, 2, 6, 3, 7
+__device__ __forceinline__ void codes8(uint32_t x, half2v* h) {
+  h[0] = codes_lo(x);
+  h[1] = codes_hi(x);
+  h[2] = codes_lo(x >> 8);
+  h[3] = codes_hi(x >> 8);
+}
+__device__ constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
+
+// byte b (0..3) of x0 and of x1 as two pairs of codes: its low nibbles, its
+// high nibbles
+__device__ __forceinline__ void codes_of_two(uint32_t x0, uint32_t x1, int b, half2v& lo, half2v& hi) {
+  const uint32_t t = __builtin_amdgcn_perm(x1, x0, 0x0c000c00u | (uint32_t)b | ((uint32_t)(4 + b) << 16));
+  lo = codes_lo(t);
+  hi = codes_hi(t);
+}
+
+__device__ __forceinline__ half8v join8(const half2v* h) {
+  return (half8v){h[0][0], h[0][1], h[1][0], h[1][1], h[2][0], h[2][1], h[3][0], h[3][1]};
+}
+
+// Power of two that brings a row's absmax to [1, 2), as an exponent; 0 for a
+// row of zeros or one that is not finite.
+__device__ __forceinline__ int row_exponent(float mx) {
+  return mx > 0.0f && mx < __builtin_inff() ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+}
+
+// An output row's last steps, 16 lanes a row with dims [a D/16, (a + 1) D/16):
+// divide by the softmax sum (0 where nothing was seen), rotate back.
+template <int D>
+__device__ __forceinline__ void finish_row(const Kv4Cache& c, float l, int a, float* w) {
+  constexpr int NC = D / 16;
+  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+  for (int e = 0; e < NC; ++e) w[e] *= inv;
+  if (c.rotate) {
+    fwht_lanes<NC, 16>(w, a);
+    const float nf = kv4_norm<D>() * kv4_tau(a);
+    uint32_t sg[NC];
+    load_signs<NC>(c.signs, a * NC, sg);
+#pragma unroll
+    for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * nf, sg[e]);
+  }
+}
+
+}  // namespace hr

@@ -41,24 +41,21 @@
 // products above 2^-24 of the whole kept.
 //
 // Rows of parts are joined by kv4_join_kernel, in the order of the parts.
-#include "kv4_device.h"
+#include "kv4_attention.h"
 
 namespace hr {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxSlack = 8.0f;    // log2 units the scores may pass the running maximum by
 
 // modes: one group a head / several, 16-bit queries; fp32 queries
 enum { kOneGroup = 0, kGroups = 1, kF32 = 2 };
 
-__device__ __forceinline__ f32x4 mma(half8v a, half8v b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
-}
-__device__ __forceinline__ f32x4 mma(bf16x8v a, bf16x8v b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
+// Waves a SIMD the registers are kept for.  At two or more the compiler takes
+// at most 256 registers and leaves the accumulators among the ordinary ones
+// (with more it moves them to and from the accumulation registers, 112 moves a
+// tile).
+constexpr int kv4_attn_waves(int dim, int mode) { return dim == 256 ? (mode == kF32 ? 1 : 2) : mode == kF32 ? 2 : 3; }
 
 // max over the four lanes that hold the same query row (lanes i + 16 g)
 __device__ __forceinline__ float max_over_g(float v) {
@@ -66,31 +63,6 @@ __device__ __forceinline__ float max_over_g(float v) {
   v = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
   s = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
   return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
-}
-
-// nibbles 0 and 4 (low half, high half) of x as codes in fp16; x's nibbles are two's complement
-__device__ __forceinline__ half2v codes_lo(uint32_t x) {
-  const half2v h = __builtin_bit_cast(half2v, (x & 0x000F000Fu) ^ 0x64086408u);     // 1024 + 8 + q
-  return h - (half2v){(_Float16)1032.0f, (_Float16)1032.0f};
-}
-// nibbles 1 and 5
-__device__ __forceinline__ half2v codes_hi(uint32_t x) {
-  const half2v h = __builtin_bit_cast(half2v, (x & 0x00F000F0u) ^ 0x64806480u);     // 1024 + 16 (8 + q)
-  const half2v s = {(_Float16)0.0625f, (_Float16)0.0625f}, o = {(_Float16)-72.0f, (_Float16)-72.0f};
-  return __builtin_elementwise_fma(h, s, o);
-}
-
-// eight codes of a dword in the order nibble 0, 4, 1, 5, 2, 6, 3, 7
-__device__ __forceinline__ void codes8(uint32_t x, half2v* h) {
-  h[0] = codes_lo(x);
-  h[1] = codes_hi(x);
-  h[2] = codes_lo(x >> 8);
-  h[3] = codes_hi(x >> 8);
-}
-__device__ constexpr int kOrder[8] = {0, 4, 1, 5, 2, 6, 3, 7};
-
-__device__ __forceinline__ half8v join8(const half2v* h) {
-  return (half8v){h[0][0], h[0][1], h[1][0], h[1][1], h[2][0], h[2][1], h[3][0], h[3][1]};
 }
 
 // x as a sum of bf16 terms
@@ -171,18 +143,8 @@ __device__ __forceinline__ void load_tile(const Kv4Cache& c, const int32_t* tabl
   }
 }
 
-// value pairs of tokens 2 j, 2 j + 1 (of the lane's eight) at dims 2 b, 2 b + 1
-// of the lane, unscaled
 template <int D, int MODE>
-__device__ __forceinline__ void value_pair(const Tile<D, MODE>& x, int b, int j, half2v& lo, half2v& hi) {
-  const uint32_t sel = 0x0c000c00u | (uint32_t)(b & 3) | ((uint32_t)(4 + (b & 3)) << 16);
-  const uint32_t t = __builtin_amdgcn_perm(x.v[2 * j + 1][b >> 2], x.v[2 * j][b >> 2], sel);
-  lo = codes_lo(t);
-  hi = codes_hi(t);
-}
-
-template <int D, int MODE>
-__global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
+__global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE)) void kv4_attn_kernel(Kv4AttnArgs p) {
   constexpr int NK = D / 32;             // matrix instructions over the dims
   constexpr int NC = D / 16;             // 16-dim slices of the output
   constexpr int LD = D + 4;              // row pitch of the exchange
@@ -196,39 +158,19 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
   const int rest = blockIdx.x / p.c.heads;
   const int tile = rest % p.tiles, part = rest / p.tiles;
 
-  // row and token indices fit 32 bits (the host checks); offsets into the cache do not
-  const int64_t cap = p.width << p.c.page_log2;
-  const int cap32 = cap < kKv4MaxLen ? (int)cap : kKv4MaxLen;
-  int len = p.lens[b];
-  len = len < 0 ? 0 : len > cap32 ? cap32 : len;
-  int s0 = b * p.max_new, s1 = s0 + p.max_new;
-  if (p.starts) {
-    s0 = p.starts[b];
-    s1 = p.starts[b + 1];
-  }
-  if (s0 < 0) s0 = 0;
-  if (s1 > (int)p.total) s1 = (int)p.total;
-  const int news = s1 - s0, rows = news * p.rep;
+  const Kv4Seq q(p, b);
   const int row0 = tile * 16;
-  if (row0 >= rows) return;
+  if (row0 >= q.rows) return;
   // what the tile's first and last row see, and this lane's row
-  auto seen_lo = [&](int n) {
-    const int lo = len - news + n - p.window + 1;
-    return p.window > 0 && lo > 0 ? lo : 0;
-  };
-  auto seen_hi = [&](int n) {
-    const int hi = len - news + n + 1;
-    return !p.causal || hi > len ? len : hi < 0 ? 0 : hi;
-  };
   const int n_first = row0 / p.rep;
-  const int n_last = (row0 + 15 < rows ? row0 + 15 : rows - 1) / p.rep;
-  const int lo = seen_lo(n_first), hi = seen_hi(n_last);
-  const int all_lo = seen_lo(n_last), all_hi = seen_hi(n_first);   // [all_lo, all_hi): seen by every row
+  const int n_last = (row0 + 15 < q.rows ? row0 + 15 : q.rows - 1) / p.rep;
+  const int lo = q.lo(n_first), hi = q.hi(n_last);
+  const int all_lo = q.lo(n_last), all_hi = q.hi(n_first);   // [all_lo, all_hi): seen by every row
   const int row = row0 + i;
-  const bool valid = row < rows;
+  const bool valid = row < q.rows;
   const int n_mine = valid ? row / p.rep : n_last;
-  const int my_lo = seen_lo(n_mine), my_hi = seen_hi(n_mine);
-  const int q_row = s0 + n_mine;
+  const int my_lo = q.lo(n_mine), my_hi = q.hi(n_mine);
+  const int q_row = q.s0 + n_mine;
   const int q_head = head * p.rep + (valid ? row - n_mine * p.rep : 0);
   // this part of the token axis; the last part takes what is left
   const int from = (lo & ~31) + part * p.chunk;
@@ -256,13 +198,12 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
       }
       fwht_regs<E>(w);
       const float b0 = (g & 1) ? -1.0f : 1.0f, b1 = (g & 2) ? -1.0f : 1.0f;
-      const float norm = D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
 #pragma unroll
       for (int e = 0; e < E; ++e) {
         auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
         const float u = fmaf(__uint_as_float(s[1]), b0, __uint_as_float(s[0]));
         s = __builtin_amdgcn_permlane32_swap(__float_as_uint(u), __float_as_uint(u), false, false);
-        w[e] = fmaf(__uint_as_float(s[1]), b1, __uint_as_float(s[0])) * norm;
+        w[e] = fmaf(__uint_as_float(s[1]), b1, __uint_as_float(s[0])) * kv4_norm<D>();
       }
     }
     if (MODE == kF32) {
@@ -280,7 +221,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
 #pragma unroll
       for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(w[e]));
       mx = max_over_g(mx);
-      const int ex = mx > 0.0f && mx < __builtin_inff() ? __builtin_amdgcn_frexp_expf(mx) - 1 : 0;
+      const int ex = row_exponent(mx);
       qf = ldexpf(qf, ex);
 #pragma unroll
       for (int c = 0; c < NK; ++c)
@@ -387,7 +328,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
-          value_pair<D, MODE>(x, bb, j, vl[j], vh[j]);
+          codes_of_two(x.v[2 * j][bb >> 2], x.v[2 * j + 1][bb >> 2], bb & 3, vl[j], vh[j]);
           vl[j] = vl[j] * sc;
           vh[j] = vh[j] * sc;
         }
@@ -411,7 +352,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           half2v vv[2];
-          value_pair<D, MODE>(x, bb, j, vv[0], vv[1]);
+          codes_of_two(x.v[2 * j][bb >> 2], x.v[2 * j + 1][bb >> 2], bb & 3, vv[0], vv[1]);
 #pragma unroll
           for (int d = 0; d < 2; ++d)
 #pragma unroll
@@ -469,9 +410,9 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
     }
   }
   const int r2 = row0 + orow;
-  const bool store = r2 < rows;
+  const bool store = r2 < q.rows;
   const int n2 = store ? r2 / p.rep : 0;
-  const int64_t out_row = (int64_t)(s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
+  const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
   if (p.nsplit > 1) {
     if (store) {
       const int64_t at = out_row * p.nsplit + part;
@@ -480,17 +421,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_attn_kernel(Kv4AttnArgs p) {
     }
     return;
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int e = 0; e < NC; ++e) w[e] *= inv;
-  if (p.c.rotate) {
-    fwht_lanes<NC, 16>(w, la);
-    const float nf = (D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f) * kv4_tau(la);
-    uint32_t sg[NC];
-    load_signs<NC>(p.c.signs, la * NC, sg);
-#pragma unroll
-    for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * nf, sg[e]);
-  }
+  finish_row<D>(p.c, l, la, w);
   if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
 }
 
@@ -506,16 +437,13 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
   const int la = kv4_logical<16>(lane);
   const int b = blockIdx.y;
   const int n = blockIdx.x / p.q_heads;
-  int s0 = b * p.max_new, s1 = s0 + p.max_new;
-  if (p.starts) {
-    s0 = p.starts[b] < 0 ? 0 : p.starts[b];
-    s1 = p.starts[b + 1];
-  }
-  if (n >= s1 - s0 || s0 + n >= (int)p.total) return;
-  const int64_t out_row = (int64_t)(s0 + n) * p.q_heads + (blockIdx.x - n * p.q_heads);
+  const Kv4Seq q(p, b);
+  if (n >= q.news) return;
+  const int64_t out_row = (int64_t)(q.s0 + n) * p.q_heads + (blockIdx.x - n * p.q_heads);
   const float2* ml = p.part_ml + out_row * p.nsplit;
   float top = -__builtin_inff();
-  for (int s = 0; s < p.nsplit; ++s) top = fmaxf(top, ml[s].x);
+  for (int s = lane; s < p.nsplit; s += 64) top = fmaxf(top, ml[s].x);
+  top = wave_max(top);
   float w[NC], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < NC; ++e) w[e] = 0.0f;
@@ -540,34 +468,28 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
 #pragma unroll
     for (int e = 0; e < NC; ++e) w[e] += o_lds[s][la * NC + e];
   }
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int e = 0; e < NC; ++e) w[e] *= inv;
-  if (p.c.rotate) {
-    fwht_lanes<NC, 16>(w, la);
-    const float nf = (D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f) * kv4_tau(la);
-    uint32_t sg[NC];
-    load_signs<NC>(p.c.signs, la * NC, sg);
-#pragma unroll
-    for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * nf, sg[e]);
-  }
+  finish_row<D>(p.c, l, la, w);
   if (grp == 0) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
 }
 
-// Parts of the token axis: enough workgroups for four a CU, none shorter than
-// 256 tokens (two tiles a wave).
+// Which kernel, and into how many parts of the token axis: enough workgroups to
+// fill the chip (three a CU of 16 rows, two of 128), none with fewer than 256
+// tokens (two tiles a wave) or, of 128 rows, 512.
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
-  a->tiles = (int)((rows + 15) / 16);
+  a->prompt = a->dtype != kDtF32 && rows > 32;
+  const int64_t rows_of = a->prompt ? kPromptRows : 16, least = a->prompt ? 512 : 256;
+  const int64_t want = a->prompt ? 512 : 768;
+  a->tiles = (int)((rows + rows_of - 1) / rows_of);
   int64_t span = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
   const int64_t groups = (int64_t)a->batch * a->c.heads * a->tiles;
-  int64_t n = groups > 0 ? (1024 + groups - 1) / groups : 1;
-  const int64_t most = (span + 255) / 256;
+  int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
+  const int64_t most = (span + least - 1) / least;
   if (n > most) n = most;
   if (n < 1) n = 1;
   int64_t chunk = ((span + n - 1) / n + 127) / 128 * 128;
-  if (chunk < 256) chunk = 256;
+  if (chunk < least) chunk = least;
   n = (span + chunk - 1) / chunk;
   a->nsplit = (int)(n < 1 ? 1 : n);
   a->chunk = (int)chunk;
@@ -576,7 +498,8 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
 template <int D>
 static void attn1(const Kv4AttnArgs& a, hipStream_t s) {
   const dim3 g((unsigned)((int64_t)a.c.heads * a.tiles * a.nsplit), a.batch), b(kAttnThreads);
-  if (a.dtype == kDtF32) hipLaunchKernelGGL((kv4_attn_kernel<D, kF32>), g, b, 0, s, a);
+  if (a.prompt) launch_kv4_prompt(a, s);
+  else if (a.dtype == kDtF32) hipLaunchKernelGGL((kv4_attn_kernel<D, kF32>), g, b, 0, s, a);
   else if (a.c.group == D) hipLaunchKernelGGL((kv4_attn_kernel<D, kOneGroup>), g, b, 0, s, a);
   else hipLaunchKernelGGL((kv4_attn_kernel<D, kGroups>), g, b, 0, s, a);
   if (a.nsplit > 1)

@@ -32,6 +32,12 @@ typedef __bf16 bf16x8v __attribute__((ext_vector_type(8)));
 
 constexpr int kRowRor8 = 0x128;
 
+// 1 / sqrt(D)
+template <int D>
+__device__ __forceinline__ constexpr float kv4_norm() {
+  return D == 64 ? 0.125f : D == 128 ? 0.08838834764831845f : 0.0625f;
+}
+
 // Logical index of this lane among the L lanes of its vector (L = 8, 16, 32).
 template <int L>
 __device__ __forceinline__ int kv4_logical(int lane) {

@@ -581,8 +581,8 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
 
 /* Bytes of workspace of an hr_kv4_attention call of these sizes (0: none;
  * negative sizes give 0). */
-int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int64_t total, int32_t batch, int32_t q_heads,
-                                   int32_t max_new, int64_t max_len, int32_t window);
+int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, int64_t total, int32_t batch,
+                                   int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window);
 
 #ifdef __cplusplus
 }

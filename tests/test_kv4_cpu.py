@@ -137,11 +137,11 @@ def test_attention_refusals(kw, status):
 
 def test_workspace_sizes():
     f = hr.lib.hr_kv4_attention_workspace
-    assert f(8, 128, 1, 1, 32, 1, 200, 0) == 0
-    big = f(8, 128, 1, 1, 32, 1, 131072, 0)
+    assert f(8, 128, hr.HR_BF16, 1, 1, 32, 1, 200, 0) == 0
+    big = f(8, 128, hr.HR_BF16, 1, 1, 32, 1, 131072, 0)
     assert big > 0 and big % (32 * (128 * 4 + 8)) == 0
-    assert f(8, 128, 1, 1, 32, 1, 131072, 100) < big          # a window leaves little to split
-    for bad in ((0, 128, 1, 1, 32, 1, 9, 0), (8, 128, -1, 1, 32, 1, 9, 0), (8, 128, 1, 1, 4, 1, 9, 0)):
+    assert f(8, 128, hr.HR_BF16, 1, 1, 32, 1, 131072, 100) < big          # a window leaves little to split
+    for bad in ((0, 128, 1, 1, 1, 32, 1, 9, 0), (8, 128, 1, -1, 1, 32, 1, 9, 0), (8, 128, 1, 1, 1, 4, 1, 9, 0)):
         assert f(*bad) == 0
 
 
