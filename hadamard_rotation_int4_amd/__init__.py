@@ -670,6 +670,7 @@ class KV4Cache:
         self.device = k_codes.device
         self._struct = _CacheStruct(*_ptrs(*args), pages, heads, dim, page, self.group, int(self.rotate))
         self._ref = ctypes.addressof(self._struct)
+        self._index = self.device.index
 
 
 def kv4_cache(pages: int, heads: int, dim: int, page: int = 64, group: int | None = None, rotate: bool = True,
@@ -682,59 +683,64 @@ def kv4_cache(pages: int, heads: int, dim: int, page: int = 64, group: int | Non
 
 
 _KV4_TYPES = {torch.bfloat16: HR_BF16, torch.float16: HR_F16, torch.float32: HR_F32}
+_KV4_BYTES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4}
+
+# A decode step makes a few of these calls for every layer, and with few tokens
+# the host's part of a call is what it costs: the checks below read each
+# property once, and the stream is read without building a Stream object
+# (0.1 against 1.8 us) where torch offers that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _kv4(cache, *named):
-    """Device and pointers of (name, tensor) pairs that a call on `cache` takes (None -> NULL)."""
-    dev = cache.device
-    out = []
-    for name, t in named:
-        if t is None:
-            out.append(None)
-            continue
+def _kv4_stream(cache) -> int:
+    return _raw_stream(cache._index) if _raw_stream is not None else _stream(cache.device)
+
+
+def _kv4_ptr(cache, t, name: str) -> int:
+    """Device pointer of a tensor that a call on `cache` takes."""
+    if t.device != cache.device:
         if not t.is_cuda:
             raise ValueError(f"{name}: tensor must live on the GPU")
-        if t.device != dev:
-            raise ValueError(f"{name}: on {t.device}, expected {dev}")
-        out.append(t.data_ptr())
-    return out
+        raise ValueError(f"{name}: on {t.device}, expected {cache.device}")
+    return t.data_ptr()
 
 
-def _kv4_rows(cache, t, name: str, heads: int | None, dtype=None):
+def _kv4_rows(cache, t, name: str):
     """Check token rows [tokens][heads][dim] whose tokens may be strided (slices
-    of a fused projection); returns (tokens, heads, row stride)."""
+    of a fused projection); returns (tokens, heads, row stride, dtype)."""
     if not isinstance(cache, KV4Cache):
         raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype not in _KV4_TYPES or (dtype is not None and t.dtype != dtype):
-        raise TypeError(f"{name}: dtype {t.dtype} not in "
-                        f"{[_DT_NAME[d] for d in (_KV4_TYPES if dtype is None else (dtype,))]}")
+    dtype = t.dtype
+    if dtype not in _KV4_TYPES:
+        raise TypeError(f"{name}: dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
     shape = t.shape
-    if len(shape) != 3 or shape[2] != cache.dim or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name}: shape {tuple(shape)}, expected [tokens][{'heads' if heads is None else heads}]"
-                         f"[{cache.dim}]")
-    stride = t.stride()
-    row = shape[1] * cache.dim
-    if shape[0] and (stride[2] != 1 or (stride[1] != cache.dim and shape[1] != 1)):
+    if len(shape) != 3 or shape[2] != cache.dim:
+        raise ValueError(f"{name}: shape {tuple(shape)}, expected [tokens][heads][{cache.dim}]")
+    tokens, heads, dim = shape
+    step, head_step, last = t.stride()
+    if tokens and (last != 1 or (head_step != dim and heads != 1)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    step = stride[0] if shape[0] > 1 else row
-    if step < row or step * t.element_size() % 16:
+    row = heads * dim
+    if tokens < 2:
+        step = row
+    if step < row or step * _KV4_BYTES[dtype] & 15:
         raise ValueError(f"{name}: tokens {step} elements apart; they must not overlap and be a multiple of 16 bytes apart")
-    return shape[0], shape[1], step
+    return tokens, heads, step, dtype
 
 
 def _kv4_index(t, name: str, dtype, shape):
-    """Check an index tensor: dtype, shape (an int is any size where negative), contiguous."""
+    """Check an index tensor: dtype, shape (any size where negative), contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     if t.dtype != dtype:
         raise TypeError(f"{name}: dtype {t.dtype} not in {[_DT_NAME[dtype]]}")
-    if t.dim() != len(shape) or any(w >= 0 and v != w for v, w in zip(t.shape, shape)):
-        raise ValueError(f"{name}: shape {tuple(t.shape)}, expected {tuple('any' if w < 0 else w for w in shape)}")
+    got = t.shape
+    if got != shape and (len(got) != len(shape) or any(w >= 0 and v != w for v, w in zip(got, shape))):
+        raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple('any' if w < 0 else w for w in shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
-    return t
 
 
 def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.Tensor) -> None:
@@ -742,14 +748,19 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     [heads][dim] bf16, fp16 or fp32, of one dtype, tokens may be strided; slots:
     int64 [tokens], page * cache.page + place, all different, a slot outside the
     cache writes nothing."""
-    tokens, _, ks = _kv4_rows(cache, k, "k", getattr(cache, "heads", None))
-    vt, _, vs = _kv4_rows(cache, v, "v", cache.heads, k.dtype)
+    tokens, heads, ks, dtype = _kv4_rows(cache, k, "k")
+    vt, vh, vs, vdtype = _kv4_rows(cache, v, "v")
+    if heads != cache.heads or vh != heads:
+        raise ValueError(f"k, v: {heads} and {vh} heads, but the cache has {cache.heads}")
+    if vdtype != dtype:
+        raise TypeError(f"v: dtype {vdtype} not in {[_DT_NAME[dtype]]}")
     if vt != tokens:
         raise ValueError(f"v: {vt} tokens, but k has {tokens}")
     _kv4_index(slots, "slots", torch.int64, (tokens,))
-    pk, pv, psl = _kv4(cache, ("k", k), ("v", v), ("slots", slots))
-    _check(lib.hr_kv4_append(cache._ref, pk, pv, _KV4_TYPES[k.dtype], ks, vs, psl, tokens, _stream(cache.device)),
-           "hr_kv4_append")
+    st = lib.hr_kv4_append(cache._ref, _kv4_ptr(cache, k, "k"), _kv4_ptr(cache, v, "v"), _KV4_TYPES[dtype], ks, vs,
+                           _kv4_ptr(cache, slots, "slots"), tokens, _kv4_stream(cache))
+    if st:
+        raise HRError(st, "hr_kv4_append")
 
 
 def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype=torch.bfloat16, k: torch.Tensor | None = None,
@@ -762,15 +773,18 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype=torch.bfloat16, k: torc
     if dtype not in _KV4_TYPES:
         raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
     shape = (slots.shape[0], cache.heads, cache.dim)
-    _arg(k, "k", dtype, shape)
-    _arg(v, "v", dtype, shape)
     if k is None:
         k = torch.empty(shape, dtype=dtype, device=cache.device)
+    else:
+        _arg(k, "k", dtype, shape)
     if v is None:
         v = torch.empty(shape, dtype=dtype, device=cache.device)
-    psl, pk, pv = _kv4(cache, ("slots", slots), ("k", k), ("v", v))
-    _check(lib.hr_kv4_read(cache._ref, psl, shape[0], _KV4_TYPES[dtype], pk, pv, _stream(cache.device)),
-           "hr_kv4_read")
+    else:
+        _arg(v, "v", dtype, shape)
+    st = lib.hr_kv4_read(cache._ref, _kv4_ptr(cache, slots, "slots"), shape[0], _KV4_TYPES[dtype],
+                         _kv4_ptr(cache, k, "k"), _kv4_ptr(cache, v, "v"), _kv4_stream(cache))
+    if st:
+        raise HRError(st, "hr_kv4_read")
     return k, v
 
 
@@ -788,7 +802,7 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     kept by a caller that captures the call in a graph; allocated when None.
     Returns out [total][q_heads][dim] of q's dtype, 0 in a row that sees no
     token."""
-    total, q_heads, step = _kv4_rows(cache, q, "q", None)
+    total, q_heads, step, dtype = _kv4_rows(cache, q, "q")
     _kv4_index(table, "table", torch.int32, (-1, -1))
     batch, width = table.shape
     _kv4_index(lens, "lens", torch.int32, (batch,))
@@ -800,21 +814,24 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
         max_len = min(width * cache.page, 1 << 30)
     if scale is None:
         scale = cache.dim ** -0.5
-    _arg(out, "out", q.dtype, (total, q_heads, cache.dim))
-    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, _KV4_TYPES[q.dtype], total, batch, q_heads,
-                                          max_new, max_len, window)
+    code = _KV4_TYPES[dtype]
+    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, code, total, batch, q_heads, max_new, max_len, window)
+    if out is not None:
+        _arg(out, "out", dtype, (total, q_heads, cache.dim))
     if workspace is not None:
         _kv4_index(workspace, "workspace", torch.uint8, (-1,))
         if workspace.shape[0] < need:
             raise ValueError(f"workspace: {workspace.shape[0]} bytes, {need} needed")
-    elif need:
-        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     if out is None:
-        out = torch.empty((total, q_heads, cache.dim), dtype=q.dtype, device=cache.device)
-    pq, pt, pl, pst, po, pw = _kv4(cache, ("q", q), ("table", table), ("lens", lens), ("starts", starts),
-                                   ("out", out), ("workspace", workspace))
-    _check(lib.hr_kv4_attention(cache._ref, pq, _KV4_TYPES[q.dtype], step, total, pst, pt, width, pl, batch,
-                                q_heads, max_new, max_len, scale, int(causal), window, po, pw,
-                                0 if workspace is None else workspace.shape[0], _stream(cache.device)),
-           "hr_kv4_attention")
+        out = torch.empty((total, q_heads, cache.dim), dtype=dtype, device=cache.device)
+    if workspace is None and need:
+        workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
+    st = lib.hr_kv4_attention(
+        cache._ref, _kv4_ptr(cache, q, "q"), code, step, total,
+        None if starts is None else _kv4_ptr(cache, starts, "starts"), _kv4_ptr(cache, table, "table"), width,
+        _kv4_ptr(cache, lens, "lens"), batch, q_heads, max_new, max_len, scale, 1 if causal else 0, window,
+        _kv4_ptr(cache, out, "out"), None if workspace is None else _kv4_ptr(cache, workspace, "workspace"),
+        0 if workspace is None else workspace.shape[0], _kv4_stream(cache))
+    if st:
+        raise HRError(st, "hr_kv4_attention")
     return out

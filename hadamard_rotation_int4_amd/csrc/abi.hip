@@ -718,7 +718,7 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
   a.window = window;
   a.out = out;
   hr::kv4_attention_plan(&a);
-  if ((int64_t)cache->heads * a.tiles * a.nsplit > INT32_MAX)
+  if (a.groups > INT32_MAX / 2)
     return fail(HR_EUNSUPPORTED, "%s: too many rows for one launch", fn);
   const int64_t need = kv4_workspace(a);
   if (need > 0) {

@@ -172,20 +172,21 @@ struct Kv4AttnArgs {
   float scale;
   int causal, window;
   void* out;             // [total][q_heads][dim]
-  float* part_o;         // [total * q_heads][nsplit][dim], null when nsplit == 1
+  float* part_o;         // [total * q_heads][nsplit][dim] sums, not yet divided; null when nsplit == 1
   float2* part_ml;       // [total * q_heads][nsplit] (running max in log2 units, sum)
-  int nsplit;            // parts of the token axis (kv4_attention_plan)
-  int chunk;             // tokens of a part
+  // by kv4_attention_plan:
+  int rows;              // of a row tile: 16, 32 or kPromptRows (kv4_prompt.hip)
   int tiles;             // row tiles of a (sequence, key/value head)
-  int prompt;            // 1: tiles of kPromptRows rows (kv4_prompt.hip), 0: of 16
+  int nsplit, chunk;     // most parts of the token axis, tokens of a part
+  int64_t groups;        // workgroups
 };
 
 hipError_t launch_kv4_append(const Kv4AppendArgs& a, hipStream_t s);
 hipError_t launch_kv4_read(const Kv4ReadArgs& a, hipStream_t s);
-// Fills prompt, nsplit, chunk and tiles from the sizes and types.
+// Fills its part of the arguments from the sizes and types.
 void kv4_attention_plan(Kv4AttnArgs* a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t s);
-void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s);   // its part when a.prompt
+void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s);   // its part when a.rows == kPromptRows
 
 hipError_t launch_harp_blocks(const HarpSchedule& sc, const float* theta, const float* fallbacks,
                               float* blocks, hipStream_t s);

@@ -12,6 +12,11 @@ constexpr float kMaxSlack = 8.0f;    // log2 units the scores may pass the runni
 
 // The query rows of one sequence, and the tokens they see.  Row and token
 // indices fit 32 bits (the host checks); offsets into the cache do not.
+// Index arrays do not change during a call: read them through the scalar cache.
+__device__ __forceinline__ int read_index(const int32_t* p, int64_t i) {
+  return ((const __attribute__((address_space(4))) int32_t*)(uintptr_t)p)[i];
+}
+
 struct Kv4Seq {
   int len, s0, news, rows;
   int window, causal;
@@ -19,13 +24,13 @@ struct Kv4Seq {
   __device__ __forceinline__ Kv4Seq(const Kv4AttnArgs& p, int b) : window(p.window), causal(p.causal) {
     const int64_t cap = p.width << p.c.page_log2;
     const int cap32 = cap < kKv4MaxLen ? (int)cap : kKv4MaxLen;
-    len = p.lens[b];
+    len = read_index(p.lens, b);
     len = len < 0 ? 0 : len > cap32 ? cap32 : len;
     s0 = b * p.max_new;
     int s1 = s0 + p.max_new;
     if (p.starts) {
-      s0 = p.starts[b];
-      s1 = p.starts[b + 1];
+      s0 = read_index(p.starts, b);
+      s1 = read_index(p.starts, b + 1);
     }
     if (s0 < 0) s0 = 0;
     if (s1 > (int)p.total) s1 = (int)p.total;
@@ -42,6 +47,14 @@ struct Kv4Seq {
     return !causal || v > len ? len : v < 0 ? 0 : v;
   }
 };
+
+// The token axis in parts: those of a row tile start at its first visible token
+// rounded down to 32, `chunk` tokens each, as many as it takes.
+__device__ __forceinline__ int kv4_part_base(int lo) { return lo & ~31; }
+__device__ __forceinline__ int kv4_part_count(int lo, int hi, int chunk) {
+  const int n = hi - kv4_part_base(lo);
+  return n <= 0 ? 1 : (n + chunk - 1) / chunk;
+}
 
 __device__ __forceinline__ f32x4 mma(half8v a, half8v b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
@@ -92,16 +105,16 @@ __device__ __forceinline__ int row_exponent(float mx) {
 // An output row's last steps, 16 lanes a row with dims [a D/16, (a + 1) D/16):
 // divide by the softmax sum (0 where nothing was seen), rotate back.
 template <int D>
-__device__ __forceinline__ void finish_row(const Kv4Cache& c, float l, int a, float* w) {
+__device__ __forceinline__ void finish_row(int rotate, const int8_t* signs, float l, int a, float* w) {
   constexpr int NC = D / 16;
   const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
   for (int e = 0; e < NC; ++e) w[e] *= inv;
-  if (c.rotate) {
+  if (rotate) {
     fwht_lanes<NC, 16>(w, a);
     const float nf = kv4_norm<D>() * kv4_tau(a);
     uint32_t sg[NC];
-    load_signs<NC>(c.signs, a * NC, sg);
+    load_signs<NC>(signs, a * NC, sg);
 #pragma unroll
     for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * nf, sg[e]);
   }

@@ -47,6 +47,7 @@ namespace hr {
 
 constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
+constexpr int kFewParts = 8;
 
 // modes: one group a head / several, 16-bit queries; fp32 queries
 enum { kOneGroup = 0, kGroups = 1, kF32 = 2 };
@@ -55,7 +56,11 @@ enum { kOneGroup = 0, kGroups = 1, kF32 = 2 };
 // at most 256 registers and leaves the accumulators among the ordinary ones
 // (with more it moves them to and from the accumulation registers, 112 moves a
 // tile).
-constexpr int kv4_attn_waves(int dim, int mode) { return dim == 256 ? (mode == kF32 ? 1 : 2) : mode == kF32 ? 2 : 3; }
+constexpr int kv4_attn_waves(int dim, int mode, int rows) {
+  return dim == 256 ? (mode == kF32 ? 1 : 2) : mode == kF32 || rows > 16 ? 2 : 3;
+}
+// Smallest exponent of the unit of value scales: its reciprocal is an fp16 number.
+constexpr int kMinScaleExp = -15;
 
 // max over the four lanes that hold the same query row (lanes i + 16 g)
 __device__ __forceinline__ float max_over_g(float v) {
@@ -84,407 +89,614 @@ struct Tile {
   uint32_t k[2][NK];
   uint32_t v[8][(NB + 3) / 4];
   half4v ks4[2];                                          // one group: tokens 4 g + r
-  _Float16 ks1[2][NS];                                    // several: token i, the lane's dims
+  half2v ks1[NS];                                         // several: token i of both blocks, the lane's dims
   half4v vs[2];
 };
 
+// Where the tokens of a tile are, the page ids one tile ahead of the codes.
+struct Ids {
+  int id[2];
+};
+__device__ __forceinline__ Ids load_ids(const Kv4Cache& c, const int32_t* table_row, int t0, int last) {
+  // past the last token, that token's tile instead (it is masked)
+  const int j = t0 > last ? last & ~31 : t0;
+  const int j1 = j + 16 > last ? j : j + 16;
+  Ids r;
+  r.id[0] = read_index(table_row, j >> c.page_log2);
+  r.id[1] = c.page_log2 >= 5 ? r.id[0] : read_index(table_row, j1 >> c.page_log2);
+  return r;
+}
+
 template <int D, int MODE>
-__device__ __forceinline__ void load_tile(const Kv4Cache& c, const int32_t* table_row, int head, int t0,
-                                          int last, int g, int i, Tile<D, MODE>& x) {
-  const int sh = c.page_log2, pmask = (1 << sh) - 1;
-  const int ng = D / c.group;
+__device__ __forceinline__ void load_block(const Kv4Cache& c, int64_t block, int off, int t, int plus, int g, int i,
+                                           Tile<D, MODE>& x) {
+  // (block, off) and `plus` tokens, the part that is a constant of the load instructions
+  const int sh = c.page_log2;
+  const int64_t cb = ((block << sh) + off) * (D / 2);
+  const int ng = MODE == kOneGroup ? 1 : D / c.group;
+  const int64_t sb = ((block * ng) << sh) + off;
+  const uint8_t* kp = c.codes[0] + cb + (i * (D / 2) + g * (D / 8)) + plus * (D / 2);
+  const uint8_t* vp = c.codes[1] + cb + (4 * g * (D / 2) + i * (D / 32)) + plus * (D / 2);
+  if (D == 64) {
+    const uint2 r = *reinterpret_cast<const uint2*>(kp);
+    x.k[t][0] = r.x;
+    x.k[t][1] = r.y;
+  } else {
 #pragma unroll
-  for (int t = 0; t < 2; ++t) {
-    // a block past the last token reads that token's block instead (it is masked)
-    int j = t0 + 16 * t;
-    if (j > last) j = last & ~15;
-    int64_t id = table_row[j >> sh];
-    if (id < 0 || id >= c.pages) id = 0;
-    const int off = j & pmask;
-    const int64_t block = id * c.heads + head;
-    const uint8_t* kc = c.codes[0] + ((block << sh) + off) * (D / 2);
-    const uint8_t* vc = c.codes[1] + ((block << sh) + off) * (D / 2);
-    const _Float16* ks = c.scales[0] + ((block * ng) << sh) + off;
-    const _Float16* vs = c.scales[1] + ((block * ng) << sh) + off;
-    const uint32_t* kp = reinterpret_cast<const uint32_t*>(kc + i * (D / 2) + g * (D / 8));
+    for (int n = 0; n < D / 128; ++n) {
+      const u32x4 r = reinterpret_cast<const u32x4*>(kp)[n];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x.k[t][4 * n + e] = r[e];
+    }
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r) {
+    const uint8_t* vr = vp + r * (D / 2);
     if (D == 64) {
-      const uint2 r = *reinterpret_cast<const uint2*>(kp);
-      x.k[t][0] = r.x;
-      x.k[t][1] = r.y;
+      x.v[4 * t + r][0] = *reinterpret_cast<const uint16_t*>(vr);
+    } else if (D == 128) {
+      x.v[4 * t + r][0] = *reinterpret_cast<const uint32_t*>(vr);
     } else {
-#pragma unroll
-      for (int n = 0; n < D / 128; ++n) {
-        const u32x4 r = reinterpret_cast<const u32x4*>(kp)[n];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x.k[t][4 * n + e] = r[e];
-      }
+      const uint2 u = *reinterpret_cast<const uint2*>(vr);
+      x.v[4 * t + r][0] = u.x;
+      x.v[4 * t + r][D / 256] = u.y;
     }
+  }
+  const _Float16* ks = c.scales[0] + sb;
+  const _Float16* vs = c.scales[1] + sb;
+  if (MODE == kOneGroup) {
+    x.ks4[t] = *reinterpret_cast<const half4v*>(ks + 4 * g + plus);
+    x.vs[t] = *reinterpret_cast<const half4v*>(vs + 4 * g + plus);
+  } else {
 #pragma unroll
-    for (int r = 0; r < 4; ++r) {
-      const uint8_t* vp = vc + (4 * g + r) * (D / 2) + i * (D / 32);
-      if (D == 64) {
-        x.v[4 * t + r][0] = *reinterpret_cast<const uint16_t*>(vp);
-      } else if (D == 128) {
-        x.v[4 * t + r][0] = *reinterpret_cast<const uint32_t*>(vp);
-      } else {
-        const uint2 u = *reinterpret_cast<const uint2*>(vp);
-        x.v[4 * t + r][0] = u.x;
-        x.v[4 * t + r][D / 256] = u.y;
-      }
-    }
-    if (MODE == kOneGroup) {
-      x.ks4[t] = *reinterpret_cast<const half4v*>(ks + 4 * g);
-      x.vs[t] = *reinterpret_cast<const half4v*>(vs + 4 * g);
-    } else {
-#pragma unroll
-      for (int n = 0; n < Tile<D, MODE>::NS; ++n) x.ks1[t][n] = ks[(((g * (D / 4) + 32 * n) / c.group) << sh) + i];
-      x.vs[t] = *reinterpret_cast<const half4v*>(vs + ((i * (D / 16) / c.group) << sh) + 4 * g);
-    }
+    for (int n = 0; n < Tile<D, MODE>::NS; ++n) x.ks1[n][t] = ks[(((g * (D / 4) + 32 * n) / c.group) << sh) + i + plus];
+    x.vs[t] = *reinterpret_cast<const half4v*>(vs + ((i * (D / 16) / c.group) << sh) + 4 * g + plus);
   }
 }
 
 template <int D, int MODE>
-__global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE)) void kv4_attn_kernel(Kv4AttnArgs p) {
+__device__ __forceinline__ void load_tile(const Kv4Cache& c, Ids ids, int head, int t0, int last, int g, int i,
+                                          Tile<D, MODE>& x) {
+  const int pmask = (1 << c.page_log2) - 1;
+  const int j = t0 > last ? last & ~31 : t0;
+  const int id0 = (unsigned)ids.id[0] < (unsigned)c.pages ? ids.id[0] : 0;
+  const int64_t block = (int64_t)id0 * c.heads + head;
+  const int off = j & pmask;
+  load_block<D, MODE>(c, block, off, 0, 0, g, i, x);
+  if (c.page_log2 >= 5) {          // the tile lies in one page
+    load_block<D, MODE>(c, block, off, 1, 16, g, i, x);
+  } else {
+    const int id1 = (unsigned)ids.id[1] < (unsigned)c.pages ? ids.id[1] : 0;
+    load_block<D, MODE>(c, (int64_t)id1 * c.heads + head, 0, 1, 0, g, i, x);
+  }
+}
+
+// ROWS query rows a workgroup (16 or 32); FINE: fp16 queries, whose output's own
+// rounding is small enough to show that of an fp16 query, key or value
+template <int D, int MODE, bool FINE, int ROWS>
+__global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void kv4_attn_kernel(Kv4AttnArgs p) {
   constexpr int NK = D / 32;             // matrix instructions over the dims
   constexpr int NC = D / 16;             // 16-dim slices of the output
   constexpr int LD = D + 4;              // row pitch of the exchange
+  constexpr int RT = ROWS / 16;
+  constexpr int QT = FINE ? 2 : 1;       // fp16 terms of a query
+  typedef Tile<D, MODE> T;
   __shared__ float o_lds[kAttnWaves][16][LD];
   __shared__ float m_lds[kAttnWaves][16], l_lds[kAttnWaves][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i = lane & 15;
-  const int b = blockIdx.y;
-  const int head = blockIdx.x % p.c.heads;
-  const int rest = blockIdx.x / p.c.heads;
-  const int tile = rest % p.tiles, part = rest / p.tiles;
-
+  // heads vary fastest, then sequences, then row tiles, then parts: every
+  // sequence has a first part, only long ones have late ones
+  int rest = blockIdx.x / p.c.heads;
+  const int head = blockIdx.x - rest * p.c.heads;
+  const int b = rest % p.batch;
+  rest /= p.batch;
+  const int part = rest / p.tiles;
+  const int row0 = (rest - part * p.tiles) * ROWS;
   const Kv4Seq q(p, b);
-  const int row0 = tile * 16;
   if (row0 >= q.rows) return;
-  // what the tile's first and last row see, and this lane's row
+  // what the workgroup's first and last row see
   const int n_first = row0 / p.rep;
-  const int n_last = (row0 + 15 < q.rows ? row0 + 15 : q.rows - 1) / p.rep;
+  const int n_last = (row0 + ROWS - 1 < q.rows ? row0 + ROWS - 1 : q.rows - 1) / p.rep;
   const int lo = q.lo(n_first), hi = q.hi(n_last);
   const int all_lo = q.lo(n_last), all_hi = q.hi(n_first);   // [all_lo, all_hi): seen by every row
-  const int row = row0 + i;
-  const bool valid = row < q.rows;
-  const int n_mine = valid ? row / p.rep : n_last;
-  const int my_lo = q.lo(n_mine), my_hi = q.hi(n_mine);
-  const int q_row = q.s0 + n_mine;
-  const int q_head = head * p.rep + (valid ? row - n_mine * p.rep : 0);
-  // this part of the token axis; the last part takes what is left
-  const int from = (lo & ~31) + part * p.chunk;
-  int to = part == p.nsplit - 1 ? hi : from + p.chunk;
-  if (to > hi) to = hi;
+  const int parts = kv4_part_count(lo, hi, p.chunk);
+  if (part >= parts) return;
+  const int from = kv4_part_base(lo) + part * p.chunk;
+  int to = from + p.chunk;
+  if (to > hi || part == p.nsplit - 1) to = hi;
 
-  // queries: rotate, scale to [1, 2) by a power of two (kept in qf), lay out as the right operand
-  half8v qh[MODE == kF32 ? 1 : NK];
-  bf16x8v qb[MODE == kF32 ? NK : 1][3];
-  float qf = p.scale * kLog2e;
-  {
-    constexpr int E = D / 4;
-    float w[E];
-    if (valid) load_vec_any<E>(p.dtype, p.q, (int64_t)q_row * p.q_stride + q_head * D + g * E, w);
-    else
-#pragma unroll
-      for (int e = 0; e < E; ++e) w[e] = 0.0f;
-    if (p.c.rotate) {
-#pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        uint32_t sg[4];
-        load_signs<4>(p.c.signs, g * E + e, sg);
-#pragma unroll
-        for (int u = 0; u < 4; ++u) w[e + u] = flip(w[e + u], sg[u]);
-      }
-      fwht_regs<E>(w);
-      const float b0 = (g & 1) ? -1.0f : 1.0f, b1 = (g & 2) ? -1.0f : 1.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
-        const float u = fmaf(__uint_as_float(s[1]), b0, __uint_as_float(s[0]));
-        s = __builtin_amdgcn_permlane32_swap(__float_as_uint(u), __float_as_uint(u), false, false);
-        w[e] = fmaf(__uint_as_float(s[1]), b1, __uint_as_float(s[0])) * kv4_norm<D>();
-      }
-    }
-    if (MODE == kF32) {
-#pragma unroll
-      for (int c = 0; c < NK; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          __bf16 t[3];
-          bf16_terms<3>(w[8 * c + kOrder[e]], t);
-#pragma unroll
-          for (int u = 0; u < 3; ++u) qb[c][u][e] = t[u];
-        }
-    } else {
-      float mx = 0.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(w[e]));
-      mx = max_over_g(mx);
-      const int ex = row_exponent(mx);
-      qf = ldexpf(qf, ex);
-#pragma unroll
-      for (int c = 0; c < NK; ++c)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) qh[c][e] = (_Float16)ldexpf(w[8 * c + kOrder[e]], -ex);
-    }
+  // the first tile sets out before the queries are dealt with
+  const int32_t* table_row = p.table + (int64_t)b * p.width;
+  constexpr int STEP = 32 * kAttnWaves;
+  const int last = to - 1;
+  int t0 = from + 32 * wave;
+  const bool some = t0 < to;
+  T x0, x1;
+  Ids ids, ids1;
+  if (some) {
+    ids = load_ids(p.c, table_row, t0, last);
+    ids1 = load_ids(p.c, table_row, t0 + STEP, last);
+    load_tile<D, MODE>(p.c, ids, head, t0, last, g, i, x0);
   }
 
-  f32x4 acc[NC], accl = {0.0f, 0.0f, 0.0f, 0.0f};
+  // queries, 16 lanes a row as in the output: rotate, scale to [1, 2) by a power of two (kept in qf), round, and
+  // through LDS into the right operand's layout
+  constexpr int QP = D + 8;              // row pitch, 16-bit elements
+  constexpr int TERMS = MODE == kF32 ? 3 : QT;
+  static_assert(RT * TERMS * QP * 2 <= kAttnWaves * LD * 4, "the queries fit the exchange");
+  uint16_t* q_lds = reinterpret_cast<uint16_t*>(o_lds);
+  float qf[RT];
+  int my_lo[RT], my_hi[RT];
 #pragma unroll
-  for (int c = 0; c < NC; ++c) acc[c] = (f32x4){0.0f, 0.0f, 0.0f, 0.0f};
-  float m = -__builtin_inff();
+  for (int rt = 0; rt < RT; ++rt) {
+    const int qrow = threadIdx.x >> 4;
+    const int la = p.c.rotate ? kv4_logical<16>(lane) : lane & 15;
+    const int row = row0 + 16 * rt + qrow;
+    const int n = row < q.rows ? row / p.rep : 0;
+    float w[NC];
+    if (row < q.rows) {
+      load_vec_any<NC>(p.dtype, p.q, (int64_t)(q.s0 + n) * p.q_stride + (head * p.rep + row - n * p.rep) * D + la * NC, w);
+    } else {
+#pragma unroll
+      for (int e = 0; e < NC; ++e) w[e] = 0.0f;
+    }
+    if (p.c.rotate) {
+      uint32_t sg[NC];
+      load_signs<NC>(p.c.signs, la * NC, sg);
+#pragma unroll
+      for (int e = 0; e < NC; ++e) w[e] = flip(w[e], sg[e]);
+      fwht_lanes<NC, 16>(w, la);
+      const float nf = kv4_norm<D>() * kv4_tau(la);
+#pragma unroll
+      for (int e = 0; e < NC; ++e) w[e] *= nf;
+    }
+    int ex = 0;
+    if (MODE != kF32) {
+      float mx = 0.0f;
+#pragma unroll
+      for (int e = 0; e < NC; ++e) mx = fmaxf(mx, fabsf(w[e]));
+      uint32_t u = umax_dpp<kQuadXor1>(__float_as_uint(mx));
+      u = umax_dpp<kQuadXor2>(u);
+      u = umax_dpp<kRowHalfMirror>(u);
+      ex = row_exponent(__uint_as_float(umax_dpp<kRowMirror>(u)));
+    }
+    if ((lane & 15) == 0) l_lds[rt][qrow] = ldexpf(p.scale * kLog2e, ex);
+    // dim d of a row at place 8 (d / 8) + (the e with kOrder[e] = d % 8)
+    constexpr int EN = NC < 8 ? NC : 8;
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t) {
+      uint16_t* to_row = q_lds + ((rt * TERMS + t) * 16 + qrow) * QP;
+#pragma unroll
+      for (int c = 0; c < (NC + 7) / 8; ++c) {
+        uint16_t h[EN];
+#pragma unroll
+        for (int e = 0; e < EN; ++e) {
+          float& y = w[8 * c + e];
+          if (MODE == kF32) {
+            const __bf16 r = (__bf16)y;
+            y -= (float)r;
+            h[e] = __builtin_bit_cast(uint16_t, r);
+          } else {
+            if (t == 0) y = ldexpf(y, -ex);
+            const _Float16 r = (_Float16)y;
+            y -= (float)r;
+            h[e] = __builtin_bit_cast(uint16_t, r);
+          }
+        }
+        if (NC >= 8) {
+          u32x4 v;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = (uint32_t)h[kOrder[2 * e] % EN] | ((uint32_t)h[kOrder[2 * e + 1] % EN] << 16);
+          *reinterpret_cast<u32x4*>(to_row + la * NC + 8 * c) = v;
+        } else {
+          // dims 4 la .. 4 la + 3: the even or the odd places of their eight
+#pragma unroll
+          for (int e = 0; e < 4; ++e) to_row[8 * (la >> 1) + 2 * e + (la & 1)] = h[e % EN];
+        }
+      }
+    }
+    const int mine = row0 + 16 * rt + i;
+    const int n_mine = (mine < q.rows ? mine : q.rows - 1) / p.rep;
+    my_lo[rt] = q.lo(n_mine);
+    my_hi[rt] = q.hi(n_mine);
+  }
+  __syncthreads();
+  half8v qh[MODE == kF32 ? 1 : RT][QT][NK];
+  bf16x8v qb[MODE == kF32 ? RT : 1][3][NK];
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+    qf[rt] = l_lds[rt][i];
+#pragma unroll
+    for (int t = 0; t < TERMS; ++t)
+#pragma unroll
+      for (int c = 0; c < NK; ++c) {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(q_lds + ((rt * TERMS + t) * 16 + i) * QP + g * (D / 4) + 8 * c);
+        if (MODE == kF32) qb[rt][t][c] = __builtin_bit_cast(bf16x8v, v);
+        else qh[rt][t % QT][c] = __builtin_bit_cast(half8v, v);
+      }
+  }
+
+  f32x4 acc[RT][NC], accl[RT];
+  float m[RT];
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+  for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+    for (int c = 0; c < NC; ++c) acc[rt][c] = zero;
+    accl[rt] = zero;
+    m[rt] = -__builtin_inff();
+  }
+  // one group a head: acc is in units of 2^vexp, at most which every value scale so far was
+  int vexp = kMinScaleExp;
+  float vcap = 0.0f;
+  _Float16 vinv = (_Float16)1;
+  const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
   const half8v ones_h = {(_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1};
   const __bf16 one_b = (__bf16)1.0f;
   const bf16x8v ones_b = {one_b, one_b, one_b, one_b, one_b, one_b, one_b, one_b};
 
-  const int32_t* table_row = p.table + (int64_t)b * p.width;
-  Tile<D, MODE> x;
-  int t0 = from + 32 * wave;
-  if (t0 < to) load_tile<D, MODE>(p.c, table_row, head, t0, to - 1, g, i, x);
-  for (; t0 < to; t0 += 32 * kAttnWaves) {
-    Tile<D, MODE> nx;
-    {
-      const int t1 = t0 + 32 * kAttnWaves < to ? t0 + 32 * kAttnWaves : t0;
-      load_tile<D, MODE>(p.c, table_row, head, t1, to - 1, g, i, nx);
-    }
+  auto step = [&](const T& x, int t0) {
     // S^T
-    f32x4 s[2] = {{0.0f, 0.0f, 0.0f, 0.0f}, {0.0f, 0.0f, 0.0f, 0.0f}};
+    f32x4 s[RT][2];
 #pragma unroll
-    for (int t = 0; t < 2; ++t)
+    for (int t = 0; t < 2; ++t) {
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s[rt][t] = zero;
 #pragma unroll
       for (int c = 0; c < NK; ++c) {
         half2v h[4];
         codes8(x.k[t][c], h);
         if (MODE == kOneGroup) {
-          s[t] = mma(join8(h), qh[c], s[t]);
-        } else {
-          const _Float16 sc = x.ks1[t][Tile<D, MODE>::NS == 1 ? 0 : c / 4];
-          if (MODE == kGroups) {
+          const half8v k = join8(h);
 #pragma unroll
-            for (int u = 0; u < 4; ++u) h[u] = h[u] * (half2v){sc, sc};
-            s[t] = mma(join8(h), qh[c], s[t]);
-          } else {
-            bf16x8v k0, k1;
+          for (int rt = 0; rt < RT; ++rt) {
+            if (FINE) s[rt][t] = mma(k, qh[rt][QT - 1][c], s[rt][t]);
+            s[rt][t] = mma(k, qh[rt][0][c], s[rt][t]);
+          }
+          continue;
+        }
+        const _Float16 sc = x.ks1[T::NS == 1 ? 0 : c / 4][t];
+        if (MODE == kGroups) {
+          half2v k1[4];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-              __bf16 y[2];
-              bf16_terms<2>((float)h[u >> 1][u & 1] * (float)sc, y);
-              k0[u] = y[0];
-              k1[u] = y[1];
+          for (int u = 0; u < 4; ++u) {
+            const half2v y = h[u] * (half2v){sc, sc};
+            if (FINE) k1[u] = __builtin_elementwise_fma(h[u], (half2v){sc, sc}, -y);   // what the rounding left
+            h[u] = y;
+          }
+          const half8v k = join8(h);
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            if (FINE) {
+              s[rt][t] = mma(join8(k1), qh[rt][0][c], s[rt][t]);
+              s[rt][t] = mma(k, qh[rt][QT - 1][c], s[rt][t]);
             }
-            s[t] = mma(k1, qb[c][1], s[t]);
-            s[t] = mma(k0, qb[c][2], s[t]);
-            s[t] = mma(k1, qb[c][0], s[t]);
-            s[t] = mma(k0, qb[c][1], s[t]);
-            s[t] = mma(k0, qb[c][0], s[t]);
+            s[rt][t] = mma(k, qh[rt][0][c], s[rt][t]);
+          }
+        } else {
+          bf16x8v k0, k1;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            __bf16 y[2];
+            bf16_terms<2>((float)h[u >> 1][u & 1] * (float)sc, y);
+            k0[u] = y[0];
+            k1[u] = y[1];
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            f32x4& o = s[rt][t];
+            o = mma(k1, qb[rt][1][c], o);
+            o = mma(k0, qb[rt][2][c], o);
+            o = mma(k1, qb[rt][0][c], o);
+            o = mma(k0, qb[rt][1][c], o);
+            o = mma(k0, qb[rt][0][c], o);
           }
         }
       }
-    // scores of this lane's row at tokens t0 + 16 t + 4 g + r
-    float z[8];
-    half4v vs[2];
-    const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-#pragma unroll
-      for (int r = 0; r < 4; ++r) z[4 * t + r] = MODE == kOneGroup ? s[t][r] * (float)x.ks4[t][r] : s[t][r];
-      // a poisoned token has NaN scales: its score carries that to the rows that see it, its value must not
-      vs[t] = __builtin_elementwise_max(x.vs[t], zero4);
     }
-    if (t0 < all_lo || t0 + 32 > (all_hi < to ? all_hi : to)) {
+    // a poisoned token has NaN scales: its score carries that to the rows that see it, its value must not
+    half4v vs[2];
+#pragma unroll
+    for (int t = 0; t < 2; ++t) vs[t] = __builtin_elementwise_max(x.vs[t], zero4);
+    const bool edge = t0 < all_lo || t0 + 32 > (all_hi < to ? all_hi : to);
+    if (edge) {
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
         const int j = t0 + 16 * (u >> 2) + 4 * g + (u & 3);
-        if (j < my_lo || j >= my_hi || j >= to) z[u] = -__builtin_inff();
         if (j < lo || j >= to) vs[u >> 2][u & 3] = (_Float16)0;    // never written: may hold anything
       }
     }
-    float mx = z[0];
+    if (MODE == kOneGroup) {
+      // value scales go into the probabilities, relative to 2^vexp
+      const half4v v4 = __builtin_elementwise_max(vs[0], vs[1]);
+      const half2v v2 = __builtin_elementwise_max((half2v){v4[0], v4[1]}, (half2v){v4[2], v4[3]});
+      const float vm = fmaxf((float)v2[0], (float)v2[1]);
+      if (__builtin_amdgcn_ballot_w64(vm > vcap)) {
+        int e = __builtin_amdgcn_frexp_expf(max_over_g(vm));
+        e = __builtin_amdgcn_readfirstlane(e < kMinScaleExp ? kMinScaleExp : e);
+        if (e > vexp) {
+          const float f = ldexpf(1.0f, vexp - e);
 #pragma unroll
-    for (int u = 1; u < 8; ++u) mx = fmaxf(mx, z[u]);
-    mx *= qf;
-    if (__builtin_amdgcn_ballot_w64(mx > m + kMaxSlack)) {
-      const float mn = fmaxf(m, max_over_g(mx));
-      const float f = mn > m ? exp2f(m - mn) : 1.0f;
-      m = mn;
+          for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
-      for (int c = 0; c < NC; ++c) acc[c] *= f;
-      accl *= f;
+            for (int c = 0; c < NC; ++c) acc[rt][c] *= f;
+          vexp = e;
+        }
+        vcap = ldexpf(1.0f, vexp);
+        vinv = (_Float16)ldexpf(1.0f, -vexp);
+      }
+#pragma unroll
+      for (int t = 0; t < 2; ++t) vs[t] = vs[t] * (half4v){vinv, vinv, vinv, vinv};
     }
-    const float mu = m == -__builtin_inff() ? 0.0f : m;
-    float pr[8];
+    // probabilities
+    half8v ph[RT], pv[RT];
+    bf16x8v pt[MODE == kF32 ? RT : 1][3];
 #pragma unroll
-    for (int u = 0; u < 8; ++u) pr[u] = __builtin_amdgcn_exp2f(fmaf(z[u], qf, -mu));
+    for (int rt = 0; rt < RT; ++rt) {
+      float z[8];      // scores of row i at tokens t0 + 16 t + 4 g + r
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        z[u] = MODE == kOneGroup ? s[rt][u >> 2][u & 3] * (float)x.ks4[u >> 2][u & 3] : s[rt][u >> 2][u & 3];
+      if (edge) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int j = t0 + 16 * (u >> 2) + 4 * g + (u & 3);
+          if (j < my_lo[rt] || j >= my_hi[rt] || j >= to) z[u] = -__builtin_inff();
+        }
+      }
+      float mx = z[0];
+#pragma unroll
+      for (int u = 1; u < 8; ++u) mx = fmaxf(mx, z[u]);
+      mx *= qf[rt];
+      if (__builtin_amdgcn_ballot_w64(mx > m[rt] + kMaxSlack)) {
+        const float mn = fmaxf(m[rt], max_over_g(mx));
+        const float f = mn > m[rt] ? exp2f(m[rt] - mn) : 1.0f;
+        m[rt] = mn;
+#pragma unroll
+        for (int c = 0; c < NC; ++c) acc[rt][c] *= f;
+        accl[rt] *= f;
+      }
+      const float mu = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
+      float pr[8];
+#pragma unroll
+      for (int u = 0; u < 8; ++u) pr[u] = __builtin_amdgcn_exp2f(fmaf(z[u], qf[rt], -mu));
+      if (MODE == kF32) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          __bf16 t[3];
+          bf16_terms<3>(pr[u], t);
+#pragma unroll
+          for (int e = 0; e < 3; ++e) pt[rt][e][u] = t[e];
+        }
+#pragma unroll
+        for (int e = 2; e >= 0; --e) accl[rt] = mma(ones_b, pt[rt][e], accl[rt]);
+      } else {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) ph[rt][u] = (_Float16)pr[u];
+        accl[rt] = mma(ones_h, ph[rt], accl[rt]);
+        pv[rt] = ph[rt];
+        if (MODE == kOneGroup && FINE) {
+#pragma unroll
+          for (int u = 0; u < 8; ++u) pv[rt][u] = (_Float16)(pr[u] * (float)vs[u >> 2][u & 3]);
+        } else if (MODE == kOneGroup) {
+          pv[rt] = ph[rt] * (half8v){vs[0][0], vs[0][1], vs[0][2], vs[0][3], vs[1][0], vs[1][1], vs[1][2], vs[1][3]};
+        }
+      }
+    }
     // O^T
-    if (MODE != kF32) {
-      half8v ph;
 #pragma unroll
-      for (int u = 0; u < 8; ++u) ph[u] = (_Float16)pr[u];
-      accl = mma(ones_h, ph, accl);
+    for (int bb = 0; bb < NC / 2; ++bb) {
+      half2v vv[2][4];
 #pragma unroll
-      for (int bb = 0; bb < NC / 2; ++bb) {
-        half2v vl[4], vh[4];
+      for (int j = 0; j < 4; ++j)
+        codes_of_two(x.v[2 * j][bb >> 2], x.v[2 * j + 1][bb >> 2], bb & 3, vv[0][j], vv[1][j]);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
-          codes_of_two(x.v[2 * j][bb >> 2], x.v[2 * j + 1][bb >> 2], bb & 3, vl[j], vh[j]);
-          vl[j] = vl[j] * sc;
-          vh[j] = vh[j] * sc;
+      for (int d = 0; d < 2; ++d) {
+        const int c = 2 * bb + d;
+        if (MODE == kF32) {
+          bf16x8v v0, v1;
+#pragma unroll
+          for (int u = 0; u < 8; ++u) {
+            __bf16 y[2];
+            bf16_terms<2>((float)vv[d][u >> 1][u & 1] * (float)vs[u >> 2][u & 3], y);
+            v0[u] = y[0];
+            v1[u] = y[1];
+          }
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt) {
+            f32x4& o = acc[rt][c];
+            o = mma(v1, pt[rt][1], o);
+            o = mma(v0, pt[rt][2], o);
+            o = mma(v1, pt[rt][0], o);
+            o = mma(v0, pt[rt][1], o);
+            o = mma(v0, pt[rt][0], o);
+          }
+          continue;
         }
-        acc[2 * bb] = mma(join8(vl), ph, acc[2 * bb]);
-        acc[2 * bb + 1] = mma(join8(vh), ph, acc[2 * bb + 1]);
-      }
-    } else {
-      bf16x8v pt[3];
+        half2v v1[4];
+        if (MODE == kGroups) {
 #pragma unroll
-      for (int u = 0; u < 8; ++u) {
-        __bf16 t[3];
-        bf16_terms<3>(pr[u], t);
-#pragma unroll
-        for (int e = 0; e < 3; ++e) pt[e][u] = t[e];
-      }
-#pragma unroll
-      for (int e = 2; e >= 0; --e) accl = mma(ones_b, pt[e], accl);
-#pragma unroll
-      for (int bb = 0; bb < NC / 2; ++bb) {
-        bf16x8v v0[2], v1[2];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          half2v vv[2];
-          codes_of_two(x.v[2 * j][bb >> 2], x.v[2 * j + 1][bb >> 2], bb & 3, vv[0], vv[1]);
-#pragma unroll
-          for (int d = 0; d < 2; ++d)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-              __bf16 y[2];
-              bf16_terms<2>((float)vv[d][e] * (float)vs[j >> 1][2 * (j & 1) + e], y);
-              v0[d][2 * j + e] = y[0];
-              v1[d][2 * j + e] = y[1];
-            }
+          for (int j = 0; j < 4; ++j) {
+            const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
+            const half2v y = vv[d][j] * sc;
+            if (FINE) v1[j] = __builtin_elementwise_fma(vv[d][j], sc, -y);
+            vv[d][j] = y;
+          }
         }
+        const half8v v = join8(vv[d]);
 #pragma unroll
-        for (int d = 0; d < 2; ++d) {
-          f32x4& o = acc[2 * bb + d];
-          o = mma(v1[d], pt[1], o);
-          o = mma(v0[d], pt[2], o);
-          o = mma(v1[d], pt[0], o);
-          o = mma(v0[d], pt[1], o);
-          o = mma(v0[d], pt[0], o);
+        for (int rt = 0; rt < RT; ++rt) {
+          if (MODE == kGroups && FINE) acc[rt][c] = mma(join8(v1), pv[rt], acc[rt][c]);
+          acc[rt][c] = mma(v, pv[rt], acc[rt][c]);
         }
       }
     }
-    x = nx;
+  };
+
+  // two tiles in registers: one at work, the next on its way; the page ids of a third
+  if (some) {
+    for (;;) {
+      ids = load_ids(p.c, table_row, t0 + 2 * STEP, last);
+      load_tile<D, MODE>(p.c, ids1, head, t0 + STEP, last, g, i, x1);
+      step(x0, t0);
+      t0 += STEP;
+      if (t0 >= to) break;
+      ids1 = load_ids(p.c, table_row, t0 + 2 * STEP, last);
+      load_tile<D, MODE>(p.c, ids, head, t0 + STEP, last, g, i, x0);
+      step(x1, t0);
+      t0 += STEP;
+      if (t0 >= to) break;
+    }
   }
 
-  // join the waves: lane (g, i) holds dims [g D/4, (g+1) D/4) of row i
-  if (g == 0) m_lds[wave][i] = m;
-  __syncthreads();
-  float top = m_lds[0][i];
+  // join the waves, 16 rows at a time: lane (g, i) holds dims [g D/4, (g+1) D/4) of row i
+  __syncthreads();           // the exchange held the queries
+  const float unit = MODE == kOneGroup ? ldexpf(1.0f, vexp) : 1.0f;
 #pragma unroll
-  for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w][i]);
-  const float f = m == -__builtin_inff() ? 0.0f : exp2f(m - top);
-  if (g == 0) l_lds[wave][i] = accl[0] * f;
+  for (int rt = 0; rt < RT; ++rt) {
+    if (rt) __syncthreads();
+    if (g == 0) m_lds[wave][i] = m[rt];
+    __syncthreads();
+    float top = m_lds[0][i];
 #pragma unroll
-  for (int r = 0; r < 4; ++r)
+    for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w][i]);
+    const float f = m[rt] == -__builtin_inff() ? 0.0f : exp2f(m[rt] - top);
+    const float fu = f * unit;
+    if (g == 0) l_lds[wave][i] = accl[rt][0] * f;
 #pragma unroll
-    for (int c = 0; c < NC; c += 4)
-      *reinterpret_cast<f32x4*>(&o_lds[wave][i][(4 * g + r) * NC + c]) =
-          (f32x4){acc[c][r] * f, acc[c + 1][r] * f, acc[c + 2][r] * f, acc[c + 3][r] * f};
-  __syncthreads();
-  // 16 lanes a row, D/16 consecutive dims each
-  const int orow = threadIdx.x >> 4;
-  const int la = kv4_logical<16>(lane);
-  float w[NC], l = 0.0f, mt = m_lds[0][orow];
+    for (int r = 0; r < 4; ++r)
 #pragma unroll
-  for (int e = 0; e < NC; ++e) w[e] = 0.0f;
+      for (int c = 0; c < NC; c += 4)
+        *reinterpret_cast<f32x4*>(&o_lds[wave][i][(4 * g + r) * NC + c]) =
+            (f32x4){acc[rt][c][r] * fu, acc[rt][c + 1][r] * fu, acc[rt][c + 2][r] * fu, acc[rt][c + 3][r] * fu};
+    __syncthreads();
+    // 16 lanes a row, D/16 consecutive dims each
+    const int orow = threadIdx.x >> 4;
+    const int la = kv4_logical<16>(lane);
+    float y[NC], l = 0.0f, mt = m_lds[0][orow];
 #pragma unroll
-  for (int v = 0; v < kAttnWaves; ++v) {
-    l += l_lds[v][orow];
-    mt = fmaxf(mt, m_lds[v][orow]);
+    for (int e = 0; e < NC; ++e) y[e] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < NC; e += 4) {
-      const f32x4 r = *reinterpret_cast<const f32x4*>(&o_lds[v][orow][la * NC + e]);
+    for (int v = 0; v < kAttnWaves; ++v) {
+      l += l_lds[v][orow];
+      mt = fmaxf(mt, m_lds[v][orow]);
 #pragma unroll
-      for (int u = 0; u < 4; ++u) w[e + u] += r[u];
+      for (int e = 0; e < NC; e += 4) {
+        const f32x4 r = *reinterpret_cast<const f32x4*>(&o_lds[v][orow][la * NC + e]);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) y[e + u] += r[u];
+      }
     }
-  }
-  const int r2 = row0 + orow;
-  const bool store = r2 < q.rows;
-  const int n2 = store ? r2 / p.rep : 0;
-  const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
-  if (p.nsplit > 1) {
-    if (store) {
+    const int r2 = row0 + 16 * rt + orow;
+    const bool store = r2 < q.rows;
+    const int n2 = store ? r2 / p.rep : 0;
+    const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
+    if (parts > 1 && p.nsplit > 1) {
+      if (!store) continue;
       const int64_t at = out_row * p.nsplit + part;
-      store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, w);
+      store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, y);
       if (la == 0) p.part_ml[at] = make_float2(mt, l);
+    } else {
+      finish_row<D>(p.c.rotate, p.c.signs, l, la, y);
+      if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, y);
     }
-    return;
   }
-  finish_row<D>(p.c, l, la, w);
-  if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
 }
 
-// One workgroup joins the parts of one output row: its 16 lane groups take the
-// parts in turn, LDS adds the groups up, the first group rotates back.
-template <int D>
+// Joins the parts of output rows.  GROUPS 16-lane groups of a workgroup share
+// a row and take its parts in turn; LDS adds the groups up, the first of them
+// rotates back.  One group a row where parts are few (a wave's work is then all
+// loads, and a workgroup does 16 rows), all 16 where they are many.
+template <int D, int GROUPS>
 __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
   constexpr int NC = D / 16;
-  __shared__ float o_lds[16][D + 4];
-  __shared__ float l_lds[16];
+  __shared__ float o_lds[GROUPS][D + 4];
+  __shared__ float l_lds[GROUPS];
   const int lane = threadIdx.x & 63;
-  const int grp = threadIdx.x >> 4;
+  const int grp = (threadIdx.x >> 4) % GROUPS;
   const int la = kv4_logical<16>(lane);
   const int b = blockIdx.y;
-  const int n = blockIdx.x / p.q_heads;
+  const int at_row = blockIdx.x * (16 / GROUPS) + (threadIdx.x >> 4) / GROUPS;
+  const int n = at_row / p.q_heads, q_head = at_row - n * p.q_heads;
   const Kv4Seq q(p, b);
-  if (n >= q.news) return;
-  const int64_t out_row = (int64_t)(q.s0 + n) * p.q_heads + (blockIdx.x - n * p.q_heads);
-  const float2* ml = p.part_ml + out_row * p.nsplit;
+  const bool valid = n < q.news;
+  const int64_t out_row = (int64_t)(q.s0 + (valid ? n : 0)) * p.q_heads + q_head;
+  // its row tile's parts (with one, the row is finished)
+  int parts = 1;
+  if (valid) {
+    const int row0 = (n * p.rep + q_head % p.rep) / p.rows * p.rows;
+    const int row1 = row0 + p.rows < q.rows ? row0 + p.rows : q.rows;
+    parts = kv4_part_count(q.lo(row0 / p.rep), q.hi((row1 - 1) / p.rep), p.chunk);
+    if (parts > p.nsplit) parts = p.nsplit;
+  }
+  if (GROUPS > 1 && parts == 1) return;      // the whole workgroup
+  const int64_t first = out_row * p.nsplit;
   float top = -__builtin_inff();
-  for (int s = lane; s < p.nsplit; s += 64) top = fmaxf(top, ml[s].x);
-  top = wave_max(top);
+  if (GROUPS > 1) {
+    for (int s = lane; s < parts; s += 64) top = fmaxf(top, p.part_ml[first + s].x);
+    top = wave_max(top);
+  } else if (parts > 1) {
+    for (int s = 0; s < parts; ++s) top = fmaxf(top, p.part_ml[first + s].x);
+  }
   float w[NC], l = 0.0f;
 #pragma unroll
   for (int e = 0; e < NC; ++e) w[e] = 0.0f;
-  for (int s = grp; s < p.nsplit; s += 16) {
-    const float2 v = ml[s];
-    const float f = v.x == -__builtin_inff() ? 0.0f : exp2f(v.x - top);
-    l += v.y * f;
-    float o[NC];
-    load_vec<kDtF32, NC>(p.part_o + (out_row * p.nsplit + s) * D + la * NC, o);
+  if (parts > 1) {
+    for (int s = grp; s < parts; s += GROUPS) {
+      const int64_t at = first + s;
+      const float2 v = p.part_ml[at];
+      const float f = v.x == -__builtin_inff() ? 0.0f : exp2f(v.x - top);
+      l += v.y * f;
+      float o[NC];
+      load_vec<kDtF32, NC>(p.part_o + at * D + la * NC, o);
 #pragma unroll
-    for (int e = 0; e < NC; ++e) w[e] = fmaf(o[e], f, w[e]);
+      for (int e = 0; e < NC; ++e) w[e] = fmaf(o[e], f, w[e]);
+    }
   }
-  store_vec<kDtF32, NC>(&o_lds[grp][la * NC], w);
-  if (la == 0) l_lds[grp] = l;
-  __syncthreads();
-  if (grp >= 4) return;      // the first wave goes on (all of it: the exchanges need whole rows)
+  if (GROUPS > 1) {
+    store_vec<kDtF32, NC>(&o_lds[grp][la * NC], w);
+    if (la == 0) l_lds[grp] = l;
+    __syncthreads();
+    if (grp >= 4) return;      // the first wave goes on (all of it: the exchanges need whole rows)
 #pragma unroll
-  for (int e = 0; e < NC; ++e) w[e] = 0.0f;
-  l = 0.0f;
-  for (int s = 0; s < 16; ++s) {
-    l += l_lds[s];
+    for (int e = 0; e < NC; ++e) w[e] = 0.0f;
+    l = 0.0f;
+    for (int s = 0; s < GROUPS; ++s) {
+      l += l_lds[s];
 #pragma unroll
-    for (int e = 0; e < NC; ++e) w[e] += o_lds[s][la * NC + e];
+      for (int e = 0; e < NC; ++e) w[e] += o_lds[s][la * NC + e];
+    }
   }
-  finish_row<D>(p.c, l, la, w);
-  if (grp == 0) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
+  finish_row<D>(p.c.rotate, p.c.signs, l, la, w);
+  if (grp == 0 && parts > 1) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
 }
 
-// Which kernel, and into how many parts of the token axis: enough workgroups to
-// fill the chip (three a CU of 16 rows, two of 128), none with fewer than 256
-// tokens (two tiles a wave) or, of 128 rows, 512.
+// Which kernel, and into how many parts of the token axis.
+//
+// Rows: 16 a workgroup of the kernel above; 32 where there are more than 16
+// and the registers allow (the codes of a tile are then made fp16 once for
+// both halves); past 32, 128 of the prompt kernel.
+// Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
+// tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
+// two and a half for several, whose lengths differ (64 sequences of 1100 to
+// 8192 tokens: 77.7 us; two a CU 84.6, six 80.7); no part under 256 tokens (two
+// tiles a wave), or 512 of the prompt kernel.
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
-  a->prompt = a->dtype != kDtF32 && rows > 32;
-  const int64_t rows_of = a->prompt ? kPromptRows : 16, least = a->prompt ? 512 : 256;
-  const int64_t want = a->prompt ? 512 : 768;
-  a->tiles = (int)((rows + rows_of - 1) / rows_of);
+  a->rows = 16;
+  if (a->dtype != kDtF32) {
+    if (rows > 32) a->rows = kPromptRows;
+    else if (rows > 16 && a->c.dim <= 128) a->rows = 32;
+  }
+  a->tiles = (int)((rows + a->rows - 1) / a->rows);
   int64_t span = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
-  const int64_t groups = (int64_t)a->batch * a->c.heads * a->tiles;
-  int64_t n = groups > 0 ? (want + groups - 1) / groups : 1;
+  const int64_t segments = (int64_t)a->batch * a->c.heads * a->tiles;
+  const int64_t least = a->rows == kPromptRows ? 512 : 256;
+  const int64_t want = a->rows == kPromptRows || a->batch == 1 ? 512 : 640;
+  int64_t n = segments > 0 ? (want + segments - 1) / segments : 1;
   const int64_t most = (span + least - 1) / least;
   if (n > most) n = most;
   if (n < 1) n = 1;
@@ -492,18 +704,32 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
   if (chunk < least) chunk = least;
   n = (span + chunk - 1) / chunk;
   a->nsplit = (int)(n < 1 ? 1 : n);
-  a->chunk = (int)chunk;
+  a->chunk = a->nsplit == 1 ? kKv4MaxLen : (int)chunk;
+  a->groups = segments * a->nsplit;
+}
+
+template <int D, int MODE, bool FINE>
+static void attn2(const Kv4AttnArgs& a, dim3 g, hipStream_t s) {
+  if (D <= 128 && MODE != kF32 && a.rows == 32)
+    hipLaunchKernelGGL((kv4_attn_kernel<D, MODE, FINE, D <= 128 && MODE != kF32 ? 32 : 16>), g, dim3(kAttnThreads), 0, s, a);
+  else
+    hipLaunchKernelGGL((kv4_attn_kernel<D, MODE, FINE, 16>), g, dim3(kAttnThreads), 0, s, a);
 }
 
 template <int D>
 static void attn1(const Kv4AttnArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)a.c.heads * a.tiles * a.nsplit), a.batch), b(kAttnThreads);
-  if (a.prompt) launch_kv4_prompt(a, s);
-  else if (a.dtype == kDtF32) hipLaunchKernelGGL((kv4_attn_kernel<D, kF32>), g, b, 0, s, a);
-  else if (a.c.group == D) hipLaunchKernelGGL((kv4_attn_kernel<D, kOneGroup>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((kv4_attn_kernel<D, kGroups>), g, b, 0, s, a);
-  if (a.nsplit > 1)
-    hipLaunchKernelGGL(kv4_join_kernel<D>, dim3((unsigned)(a.max_new * a.q_heads), a.batch), b, 0, s, a);
+  const dim3 g((unsigned)a.groups);
+  if (a.rows == kPromptRows) launch_kv4_prompt(a, s);
+  else if (a.dtype == kDtF32) attn2<D, kF32, false>(a, g, s);
+  else if (a.c.group == D && a.dtype == kDtF16) attn2<D, kOneGroup, true>(a, g, s);
+  else if (a.c.group == D) attn2<D, kOneGroup, false>(a, g, s);
+  else if (a.dtype == kDtF16) attn2<D, kGroups, true>(a, g, s);
+  else attn2<D, kGroups, false>(a, g, s);
+  if (a.nsplit > kFewParts)
+    hipLaunchKernelGGL((kv4_join_kernel<D, 16>), dim3((unsigned)(a.max_new * a.q_heads), a.batch), dim3(kAttnThreads), 0, s, a);
+  else if (a.nsplit > 1)
+    hipLaunchKernelGGL((kv4_join_kernel<D, 1>), dim3((unsigned)((a.max_new * a.q_heads + 15) / 16), a.batch),
+                       dim3(kAttnThreads), 0, s, a);
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t s) {

@@ -84,6 +84,31 @@ __device__ __forceinline__ void fwht_lanes(float* w, int a) {
   }
 }
 
+// The same for two vectors of 8 elements a lane at once, w[0..7] and w[8..15]:
+// one instruction an element and exchange.
+template <int L>
+__device__ __forceinline__ void fwht_lanes2(float* w, int a) {
+  fwht_regs<8>(w);
+  fwht_regs<8>(w + 8);
+  const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;
+  const float b2 = (a & 4) ? -1.0f : 1.0f;
+  HR_FMAC_DPP16(w, b0, "quad_perm:[1,0,3,2]");
+  HR_FMAC_DPP16(w, b1, "quad_perm:[2,3,0,1]");
+  HR_FMAC_DPP16(w, b2, "row_half_mirror");
+  if (L >= 16) {
+    const float b3 = (a & 8) ? -1.0f : 1.0f;
+    HR_FMAC_DPP16(w, b3, "row_ror:8");
+  }
+  if (L >= 32) {
+    const float b4 = (a & 16) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
+      w[e] = fmaf(__uint_as_float(s[1]), b4, __uint_as_float(s[0]));
+    }
+  }
+}
+
 // N consecutive elements (N * size a multiple of 8 bytes) of type DT to fp32.
 template <int DT, int N>
 __device__ __forceinline__ void load_vec(const void* p, float* w) {

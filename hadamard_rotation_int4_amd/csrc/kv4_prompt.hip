@@ -158,20 +158,23 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
-  const int b = blockIdx.y;
   const int head = blockIdx.x % p.c.heads;
-  const int rest = blockIdx.x / p.c.heads;
+  int rest = blockIdx.x / p.c.heads;
   const int part = rest % p.nsplit;
-  const int tile = p.tiles - 1 - rest / p.nsplit;
+  rest /= p.nsplit;
+  const int b = rest % p.batch;
+  const int tile = p.tiles - 1 - rest / p.batch;
   const Kv4Seq q(p, b);
   const int row0 = tile * kPromptRows;
   if (row0 >= q.rows) return;
   // what the workgroup's rows see
   const int row_end = row0 + kPromptRows < q.rows ? row0 + kPromptRows : q.rows;
   const int lo = q.lo(row0 / p.rep), hi = q.hi((row_end - 1) / p.rep);
-  const int from = (lo & ~31) + part * p.chunk;
-  int to = part == p.nsplit - 1 ? hi : from + p.chunk;
-  if (to > hi) to = hi;
+  const int parts = kv4_part_count(lo, hi, p.chunk);
+  if (part >= parts) return;
+  const int from = kv4_part_base(lo) + part * p.chunk;
+  int to = from + p.chunk;
+  if (to > hi || part == p.nsplit - 1) to = hi;
   // what this wave's rows see; a wave past the rows sees nothing
   const int wrow0 = row0 + 32 * wave;
   const bool any = wrow0 < q.rows;
@@ -350,14 +353,14 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
       const bool store = r2 < q.rows;
       const int n2 = store ? r2 / p.rep : 0;
       const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
-      if (p.nsplit > 1) {
+      if (parts > 1 && p.nsplit > 1) {
         if (store) {
           const int64_t at = out_row * p.nsplit + part;
           store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, w);
           if (la == 0) p.part_ml[at] = make_float2(mr, lr);
         }
       } else {
-        finish_row<D>(p.c, lr, la, w);
+        finish_row<D>(p.c.rotate, p.c.signs, lr, la, w);
         if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
       }
     }
@@ -367,7 +370,7 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
 
 template <int D>
 static void prompt1(const Kv4AttnArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)((int64_t)a.c.heads * a.tiles * a.nsplit), a.batch), b(kPromptThreads);
+  const dim3 g((unsigned)a.groups), b(kPromptThreads);
   if (a.dtype == kDtF16) hipLaunchKernelGGL((kv4_prompt_kernel<D, 2>), g, b, 0, s, a);
   else hipLaunchKernelGGL((kv4_prompt_kernel<D, 1>), g, b, 0, s, a);
 }

@@ -517,7 +517,8 @@ typedef struct {
  * For the key and the value x of every (token, head): y = x or its rotation;
  * per group a = max |y|, s = fp16(a / 7) (stored), k = 1 / s (0 when s == 0),
  * q = clamp(rint(y k), -7, 7), each step one fp32 operation rounded to nearest
- * even (with the rotation, k and 1 / sqrt(dim) are one factor).
+ * even (with the rotation, k and 1 / sqrt(dim) are one factor, whose product is
+ * rounded to an integer at once).
  * A (token, head) whose key or value is not finite, or needs a scale above the
  * fp16 range, is stored with zero codes and NaN scales in both: reading it, or
  * attending to it, gives NaN.
