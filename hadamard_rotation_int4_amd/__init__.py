@@ -778,7 +778,7 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype=torch.bfloat16, k: torc
     else:
         _arg(k, "k", dtype, shape)
     if v is None:
-        v = torch.empty(shape, dtype=dtype, device=cache.device)
+        v = torch.empty_like(k)
     else:
         _arg(v, "v", dtype, shape)
     st = lib.hr_kv4_read(cache._ref, _kv4_ptr(cache, slots, "slots"), shape[0], _KV4_TYPES[dtype],

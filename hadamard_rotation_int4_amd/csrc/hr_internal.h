@@ -125,9 +125,6 @@ constexpr int kDtF32 = 0, kDtBf16 = 1, kDtF16 = 2;
 // Largest cached length: token indices of a sequence stay in 32 bits.
 constexpr int kKv4MaxLen = 1 << 30;
 
-// Query rows of a workgroup of the prompt kernel.
-constexpr int kPromptRows = 128;
-
 // A 4-bit key/value cache after host validation (layout: kv4_device.h).
 struct Kv4Cache {
   uint8_t* codes[2];     // keys, values
@@ -175,7 +172,7 @@ struct Kv4AttnArgs {
   float* part_o;         // [total * q_heads][nsplit][dim] sums, not yet divided; null when nsplit == 1
   float2* part_ml;       // [total * q_heads][nsplit] (running max in log2 units, sum)
   // by kv4_attention_plan:
-  int rows;              // of a row tile: 16, 32 or kPromptRows (kv4_prompt.hip)
+  int rows;              // of a row tile: 16, 32, or 128 or 256 (kv4_prompt.hip)
   int tiles;             // row tiles of a (sequence, key/value head)
   int nsplit, chunk;     // most parts of the token axis, tokens of a part
   int64_t groups;        // workgroups
@@ -186,7 +183,7 @@ hipError_t launch_kv4_read(const Kv4ReadArgs& a, hipStream_t s);
 // Fills its part of the arguments from the sizes and types.
 void kv4_attention_plan(Kv4AttnArgs* a);
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t s);
-void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s);   // its part when a.rows == kPromptRows
+void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s);   // its part when a.rows >= 128
 
 hipError_t launch_harp_blocks(const HarpSchedule& sc, const float* theta, const float* fallbacks,
                               float* blocks, hipStream_t s);

@@ -357,7 +357,7 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
           }
           continue;
         }
-        const _Float16 sc = x.ks1[T::NS == 1 ? 0 : c / 4][t];
+        const _Float16 sc = (c < 4 ? x.ks1[0] : x.ks1[T::NS - 1])[t];
         if (MODE == kGroups) {
           half2v k1[4];
 #pragma unroll
@@ -677,25 +677,31 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
 //
 // Rows: 16 a workgroup of the kernel above; 32 where there are more than 16
 // and the registers allow (the codes of a tile are then made fp16 once for
-// both halves); past 32, 128 of the prompt kernel.
+// both halves); past 32 bf16 ones, 128 of the prompt kernel, or 256 of it for 128 dims
+// and more than 128 rows (2048 tokens, 32 heads on 8, over 8192: 276 against
+// 292 us; 64 dims lose the third workgroup a CU, 127 against 101 us, and 256
+// dims the registers).  The prompt kernel's keys and values are rounded to
+// fp16, which an fp16 output would show (its error 5.5e-4 where the rounding of
+// the output alone is 2.1e-4, against 2.4e-4 here, at 372 against 446 us).
 // Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
 // two and a half for several, whose lengths differ (64 sequences of 1100 to
 // 8192 tokens: 77.7 us; two a CU 84.6, six 80.7); no part under 256 tokens (two
-// tiles a wave), or 512 of the prompt kernel.
+// tiles a wave), or 512 of the prompt kernel.  The prompt kernel gets as many
+// workgroups as run at once.
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
   a->rows = 16;
   if (a->dtype != kDtF32) {
-    if (rows > 32) a->rows = kPromptRows;
+    if (rows > 32 && a->dtype == kDtBf16) a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
     else if (rows > 16 && a->c.dim <= 128) a->rows = 32;
   }
   a->tiles = (int)((rows + a->rows - 1) / a->rows);
   int64_t span = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
   const int64_t segments = (int64_t)a->batch * a->c.heads * a->tiles;
-  const int64_t least = a->rows == kPromptRows ? 512 : 256;
-  const int64_t want = a->rows == kPromptRows || a->batch == 1 ? 512 : 640;
+  const int64_t least = a->rows >= 128 ? 512 : 256;
+  const int64_t want = a->rows == 256 ? 256 : a->rows == 128 || a->batch == 1 ? 512 : 640;
   int64_t n = segments > 0 ? (want + segments - 1) / segments : 1;
   const int64_t most = (span + least - 1) / least;
   if (n > most) n = most;
@@ -719,7 +725,7 @@ static void attn2(const Kv4AttnArgs& a, dim3 g, hipStream_t s) {
 template <int D>
 static void attn1(const Kv4AttnArgs& a, hipStream_t s) {
   const dim3 g((unsigned)a.groups);
-  if (a.rows == kPromptRows) launch_kv4_prompt(a, s);
+  if (a.rows >= 128) launch_kv4_prompt(a, s);
   else if (a.dtype == kDtF32) attn2<D, kF32, false>(a, g, s);
   else if (a.c.group == D && a.dtype == kDtF16) attn2<D, kOneGroup, true>(a, g, s);
   else if (a.c.group == D) attn2<D, kOneGroup, false>(a, g, s);

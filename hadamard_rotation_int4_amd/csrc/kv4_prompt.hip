@@ -1,11 +1,11 @@
 // Attention over the 4-bit key/value cache for many query rows (prompts and
-// chunks of prompts), 16-bit queries.  The mathematics is kv4_attention.hip's;
+// chunks of prompts), bf16 queries.  The mathematics is kv4_attention.hip's;
 // here it is the matrix products that count, so a workgroup shares each tile's
 // codes-to-fp16 work among 128 query rows through LDS.
 //
-// One workgroup of 4 waves takes 128 query rows of one (sequence, key/value
-// head), row = new token * rep + head of the group, and walks over 64-token
-// tiles.  Each wave owns 32 rows and computes, on 32x32x16 instructions,
+// One workgroup of 4 or 8 waves takes 32 query rows a wave of one (sequence,
+// key/value head), row = new token * rep + head of the group, and walks over
+// 64-token tiles.  Each wave computes, on 32x32x16 instructions,
 //   S^T = K q'^T (rows: tokens),   O^T = V^T P^T (rows: dims):
 // S^T leaves query row n = lane % 32 in the lane, with tokens
 // 8 (r / 4) + 4 h + r % 4 in register r (h = lane / 32), which is what the
@@ -22,8 +22,16 @@
 //           tokens of slots (h, .) of 16-token step t; a piece's place among
 //           the dims is the transposed (dim % (dim/16), dim / (dim/16)), so
 //           that 16 lanes that hold neighbouring dims write contiguously.
-// Two buffers: while the products read one tile, the next one's codes are on
-// their way to registers, and then to the other buffer; one barrier a tile.
+// Two buffers of each.  A turn of the loop makes the scores of tile t + 1 while
+// the softmax works on those of tile t, then adds tile t's values while the keys
+// of t + 2 and the values of t + 1 become fp16; one barrier a turn.  With 8
+// waves four deal with the keys and four with the values.
+//
+// Bound by the matrix instructions at the clock they leave: without the
+// fp16 work, the exponentials and the LDS reads the rest of the loop takes 199
+// of 290 us (2048 tokens, 32 heads on 8, 128 dims, over 8192; 4 waves), which
+// is the rate of a large library product; making fp16 costs 65 of it (8 waves
+// halve that), the LDS reads 22, the exponentials 16.
 //
 // Heads vary fastest over the grid, so that with 8 heads the workgroups of one
 // head share an XCD's L2; the last rows, which see most, go first.
@@ -31,45 +39,49 @@
 
 namespace hr {
 
-constexpr int kPromptThreads = 256;
-constexpr int kPromptWaves = kPromptThreads / 64;
 constexpr int kPromptTokens = 64;           // of a tile
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
+
 
 __device__ __forceinline__ f32x16 mma32(half8v a, half8v b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
 }
 
-// One thread's share of a tile's codes and scales on their way to LDS: a
-// quarter of one token's key, and dim / 16 dims of four tokens' values.
+// One thread's share of a tile on its way to LDS: a quarter of one token's key,
+// and dim / 16 dims of four tokens' values, with their scales.  Wave w's shares
+// are of the tile's 16-token block w: one page.
 template <int D>
-struct Share {
-  static constexpr int NK = D / 32;                     // key dwords
-  static constexpr int NV = (D + 127) / 128;            // value dwords a token
-  static constexpr int NS = D == 256 ? 2 : 1;           // 32-dim spans of the key's share with scales of their own
-  uint32_t k[NK];
+struct KeyShare {
+  static constexpr int NS = D == 256 ? 2 : 1;           // 32-dim spans with scales of their own
+  uint32_t k[D / 32];
+  _Float16 s[NS];
+};
+template <int D>
+struct ValueShare {
+  static constexpr int NV = (D + 127) / 128;            // dwords a token
   uint32_t v[4][NV];
-  _Float16 ks[NS];
-  half4v vs;
+  half4v s;
 };
 
-// Wave w's share is the tile's 16-token block w: one page.
+// Token block and codes' place of token j, a multiple of 16; past the last
+// token any block of the sequence (it is masked).
+struct Place {
+  int64_t block;
+  int off;
+};
+__device__ __forceinline__ Place place_of(const Kv4Cache& c, const int32_t* table_row, int head, int j, int last) {
+  if (j > last) j = last & ~15;
+  int id = read_index(table_row, j >> c.page_log2);
+  if ((unsigned)id >= (unsigned)c.pages) id = 0;
+  return {(int64_t)id * c.heads + head, j & ((1 << c.page_log2) - 1)};
+}
+
 template <int D>
-__device__ __forceinline__ void load_share(const Kv4Cache& c, const int32_t* table_row, int head, int j, int last,
-                                           int lane, Share<D>& x) {
-  if (j > last) j = last & ~15;        // past the end: any block of the sequence, masked
+__device__ __forceinline__ void load_keys(const Kv4Cache& c, Place at, int lane, KeyShare<D>& x) {
   const int sh = c.page_log2;
-  int64_t id = table_row[j >> sh];
-  if (id < 0 || id >= c.pages) id = 0;
-  const int off = j & ((1 << sh) - 1);
-  const int64_t block = id * c.heads + head;
-  const uint8_t* kc = c.codes[0] + ((block << sh) + off) * (D / 2);
-  const uint8_t* vc = c.codes[1] + ((block << sh) + off) * (D / 2);
-  const int64_t sb = ((block * (D / c.group)) << sh) + off;
-  const int kt = lane >> 2, kp = lane & 3;              // key: token of the block, quarter
-  const int vq = lane >> 4, va = lane & 15;             // value: token quad of the block, dims
-  const uint8_t* kk = kc + kt * (D / 2) + kp * (D / 8);
+  const int kt = lane >> 2, kp = lane & 3;              // token of the block, quarter
+  const uint8_t* kk = c.codes[0] + ((at.block << sh) + at.off) * (D / 2) + (kt * (D / 2) + kp * (D / 8));
   if (D == 64) {
     const uint2 r = *reinterpret_cast<const uint2*>(kk);
     x.k[0] = r.x;
@@ -82,9 +94,19 @@ __device__ __forceinline__ void load_share(const Kv4Cache& c, const int32_t* tab
       for (int e = 0; e < 4; ++e) x.k[4 * n + e] = r[e];
     }
   }
+  const _Float16* sc = c.scales[0] + ((at.block * (D / c.group)) << sh) + at.off;
+#pragma unroll
+  for (int n = 0; n < KeyShare<D>::NS; ++n) x.s[n] = sc[(((kp * (D / 4) + 32 * n) / c.group) << sh) + kt];
+}
+
+template <int D>
+__device__ __forceinline__ void load_values(const Kv4Cache& c, Place at, int lane, ValueShare<D>& x) {
+  const int sh = c.page_log2;
+  const int vq = lane >> 4, va = lane & 15;             // token quad of the block, dims
+  const uint8_t* vc = c.codes[1] + ((at.block << sh) + at.off) * (D / 2) + (4 * vq * (D / 2) + va * (D / 32));
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
-    const uint8_t* vv = vc + (4 * vq + r) * (D / 2) + va * (D / 32);
+    const uint8_t* vv = vc + r * (D / 2);
     if (D == 64) {
       x.v[r][0] = *reinterpret_cast<const uint16_t*>(vv);
     } else if (D == 128) {
@@ -92,46 +114,50 @@ __device__ __forceinline__ void load_share(const Kv4Cache& c, const int32_t* tab
     } else {
       const uint2 u = *reinterpret_cast<const uint2*>(vv);
       x.v[r][0] = u.x;
-      x.v[r][Share<D>::NV - 1] = u.y;
+      x.v[r][ValueShare<D>::NV - 1] = u.y;
     }
   }
-#pragma unroll
-  for (int n = 0; n < Share<D>::NS; ++n) x.ks[n] = c.scales[0][sb + (((kp * (D / 4) + 32 * n) / c.group) << sh) + kt];
-  x.vs = *reinterpret_cast<const half4v*>(c.scales[1] + sb + ((va * (D / 16) / c.group) << sh) + 4 * vq);
+  x.s = *reinterpret_cast<const half4v*>(c.scales[1] + ((at.block * (D / c.group)) << sh) + at.off +
+                                         ((va * (D / 16) / c.group) << sh) + 4 * vq);
 }
 
 template <int D>
 struct PromptLds {
   static constexpr int KROW = kPromptTokens * 16 + 16;  // bytes of a row of key pieces
   static constexpr int KEYS = D / 8 * KROW;
-  static constexpr int BUF = KEYS + kPromptTokens / 8 * D * 16;
+  static constexpr int VALUES = kPromptTokens / 8 * D * 16;
+  static constexpr int ALL = 2 * KEYS + 2 * VALUES;     // two key buffers, two value buffers
 };
 
-// The share to fp16 and into a buffer.  [lo, to): tokens that some row of the
-// tile sees; values of others may be anything and become 0.
+// The shares to fp16 and into a buffer.
 template <int D>
-__device__ __forceinline__ void store_share(const Share<D>& x, char* buf, int wave, int lane, int j0, int lo, int to) {
-  typedef PromptLds<D> L;
+__device__ __forceinline__ void store_keys(const KeyShare<D>& x, char* buf, int wave, int lane) {
   const int kt = lane >> 2, kp = lane & 3;
-  const int vq = lane >> 4, va = lane & 15;
 #pragma unroll
   for (int n = 0; n < D / 32; ++n) {
     half2v h[4];
     codes8(x.k[n], h);
-    const _Float16 s = x.ks[Share<D>::NS == 1 ? 0 : n / 4];
+    const _Float16 s = x.s[KeyShare<D>::NS == 1 ? 0 : n / 4];
 #pragma unroll
     for (int u = 0; u < 4; ++u) h[u] = h[u] * (half2v){s, s};
-    *reinterpret_cast<half8v*>(buf + (kp * (D / 32) + n) * L::KROW + (16 * wave + kt) * 16) = join8(h);
+    *reinterpret_cast<half8v*>(buf + (kp * (D / 32) + n) * PromptLds<D>::KROW + (16 * wave + kt) * 16) = join8(h);
   }
+}
+
+// [lo, to): tokens that some row of the tile sees; values of others may be
+// anything and become 0.
+template <int D>
+__device__ __forceinline__ void store_values(const ValueShare<D>& x, char* buf, int wave, int lane, int j0, int lo, int to) {
+  const int vq = lane >> 4, va = lane & 15;
   const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
-  half4v vs = __builtin_elementwise_max(x.vs, zero4);   // a poisoned token's NaN is in its score
+  half4v vs = __builtin_elementwise_max(x.s, zero4);    // a poisoned token's NaN is in its score
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const int j = j0 + 4 * vq + r;
-    if (j < lo || j >= to) vs[r] = (_Float16)0;
+    vs[r] = j < lo || j >= to ? (_Float16)0 : vs[r];
   }
   const half2v s01 = {vs[0], vs[1]}, s23 = {vs[2], vs[3]};
-  char* vb = buf + L::KEYS + (2 * wave + (vq & 1)) * (D * 16) + (vq >> 1) * 8;
+  char* vb = buf + (2 * wave + (vq & 1)) * (D * 16) + (vq >> 1) * 8;
 #pragma unroll
   for (int b = 0; b < D / 32; ++b) {
     half2v lo2[2], hi2[2];
@@ -146,15 +172,13 @@ __device__ __forceinline__ void store_share(const Share<D>& x, char* buf, int wa
   }
 }
 
-// QT: fp16 terms of a query (2 for fp16 queries, whose output shows the
-// rounding of one; 1 for bf16)
-template <int D, int QT>
-__global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv4AttnArgs p) {
+template <int D, int W>
+__global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv4AttnArgs p) {
   typedef PromptLds<D> L;
   constexpr int NC = D / 16, NB = D / 32;
   constexpr int LD = D + 4;
-  static_assert(kPromptWaves * 16 * LD * 4 <= 2 * L::BUF, "the output staging fits the buffers");
-  __shared__ __attribute__((aligned(16))) char lds[2 * L::BUF];
+  constexpr int LDS = W * 16 * LD * 4 > L::ALL ? W * 16 * LD * 4 : L::ALL;    // the output's way out needs less or a little more
+  __shared__ __attribute__((aligned(16))) char lds[LDS];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
@@ -162,13 +186,14 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
   int rest = blockIdx.x / p.c.heads;
   const int part = rest % p.nsplit;
   rest /= p.nsplit;
-  const int b = rest % p.batch;
-  const int tile = p.tiles - 1 - rest / p.batch;
+  const int b = rest / p.tiles;
+  const int tile = p.tiles - 1 - (rest - b * p.tiles);
   const Kv4Seq q(p, b);
-  const int row0 = tile * kPromptRows;
+  constexpr int ROWS = 32 * W;
+  const int row0 = tile * ROWS;
   if (row0 >= q.rows) return;
   // what the workgroup's rows see
-  const int row_end = row0 + kPromptRows < q.rows ? row0 + kPromptRows : q.rows;
+  const int row_end = row0 + ROWS < q.rows ? row0 + ROWS : q.rows;
   const int lo = q.lo(row0 / p.rep), hi = q.hi((row_end - 1) / p.rep);
   const int parts = kv4_part_count(lo, hi, p.chunk);
   if (part >= parts) return;
@@ -180,7 +205,6 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
   const bool any = wrow0 < q.rows;
   const int w_first = any ? wrow0 / p.rep : 0;
   const int w_last = any ? ((wrow0 + 31 < q.rows ? wrow0 + 31 : q.rows - 1) / p.rep) : 0;
-  const int w_lo = any ? q.lo(w_first) : 0, w_hi = any ? q.hi(w_last) : 0;
   const int all_lo = q.lo(w_last), all_hi = q.hi(w_first);
   const int row = wrow0 + n;
   const bool valid = row < q.rows;
@@ -188,7 +212,7 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
   const int my_lo = q.lo(n_mine), my_hi = valid ? q.hi(n_mine) : 0;
 
   // queries: lane (h, n) holds dims 16 c + 8 h + e of row n
-  half8v qf[QT][NC];
+  half8v qf[NC];
   float qs = p.scale * kLog2e;
   {
     constexpr int E = D / 2;
@@ -196,7 +220,7 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
     const int64_t at = (int64_t)(q.s0 + n_mine) * p.q_stride + (head * p.rep + (valid ? row - n_mine * p.rep : 0)) * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) {
-      if (valid) load_vec_any<8>(p.dtype, p.q, at + 16 * c + 8 * h, w + 8 * c);
+      if (valid) load_vec<kDtBf16, 8>(reinterpret_cast<const uint16_t*>(p.q) + at + 16 * c + 8 * h, w + 8 * c);
       else
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[8 * c + e] = 0.0f;
@@ -226,11 +250,7 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float y = ldexpf(w[8 * c + kOrder[e]], -ex);
-        qf[0][c][e] = (_Float16)y;
-        if (QT == 2) qf[QT - 1][c][e] = (_Float16)(y - (float)qf[0][c][e]);
-      }
+      for (int e = 0; e < 8; ++e) qf[c][e] = (_Float16)ldexpf(w[8 * c + kOrder[e]], -ex);
   }
 
   f32x16 acc[NB];
@@ -241,83 +261,116 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
   float m = -__builtin_inff(), l = 0.0f;
 
   const int32_t* table_row = p.table + (int64_t)b * p.width;
-  Share<D> x;
-  int cur = 0;
-  if (from < to) {
-    load_share<D>(p.c, table_row, head, from + 16 * wave, to - 1, lane, x);
-    store_share<D>(x, lds, wave, lane, from + 16 * wave, lo, to);
-    load_share<D>(p.c, table_row, head, from + kPromptTokens + 16 * wave, to - 1, lane, x);
-  }
-  __syncthreads();
-  for (int t0 = from; t0 < to; t0 += kPromptTokens) {
-    const char* buf = lds + cur * L::BUF;
-    if (t0 < w_hi && t0 + kPromptTokens > w_lo) {
-      // S^T of two 32-token blocks
-      f32x16 s[2];
+  char* const kbuf = lds;
+  char* const vbuf = lds + 2 * L::KEYS;
+  const int last = to - 1, blk = 16 * (wave & 3);
+  // of 8 waves four deal with the keys and four with the values
+  const bool does_k = W == 4 || wave < 4, does_v = W == 4 || wave >= 4;
+  auto scores = [&](const char* buf, f32x16* s) {
+#pragma unroll
+    for (int st = 0; st < 2; ++st)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) s[st][r] = 0.0f;
+    // the two blocks' sums in turn, so that neither waits for itself
+#pragma unroll
+    for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int st = 0; st < 2; ++st) {
-#pragma unroll
-        for (int r = 0; r < 16; ++r) s[st][r] = 0.0f;
-#pragma unroll
-        for (int c = 0; c < NC; ++c) {
-          const half8v a = *reinterpret_cast<const half8v*>(buf + (2 * c + h) * L::KROW + (32 * st + n) * 16);
-          if (QT == 2) s[st] = mma32(a, qf[QT - 1][c], s[st]);
-          s[st] = mma32(a, qf[0][c], s[st]);
-        }
+        const half8v a = *reinterpret_cast<const half8v*>(buf + (2 * c + h) * L::KROW + (32 * st + n) * 16);
+        s[st] = mma32(a, qf[c], s[st]);
       }
-      const int end = all_hi < to ? all_hi : to;
-      if (t0 < all_lo || t0 + kPromptTokens > end) {
-#pragma unroll
-        for (int st = 0; st < 2; ++st)
-#pragma unroll
-          for (int r = 0; r < 16; ++r) {
-            const int j = t0 + 32 * st + 8 * (r >> 2) + 4 * h + (r & 3);
-            if (j < my_lo || j >= my_hi || j >= to) s[st][r] = -__builtin_inff();
-          }
-      }
-      float mx = s[0][0];
-#pragma unroll
-      for (int st = 0; st < 2; ++st)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[st][r]);
-      mx *= qs;
-      if (__builtin_amdgcn_ballot_w64(mx > m + kMaxSlack)) {
-        const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-        const float mn = fmaxf(m, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
-        const float f = mn > m ? exp2f(m - mn) : 1.0f;
-        m = mn;
-        l *= f;
-#pragma unroll
-        for (int db = 0; db < NB; ++db) acc[db] *= f;
-      }
-      const float mu = m == -__builtin_inff() ? 0.0f : m;
+  };
+  // Scores of tile t + 1 are made while the softmax works on those of t; keys
+  // are a tile ahead of the values, in LDS and on their way.
+  KeyShare<D> xk;
+  ValueShare<D> xv;
+  f32x16 s[2];
+  if (from < to) {
+    auto at = [&](int t) { return place_of(p.c, table_row, head, from + t * kPromptTokens + blk, last); };
+    if (does_k) {
+      load_keys<D>(p.c, at(0), lane, xk);
+      store_keys<D>(xk, kbuf, wave & 3, lane);
+      load_keys<D>(p.c, at(1), lane, xk);
+      store_keys<D>(xk, kbuf + L::KEYS, wave & 3, lane);
+      load_keys<D>(p.c, at(2), lane, xk);
+    }
+    if (does_v) {
+      load_values<D>(p.c, at(0), lane, xv);
+      store_values<D>(xv, vbuf, wave & 3, lane, from + blk, lo, to);
+      load_values<D>(p.c, at(1), lane, xv);
+    }
+  }
+  __syncthreads();
+  if (from < to) scores(kbuf, s);
+  __syncthreads();
+  int cur = 0;
+  for (int t0 = from; t0 < to; t0 += kPromptTokens) {
+    const int end = all_hi < to ? all_hi : to;
+    if (t0 < all_lo || t0 + kPromptTokens > end) {
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          s[st][r] = __builtin_amdgcn_exp2f(fmaf(s[st][r], qs, -mu));
-          l += s[st][r];
+          const int j = t0 + 32 * st + 8 * (r >> 2) + 4 * h + (r & 3);
+          if (j < my_lo || j >= my_hi || j >= to) s[st][r] = -__builtin_inff();
         }
-      // O^T over four 16-token steps
+    }
+    float mx = s[0][0];
 #pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        half8v ph;
+    for (int st = 0; st < 2; ++st)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) ph[i] = (_Float16)s[t >> 1][8 * (t & 1) + i];
+      for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[st][r]);
+    mx *= qs;
+    if (__builtin_amdgcn_ballot_w64(mx > m + kMaxSlack)) {
+      const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
+      const float mn = fmaxf(m, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
+      const float f = mn > m ? exp2f(m - mn) : 1.0f;
+      m = mn;
+      l *= f;
 #pragma unroll
-        for (int db = 0; db < NB; ++db) {
-          const half8v a = *reinterpret_cast<const half8v*>(buf + L::KEYS + ((2 * t + h) * D + 32 * db + n) * 16);
-          acc[db] = mma32(a, ph, acc[db]);
-        }
+      for (int db = 0; db < NB; ++db) acc[db] *= f;
+    }
+    const float mu = m == -__builtin_inff() ? 0.0f : m;
+    // the places of what is loaded at the end of this turn, read early
+    const Place pk = place_of(p.c, table_row, head, t0 + 3 * kPromptTokens + blk, last);
+    const Place pv = place_of(p.c, table_row, head, t0 + 2 * kPromptTokens + blk, last);
+
+    // the next tile's scores, and this one's probabilities
+    f32x16 sn[2];
+    scores(kbuf + (cur ^ 1) * L::KEYS, sn);
+    half8v ph[4];
+    const half2v one2 = {(_Float16)1, (_Float16)1};
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int i = 0; i < 8; i += 2) {
+        const float e0 = __builtin_amdgcn_exp2f(fmaf(s[t >> 1][8 * (t & 1) + i], qs, -mu));
+        const float e1 = __builtin_amdgcn_exp2f(fmaf(s[t >> 1][8 * (t & 1) + i + 1], qs, -mu));
+        const half2v e = {(_Float16)e0, (_Float16)e1};
+        ph[t][i] = e[0];
+        ph[t][i + 1] = e[1];
+        l = __builtin_amdgcn_fdot2(e, one2, l, false);
       }
+
+    // O^T over four 16-token steps, and the next tiles' codes to LDS
+#pragma unroll
+    for (int t = 0; t < 4; ++t)
+#pragma unroll
+      for (int db = 0; db < NB; ++db) {
+        const half8v a = *reinterpret_cast<const half8v*>(vbuf + cur * L::VALUES + ((2 * t + h) * D + 32 * db + n) * 16);
+        acc[db] = mma32(a, ph[t], acc[db]);
+      }
+    if (does_k) {
+      store_keys<D>(xk, kbuf + cur * L::KEYS, wave & 3, lane);
+      load_keys<D>(p.c, pk, lane, xk);
     }
-    // the next tile: registers to the other buffer, the one after it to registers
-    const int t1 = t0 + kPromptTokens;
+    if (does_v) {
+      store_values<D>(xv, vbuf + (cur ^ 1) * L::VALUES, wave & 3, lane, t0 + kPromptTokens + blk, lo, to);
+      load_values<D>(p.c, pv, lane, xv);
+    }
+    s[0] = sn[0];
+    s[1] = sn[1];
     cur ^= 1;
-    if (t1 < to) {
-      store_share<D>(x, lds + cur * L::BUF, wave, lane, t1 + 16 * wave, lo, to);
-      load_share<D>(p.c, table_row, head, t1 + kPromptTokens + 16 * wave, to - 1, lane, x);
-    }
     __syncthreads();
   }
   {
@@ -361,25 +414,26 @@ __global__ __launch_bounds__(kPromptThreads, D == 256 ? 1 : 2) void kv4_prompt_k
         }
       } else {
         finish_row<D>(p.c.rotate, p.c.signs, lr, la, w);
-        if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, w);
+        if (store) store_vec<kDtBf16, NC>(reinterpret_cast<uint16_t*>(p.out) + out_row * D + la * NC, w);
       }
     }
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int D>
-static void prompt1(const Kv4AttnArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.groups), b(kPromptThreads);
-  if (a.dtype == kDtF16) hipLaunchKernelGGL((kv4_prompt_kernel<D, 2>), g, b, 0, s, a);
-  else hipLaunchKernelGGL((kv4_prompt_kernel<D, 1>), g, b, 0, s, a);
+template <int D, int W>
+static void prompt2(const Kv4AttnArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((kv4_prompt_kernel<D, W>), dim3((unsigned)a.groups), dim3(64 * W), 0, s, a);
 }
 
 void launch_kv4_prompt(const Kv4AttnArgs& a, hipStream_t s) {
   switch (a.c.dim) {
-    case 64: prompt1<64>(a, s); break;
-    case 128: prompt1<128>(a, s); break;
-    default: prompt1<256>(a, s); break;
+    case 64: prompt2<64, 4>(a, s); break;
+    case 128:
+      if (a.rows == 256) prompt2<128, 8>(a, s);
+      else prompt2<128, 4>(a, s);
+      break;
+    default: prompt2<256, 4>(a, s); break;
   }
 }
 
