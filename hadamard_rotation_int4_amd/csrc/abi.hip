@@ -588,6 +588,9 @@ static int32_t kv4_cache(const char* fn, const hr_kv4_cache* c, bool need, hr::K
   return HR_OK;
 }
 
+// Vectors of one call: a launch holds fewer than 2^32 threads.
+constexpr int64_t kKv4MaxVectors = int64_t(1) << 26;
+
 static bool kv4_dtype(int32_t dt) { return dt == HR_F32 || dt == HR_BF16 || dt == HR_F16; }
 
 // Rows `stride` elements apart: long enough and 16-byte aligned.
@@ -609,8 +612,8 @@ int32_t hr_kv4_append(const hr_kv4_cache* cache, const void* k, const void* v, i
   const int64_t row = (int64_t)cache->heads * cache->dim;
   if (!kv4_stride(k_stride, row, dtype) || !kv4_stride(v_stride, row, dtype))
     return fail(HR_EINVAL, "%s: k_stride and v_stride must be at least heads * dim and multiples of 16 bytes", fn);
-  if (tokens > INT32_MAX / cache->heads)
-    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^31 - 1", fn);
+  if (tokens > kKv4MaxVectors / cache->heads)
+    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^26", fn);
   if (tokens == 0 || cache->pages == 0) return ok();
   a.x[0] = k;
   a.x[1] = v;
@@ -633,8 +636,8 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
   if (tokens > 0 && (!k || !v || !slots)) return fail(HR_EINVAL, "%s: k, v and slots are required", fn);
   if (!aligned16(k) || !aligned16(v)) return fail(HR_EINVAL, "%s: k and v must be 16-byte aligned", fn);
   if (reinterpret_cast<uintptr_t>(slots) & 7u) return fail(HR_EINVAL, "%s: slots must be 8-byte aligned", fn);
-  if (tokens > INT32_MAX / cache->heads)
-    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^31 - 1", fn);
+  if (tokens > kKv4MaxVectors / cache->heads)
+    return fail(HR_EUNSUPPORTED, "%s: tokens * heads above 2^26", fn);
   if (tokens == 0) return ok();
   a.y[0] = k;
   a.y[1] = v;
@@ -695,8 +698,8 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
     return fail(HR_EINVAL, "%s: q_stride must be at least q_heads * dim and a multiple of 16 bytes", fn);
   if (!starts && (int64_t)batch * max_new != total)
     return fail(HR_EINVAL, "%s: without starts, total must be batch * max_new", fn);
-  if (total > INT32_MAX / q_heads || max_new > INT32_MAX / q_heads)
-    return fail(HR_EUNSUPPORTED, "%s: rows * q_heads above 2^31 - 1", fn);
+  if (total > kKv4MaxVectors / q_heads || max_new > kKv4MaxVectors / q_heads)
+    return fail(HR_EUNSUPPORTED, "%s: rows * q_heads above 2^26", fn);
   if (batch > 65535) return fail(HR_EUNSUPPORTED, "%s: batch=%d above 65535", fn, batch);
   if (max_len > hr::kKv4MaxLen) return fail(HR_EUNSUPPORTED, "%s: max_len above 2^30", fn);
   if (!some || max_new == 0) return ok();
@@ -718,7 +721,7 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
   a.window = window;
   a.out = out;
   hr::kv4_attention_plan(&a);
-  if (a.groups > INT32_MAX / 2)
+  if (a.groups > (1 << 22))
     return fail(HR_EUNSUPPORTED, "%s: too many rows for one launch", fn);
   const int64_t need = kv4_workspace(a);
   if (need > 0) {

@@ -594,10 +594,11 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
     const int n2 = store ? r2 / p.rep : 0;
     const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
     if (parts > 1 && p.nsplit > 1) {
-      if (!store) continue;
-      const int64_t at = out_row * p.nsplit + part;
-      store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, y);
-      if (la == 0) p.part_ml[at] = make_float2(mt, l);
+      if (store) {
+        const int64_t at = out_row * p.nsplit + part;
+        store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, y);
+        if (la == 0) p.part_ml[at] = make_float2(mt, l);
+      }
     } else {
       finish_row<D>(p.c.rotate, p.c.signs, l, la, y);
       if (store) store_vec_any<NC>(p.dtype, p.out, out_row * D + la * NC, y);
@@ -621,7 +622,7 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
   const int at_row = blockIdx.x * (16 / GROUPS) + (threadIdx.x >> 4) / GROUPS;
   const int n = at_row / p.q_heads, q_head = at_row - n * p.q_heads;
   const Kv4Seq q(p, b);
-  const bool valid = n < q.news;
+  const bool valid = n < q.news && n < p.max_new;
   const int64_t out_row = (int64_t)(q.s0 + (valid ? n : 0)) * p.q_heads + q_head;
   // its row tile's parts (with one, the row is finished)
   int parts = 1;

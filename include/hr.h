@@ -528,6 +528,7 @@ typedef struct {
  *             heads * dim; a multiple of 16 bytes).
  *   slots     [tokens] int64, all different; a slot outside
  *             [0, pages * page) writes nothing.
+ *   tokens * heads is at most 2^26.
  */
 int32_t hr_kv4_append(const hr_kv4_cache* cache, const void* k, const void* v, int32_t dtype, int64_t k_stride,
                       int64_t v_stride, const int64_t* slots, int64_t tokens, void* stream);
@@ -539,6 +540,7 @@ int32_t hr_kv4_append(const hr_kv4_cache* cache, const void* k, const void* v, i
  *
  *   slots     [tokens] int64; a slot outside [0, pages * page) reads zeros.
  *   k, v      [tokens][heads][dim] of dtype (HR_F32, HR_BF16 or HR_F16).
+ *   tokens * heads is at most 2^26.
  */
 int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tokens, int32_t dtype, void* k,
                     void* v, void* stream);
@@ -564,7 +566,7 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  *   table     [batch][width] int32 page ids; only entries of cached tokens are
  *             used.  An id outside [0, pages) is read as 0.
  *   lens      [batch] int32 (device), at most width * page.
- *   q_heads   a multiple of heads.
+ *   q_heads   a multiple of heads; total * q_heads is at most 2^26.
  *   max_new, max_len  upper bounds of a sequence's query rows and cached
  *             length, for the launch; rows past max_new are not computed.  A
  *             max_len below a sequence's length costs time only.
