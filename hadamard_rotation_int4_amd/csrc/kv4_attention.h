@@ -103,21 +103,27 @@ __device__ __forceinline__ int row_exponent(float mx) {
 }
 
 // An output row's last steps, 16 lanes a row with dims [a D/16, (a + 1) D/16):
-// divide by the softmax sum (0 where nothing was seen), rotate back.
+// times a weight (1 / the softmax sum), rotated back.
+template <int D>
+__device__ __forceinline__ void turn_back(int rotate, const int8_t* signs, float weight, int a, float* w) {
+  constexpr int NC = D / 16;
+  if (!rotate) {
+#pragma unroll
+    for (int e = 0; e < NC; ++e) w[e] *= weight;
+    return;
+  }
+  fwht_lanes<NC, 16>(w, a);
+  const float f = weight * kv4_norm<D>() * kv4_tau(a);
+  uint32_t sg[NC];
+  load_signs<NC>(signs, a * NC, sg);
+#pragma unroll
+  for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * f, sg[e]);
+}
+
+// The same from the softmax sum; 0 where nothing was seen.
 template <int D>
 __device__ __forceinline__ void finish_row(int rotate, const int8_t* signs, float l, int a, float* w) {
-  constexpr int NC = D / 16;
-  const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-#pragma unroll
-  for (int e = 0; e < NC; ++e) w[e] *= inv;
-  if (rotate) {
-    fwht_lanes<NC, 16>(w, a);
-    const float nf = kv4_norm<D>() * kv4_tau(a);
-    uint32_t sg[NC];
-    load_signs<NC>(signs, a * NC, sg);
-#pragma unroll
-    for (int e = 0; e < NC; ++e) w[e] = flip(w[e] * nf, sg[e]);
-  }
+  turn_back<D>(rotate, signs, l == 0.0f ? 0.0f : 1.0f / l, a, w);
 }
 
 }  // namespace hr

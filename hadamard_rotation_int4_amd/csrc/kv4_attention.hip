@@ -228,7 +228,8 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
   static_assert(RT * TERMS * QP * 2 <= kAttnWaves * LD * 4, "the queries fit the exchange");
   uint16_t* q_lds = reinterpret_cast<uint16_t*>(o_lds);
   float qf[RT];
-  int my_lo[RT], my_hi[RT];
+  int my_lo[RT];
+  unsigned my_span[RT];        // the row's tokens: [my_lo, my_lo + my_span)
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     const int qrow = threadIdx.x >> 4;
@@ -300,7 +301,8 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
     const int mine = row0 + 16 * rt + i;
     const int n_mine = (mine < q.rows ? mine : q.rows - 1) / p.rep;
     my_lo[rt] = q.lo(n_mine);
-    my_hi[rt] = q.hi(n_mine);
+    const int my_end = q.hi(n_mine) < to ? q.hi(n_mine) : to;
+    my_span[rt] = my_end > my_lo[rt] ? my_end - my_lo[rt] : 0;
   }
   __syncthreads();
   half8v qh[MODE == kF32 ? 1 : RT][QT][NK];
@@ -443,7 +445,7 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const int j = t0 + 16 * (u >> 2) + 4 * g + (u & 3);
-          if (j < my_lo[rt] || j >= my_hi[rt] || j >= to) z[u] = -__builtin_inff();
+          z[u] = (unsigned)(j - my_lo[rt]) < my_span[rt] ? z[u] : -__builtin_inff();
         }
       }
       float mx = z[0];

@@ -64,24 +64,26 @@ struct ValueShare {
   half4v s;
 };
 
-// Token block and codes' place of token j, a multiple of 16; past the last
-// token any block of the sequence (it is masked).
+// Where the codes (bytes) and scales (elements) of the 16 tokens from token j, a
+// multiple of 16, start in either of the cache's arrays; past the last token,
+// any block of the sequence (it is masked).
 struct Place {
-  int64_t block;
-  int off;
+  int64_t codes, scales;
 };
+template <int D>
 __device__ __forceinline__ Place place_of(const Kv4Cache& c, const int32_t* table_row, int head, int j, int last) {
   if (j > last) j = last & ~15;
   int id = read_index(table_row, j >> c.page_log2);
   if ((unsigned)id >= (unsigned)c.pages) id = 0;
-  return {(int64_t)id * c.heads + head, j & ((1 << c.page_log2) - 1)};
+  const int off = j & ((1 << c.page_log2) - 1);
+  const int64_t block = (int64_t)id * c.heads + head;
+  return {((block << c.page_log2) + off) * (D / 2), ((block * (D / c.group)) << c.page_log2) + off};
 }
 
 template <int D>
 __device__ __forceinline__ void load_keys(const Kv4Cache& c, Place at, int lane, KeyShare<D>& x) {
-  const int sh = c.page_log2;
   const int kt = lane >> 2, kp = lane & 3;              // token of the block, quarter
-  const uint8_t* kk = c.codes[0] + ((at.block << sh) + at.off) * (D / 2) + (kt * (D / 2) + kp * (D / 8));
+  const uint8_t* kk = c.codes[0] + at.codes + (kt * (D / 2) + kp * (D / 8));
   if (D == 64) {
     const uint2 r = *reinterpret_cast<const uint2*>(kk);
     x.k[0] = r.x;
@@ -94,16 +96,15 @@ __device__ __forceinline__ void load_keys(const Kv4Cache& c, Place at, int lane,
       for (int e = 0; e < 4; ++e) x.k[4 * n + e] = r[e];
     }
   }
-  const _Float16* sc = c.scales[0] + ((at.block * (D / c.group)) << sh) + at.off;
+  const _Float16* sc = c.scales[0] + at.scales;
 #pragma unroll
-  for (int n = 0; n < KeyShare<D>::NS; ++n) x.s[n] = sc[(((kp * (D / 4) + 32 * n) / c.group) << sh) + kt];
+  for (int n = 0; n < KeyShare<D>::NS; ++n) x.s[n] = sc[(((kp * (D / 4) + 32 * n) / c.group) << c.page_log2) + kt];
 }
 
 template <int D>
 __device__ __forceinline__ void load_values(const Kv4Cache& c, Place at, int lane, ValueShare<D>& x) {
-  const int sh = c.page_log2;
   const int vq = lane >> 4, va = lane & 15;             // token quad of the block, dims
-  const uint8_t* vc = c.codes[1] + ((at.block << sh) + at.off) * (D / 2) + (4 * vq * (D / 2) + va * (D / 32));
+  const uint8_t* vc = c.codes[1] + at.codes + (4 * vq * (D / 2) + va * (D / 32));
 #pragma unroll
   for (int r = 0; r < 4; ++r) {
     const uint8_t* vv = vc + r * (D / 2);
@@ -117,8 +118,7 @@ __device__ __forceinline__ void load_values(const Kv4Cache& c, Place at, int lan
       x.v[r][ValueShare<D>::NV - 1] = u.y;
     }
   }
-  x.s = *reinterpret_cast<const half4v*>(c.scales[1] + ((at.block * (D / c.group)) << sh) + at.off +
-                                         ((va * (D / 16) / c.group) << sh) + 4 * vq);
+  x.s = *reinterpret_cast<const half4v*>(c.scales[1] + at.scales + ((va * (D / 16) / c.group) << c.page_log2) + 4 * vq);
 }
 
 template <int D>
@@ -209,7 +209,33 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   const int row = wrow0 + n;
   const bool valid = row < q.rows;
   const int n_mine = valid ? row / p.rep : w_last;
-  const int my_lo = q.lo(n_mine), my_hi = valid ? q.hi(n_mine) : 0;
+  const int my_lo = q.lo(n_mine), my_end = valid ? (q.hi(n_mine) < to ? q.hi(n_mine) : to) : 0;
+  const unsigned my_span = my_end > my_lo ? my_end - my_lo : 0;
+
+  const int32_t* table_row = p.table + (int64_t)b * p.width;
+  char* const kbuf = lds;
+  char* const vbuf = lds + 2 * L::KEYS;
+  const int last = to - 1, blk = 16 * (wave & 3);
+  // of 8 waves four deal with the keys and four with the values
+  const bool does_k = W == 4 || wave < 4, does_v = W == 4 || wave >= 4;
+  // the first tiles set out before the queries are dealt with
+  KeyShare<D> xk0, xk1, xk;
+  ValueShare<D> xv0, xv;
+  Place ahead = {0, 0};          // of the tile whose keys were asked for last
+  if (from < to) {
+    const Place p0 = place_of<D>(p.c, table_row, head, from + blk, last);
+    const Place p1 = place_of<D>(p.c, table_row, head, from + kPromptTokens + blk, last);
+    ahead = place_of<D>(p.c, table_row, head, from + 2 * kPromptTokens + blk, last);
+    if (does_k) {
+      load_keys<D>(p.c, p0, lane, xk0);
+      load_keys<D>(p.c, p1, lane, xk1);
+      load_keys<D>(p.c, ahead, lane, xk);
+    }
+    if (does_v) {
+      load_values<D>(p.c, p0, lane, xv0);
+      load_values<D>(p.c, p1, lane, xv);
+    }
+  }
 
   // queries: lane (h, n) holds dims 16 c + 8 h + e of row n
   half8v qf[NC];
@@ -260,12 +286,6 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     for (int r = 0; r < 16; ++r) acc[db][r] = 0.0f;
   float m = -__builtin_inff(), l = 0.0f;
 
-  const int32_t* table_row = p.table + (int64_t)b * p.width;
-  char* const kbuf = lds;
-  char* const vbuf = lds + 2 * L::KEYS;
-  const int last = to - 1, blk = 16 * (wave & 3);
-  // of 8 waves four deal with the keys and four with the values
-  const bool does_k = W == 4 || wave < 4, does_v = W == 4 || wave >= 4;
   auto scores = [&](const char* buf, f32x16* s) {
 #pragma unroll
     for (int st = 0; st < 2; ++st)
@@ -282,23 +302,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   };
   // Scores of tile t + 1 are made while the softmax works on those of t; keys
   // are a tile ahead of the values, in LDS and on their way.
-  KeyShare<D> xk;
-  ValueShare<D> xv;
   f32x16 s[2];
   if (from < to) {
-    auto at = [&](int t) { return place_of(p.c, table_row, head, from + t * kPromptTokens + blk, last); };
     if (does_k) {
-      load_keys<D>(p.c, at(0), lane, xk);
-      store_keys<D>(xk, kbuf, wave & 3, lane);
-      load_keys<D>(p.c, at(1), lane, xk);
-      store_keys<D>(xk, kbuf + L::KEYS, wave & 3, lane);
-      load_keys<D>(p.c, at(2), lane, xk);
+      store_keys<D>(xk0, kbuf, wave & 3, lane);
+      store_keys<D>(xk1, kbuf + L::KEYS, wave & 3, lane);
     }
-    if (does_v) {
-      load_values<D>(p.c, at(0), lane, xv);
-      store_values<D>(xv, vbuf, wave & 3, lane, from + blk, lo, to);
-      load_values<D>(p.c, at(1), lane, xv);
-    }
+    if (does_v) store_values<D>(xv0, vbuf, wave & 3, lane, from + blk, lo, to);
   }
   __syncthreads();
   if (from < to) scores(kbuf, s);
@@ -307,12 +317,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   for (int t0 = from; t0 < to; t0 += kPromptTokens) {
     const int end = all_hi < to ? all_hi : to;
     if (t0 < all_lo || t0 + kPromptTokens > end) {
+      // tokens [my_lo, my_lo + my_span) by one comparison
+      const int t4 = t0 + 4 * h - my_lo;
 #pragma unroll
       for (int st = 0; st < 2; ++st)
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const int j = t0 + 32 * st + 8 * (r >> 2) + 4 * h + (r & 3);
-          if (j < my_lo || j >= my_hi || j >= to) s[st][r] = -__builtin_inff();
+          const unsigned j = (unsigned)(t4 + (32 * st + 8 * (r >> 2) + (r & 3)));
+          s[st][r] = j < my_span ? s[st][r] : -__builtin_inff();
         }
     }
     float mx = s[0][0];
@@ -331,9 +343,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
       for (int db = 0; db < NB; ++db) acc[db] *= f;
     }
     const float mu = m == -__builtin_inff() ? 0.0f : m;
-    // the places of what is loaded at the end of this turn, read early
-    const Place pk = place_of(p.c, table_row, head, t0 + 3 * kPromptTokens + blk, last);
-    const Place pv = place_of(p.c, table_row, head, t0 + 2 * kPromptTokens + blk, last);
+    // what is asked for at the end of this turn; its page id is read early
+    const Place pv = ahead;
+    ahead = place_of<D>(p.c, table_row, head, t0 + 3 * kPromptTokens + blk, last);
 
     // the next tile's scores, and this one's probabilities
     f32x16 sn[2];
@@ -362,7 +374,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
       }
     if (does_k) {
       store_keys<D>(xk, kbuf + cur * L::KEYS, wave & 3, lane);
-      load_keys<D>(p.c, pk, lane, xk);
+      load_keys<D>(p.c, ahead, lane, xk);
     }
     if (does_v) {
       store_values<D>(xv, vbuf + (cur ^ 1) * L::VALUES, wave & 3, lane, t0 + kPromptTokens + blk, lo, to);
@@ -377,6 +389,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
+  const bool is_part = parts > 1 && p.nsplit > 1;
+  const float weight = is_part ? l : l == 0.0f ? 0.0f : 1.0f / l;
 
   // output: 16 rows at a time through the wave's own piece of LDS
   float* o_lds = reinterpret_cast<float*>(lds) + wave * 16 * LD;
@@ -401,19 +415,19 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
       float w[NC];
       load_vec<kDtF32, NC>(o_lds + r16 * LD + la * NC, w);
       const int from_lane = 16 * half + r16;
-      const float lr = __shfl(l, from_lane, 64), mr = __shfl(m, from_lane, 64);
+      const float lr = __shfl(weight, from_lane, 64), mr = __shfl(m, from_lane, 64);
       const int r2 = wrow0 + 16 * half + r16;
       const bool store = r2 < q.rows;
       const int n2 = store ? r2 / p.rep : 0;
       const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
-      if (parts > 1 && p.nsplit > 1) {
+      if (is_part) {
         if (store) {
           const int64_t at = out_row * p.nsplit + part;
           store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, w);
           if (la == 0) p.part_ml[at] = make_float2(mr, lr);
         }
       } else {
-        finish_row<D>(p.c.rotate, p.c.signs, lr, la, w);
+        turn_back<D>(p.c.rotate, p.c.signs, lr, la, w);
         if (store) store_vec<kDtBf16, NC>(reinterpret_cast<uint16_t*>(p.out) + out_row * D + la * NC, w);
       }
     }
