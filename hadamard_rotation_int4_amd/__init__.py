@@ -14,6 +14,7 @@ library built from other sources, raises ImportError.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
@@ -683,6 +684,7 @@ def kv4_cache(pages: int, heads: int, dim: int, page: int = 64, group: int | Non
 
 
 _KV4_TYPES = {torch.bfloat16: HR_BF16, torch.float16: HR_F16, torch.float32: HR_F32}
+_ANY_2D = (-1, -1)
 _KV4_BYTES = {torch.bfloat16: 2, torch.float16: 2, torch.float32: 4}
 
 # A decode step makes a few of these calls for every layer, and with few tokens
@@ -698,18 +700,22 @@ def _kv4_stream(cache) -> int:
 
 def _kv4_ptr(cache, t, name: str) -> int:
     """Device pointer of a tensor that a call on `cache` takes."""
-    if t.device != cache.device:
+    if t.get_device() != cache._index:
         if not t.is_cuda:
             raise ValueError(f"{name}: tensor must live on the GPU")
         raise ValueError(f"{name}: on {t.device}, expected {cache.device}")
     return t.data_ptr()
 
 
+# A size of sizes: step after step asks for the same.
+@functools.lru_cache(maxsize=256)
+def _kv4_workspace(*sizes) -> int:
+    return lib.hr_kv4_attention_workspace(*sizes)
+
+
 def _kv4_rows(cache, t, name: str):
     """Check token rows [tokens][heads][dim] whose tokens may be strided (slices
     of a fused projection); returns (tokens, heads, row stride, dtype)."""
-    if not isinstance(cache, KV4Cache):
-        raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
     dtype = t.dtype
@@ -734,10 +740,10 @@ def _kv4_index(t, name: str, dtype, shape):
     """Check an index tensor: dtype, shape (any size where negative), contiguous."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name}: dtype {t.dtype} not in {[_DT_NAME[dtype]]}")
     got = t.shape
-    if got != shape and (len(got) != len(shape) or any(w >= 0 and v != w for v, w in zip(got, shape))):
+    if got != shape and (len(got) != len(shape) or any(v != w for v, w in zip(got, shape) if w >= 0)):
         raise ValueError(f"{name}: shape {tuple(got)}, expected {tuple('any' if w < 0 else w for w in shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: tensor must be contiguous")
@@ -748,11 +754,13 @@ def kv4_append(cache: KV4Cache, k: torch.Tensor, v: torch.Tensor, slots: torch.T
     [heads][dim] bf16, fp16 or fp32, of one dtype, tokens may be strided; slots:
     int64 [tokens], page * cache.page + place, all different, a slot outside the
     cache writes nothing."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
     tokens, heads, ks, dtype = _kv4_rows(cache, k, "k")
     vt, vh, vs, vdtype = _kv4_rows(cache, v, "v")
     if heads != cache.heads or vh != heads:
         raise ValueError(f"k, v: {heads} and {vh} heads, but the cache has {cache.heads}")
-    if vdtype != dtype:
+    if vdtype is not dtype:
         raise TypeError(f"v: dtype {vdtype} not in {[_DT_NAME[dtype]]}")
     if vt != tokens:
         raise ValueError(f"v: {vt} tokens, but k has {tokens}")
@@ -802,8 +810,10 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     kept by a caller that captures the call in a graph; allocated when None.
     Returns out [total][q_heads][dim] of q's dtype, 0 in a row that sees no
     token."""
+    if not isinstance(cache, KV4Cache):
+        raise TypeError(f"cache: expected a KV4Cache, got {type(cache).__name__}")
     total, q_heads, step, dtype = _kv4_rows(cache, q, "q")
-    _kv4_index(table, "table", torch.int32, (-1, -1))
+    _kv4_index(table, "table", torch.int32, _ANY_2D)
     batch, width = table.shape
     _kv4_index(lens, "lens", torch.int32, (batch,))
     if starts is not None:
@@ -815,7 +825,7 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     if scale is None:
         scale = cache.dim ** -0.5
     code = _KV4_TYPES[dtype]
-    need = lib.hr_kv4_attention_workspace(cache.heads, cache.dim, code, total, batch, q_heads, max_new, max_len, window)
+    need = _kv4_workspace(cache.heads, cache.dim, code, total, batch, q_heads, max_new, max_len, window)
     if out is not None:
         _arg(out, "out", dtype, (total, q_heads, cache.dim))
     if workspace is not None:
@@ -823,7 +833,7 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
         if workspace.shape[0] < need:
             raise ValueError(f"workspace: {workspace.shape[0]} bytes, {need} needed")
     if out is None:
-        out = torch.empty((total, q_heads, cache.dim), dtype=dtype, device=cache.device)
+        out = torch.empty_like(q)          # contiguous: q is, or is not dense
     if workspace is None and need:
         workspace = torch.empty(need, dtype=torch.uint8, device=cache.device)
     st = lib.hr_kv4_attention(
