@@ -27,6 +27,7 @@ namespace hr {
 
 constexpr int kKv4Threads = 256;
 constexpr int kKv4Waves = kKv4Threads / 64;
+constexpr float kMaxScale = 9352.0f;     // 7 of these are an fp16 number
 
 // Group absmax over the group's lanes (non-negative floats and NaN compare as
 // integers, NaN above all).
@@ -66,7 +67,7 @@ __device__ __forceinline__ void quantize_pair(float* w, int a, int group, int la
     float s32 = div7(ROT ? am * kv4_norm<D>() : am);
     asm("" : "+v"(s32));       // rounded to fp32 before fp16: a mixed-precision fma would round once
     s16[kv] = (_Float16)s32;
-    bad |= !((float)s16[kv] < __builtin_inff()) || z != z;
+    bad |= !((float)s16[kv] <= kMaxScale) || z != z;
   }
   const uint64_t bads = __builtin_amdgcn_ballot_w64(bad);
   const uint64_t mine = (L == 64 ? ~0ull : (1ull << L) - 1) << (lane & ~(L - 1));

@@ -59,10 +59,6 @@ __device__ __forceinline__ int kv4_part_count(int lo, int hi, int chunk) {
 __device__ __forceinline__ f32x4 mma(half8v a, half8v b, f32x4 c) {
   return __builtin_amdgcn_mfma_f32_16x16x32_f16(a, b, c, 0, 0, 0);
 }
-__device__ __forceinline__ f32x4 mma(bf16x8v a, bf16x8v b, f32x4 c) {
-  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-}
-
 // nibbles 0 and 4 (low half, high half) of x as codes in fp16; x's nibbles are two's complement
 __device__ __forceinline__ half2v codes_lo(uint32_t x) {
   const half2v h = __builtin_bit_cast(half2v, (x & 0x000F000Fu) ^ 0x64086408u);     // 1024 + 8 + q

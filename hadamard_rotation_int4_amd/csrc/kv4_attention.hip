@@ -36,9 +36,12 @@
 // The running maximum moves only when some score passes it by 2^8, so most
 // tiles need neither the exchange between lanes nor the rescale.
 //
-// fp32 queries: every operand as a sum of bf16 terms (the queries and
-// probabilities three, the scaled codes two, which hold them exactly), all
-// products above 2^-24 of the whole kept.
+// fp16 outputs would show the rounding of the queries and keys (4.5e-4 and 4e-4
+// rms of an output, where its own is 2.1e-4): for fp16 queries these are two
+// fp16 terms each, queries always, keys and values where several groups make a
+// scaled code more than 11 bits (two terms hold it exactly).  fp32 queries do
+// the same, and probabilities in two terms too, lifted by 2^11 so that small
+// ones keep their bits: all products above 2^-22 of the whole are there.
 //
 // Rows of parts are joined by kv4_join_kernel, in the order of the parts.
 #include "kv4_attention.h"
@@ -49,15 +52,15 @@ constexpr int kAttnThreads = 256;
 constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kFewParts = 8;
 
-// modes: one group a head / several, 16-bit queries; fp32 queries
-enum { kOneGroup = 0, kGroups = 1, kF32 = 2 };
+// what the fp16 operands have to hold: enough for bf16, fp16 or fp32 outputs
+enum { kForBf16 = 0, kForF16 = 1, kForF32 = 2 };
 
 // Waves a SIMD the registers are kept for.  At two or more the compiler takes
 // at most 256 registers and leaves the accumulators among the ordinary ones
 // (with more it moves them to and from the accumulation registers, 112 moves a
 // tile).
-constexpr int kv4_attn_waves(int dim, int mode, int rows) {
-  return dim == 256 ? (mode == kF32 ? 1 : 2) : mode == kF32 || rows > 16 ? 2 : 3;
+constexpr int kv4_attn_waves(int dim, bool groups, int rows, int prec) {
+  return dim == 256 || rows > 16 || (dim == 128 && (prec == kForF32 || (groups && prec == kForF16))) ? 2 : 3;
 }
 // Smallest exponent of the unit of value scales: its reciprocal is an fp16 number.
 constexpr int kMinScaleExp = -15;
@@ -70,22 +73,12 @@ __device__ __forceinline__ float max_over_g(float v) {
   return fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1]));
 }
 
-// x as a sum of bf16 terms
-template <int N>
-__device__ __forceinline__ void bf16_terms(float x, __bf16* t) {
-#pragma unroll
-  for (int i = 0; i < N; ++i) {
-    t[i] = (__bf16)x;
-    x -= (float)t[i];
-  }
-}
-
 // the codes and scales of one 32-token tile, as one lane holds them
-template <int D, int MODE>
+template <int D, bool GROUPS>
 struct Tile {
   static constexpr int NK = D / 32;                       // key dwords a token
   static constexpr int NB = D / 32;                       // value bytes a token
-  static constexpr int NS = MODE == kOneGroup ? 1 : D / 128 > 0 ? D / 128 : 1;   // 32-dim spans with scales of their own
+  static constexpr int NS = GROUPS && D == 256 ? 2 : 1;   // 32-dim spans with scales of their own
   uint32_t k[2][NK];
   uint32_t v[8][(NB + 3) / 4];
   half4v ks4[2];                                          // one group: tokens 4 g + r
@@ -107,13 +100,13 @@ __device__ __forceinline__ Ids load_ids(const Kv4Cache& c, const int32_t* table_
   return r;
 }
 
-template <int D, int MODE>
+template <int D, bool GROUPS>
 __device__ __forceinline__ void load_block(const Kv4Cache& c, int64_t block, int off, int t, int plus, int g, int i,
-                                           Tile<D, MODE>& x) {
+                                           Tile<D, GROUPS>& x) {
   // (block, off) and `plus` tokens, the part that is a constant of the load instructions
   const int sh = c.page_log2;
   const int64_t cb = ((block << sh) + off) * (D / 2);
-  const int ng = MODE == kOneGroup ? 1 : D / c.group;
+  const int ng = GROUPS ? D / c.group : 1;
   const int64_t sb = ((block * ng) << sh) + off;
   const uint8_t* kp = c.codes[0] + cb + (i * (D / 2) + g * (D / 8)) + plus * (D / 2);
   const uint8_t* vp = c.codes[1] + cb + (4 * g * (D / 2) + i * (D / 32)) + plus * (D / 2);
@@ -144,43 +137,46 @@ __device__ __forceinline__ void load_block(const Kv4Cache& c, int64_t block, int
   }
   const _Float16* ks = c.scales[0] + sb;
   const _Float16* vs = c.scales[1] + sb;
-  if (MODE == kOneGroup) {
+  if (!GROUPS) {
     x.ks4[t] = *reinterpret_cast<const half4v*>(ks + 4 * g + plus);
     x.vs[t] = *reinterpret_cast<const half4v*>(vs + 4 * g + plus);
   } else {
 #pragma unroll
-    for (int n = 0; n < Tile<D, MODE>::NS; ++n) x.ks1[n][t] = ks[(((g * (D / 4) + 32 * n) / c.group) << sh) + i + plus];
+    for (int n = 0; n < Tile<D, GROUPS>::NS; ++n) x.ks1[n][t] = ks[(((g * (D / 4) + 32 * n) / c.group) << sh) + i + plus];
     x.vs[t] = *reinterpret_cast<const half4v*>(vs + ((i * (D / 16) / c.group) << sh) + 4 * g + plus);
   }
 }
 
-template <int D, int MODE>
+template <int D, bool GROUPS>
 __device__ __forceinline__ void load_tile(const Kv4Cache& c, Ids ids, int head, int t0, int last, int g, int i,
-                                          Tile<D, MODE>& x) {
+                                          Tile<D, GROUPS>& x) {
   const int pmask = (1 << c.page_log2) - 1;
   const int j = t0 > last ? last & ~31 : t0;
   const int id0 = (unsigned)ids.id[0] < (unsigned)c.pages ? ids.id[0] : 0;
   const int64_t block = (int64_t)id0 * c.heads + head;
   const int off = j & pmask;
-  load_block<D, MODE>(c, block, off, 0, 0, g, i, x);
+  load_block<D, GROUPS>(c, block, off, 0, 0, g, i, x);
   if (c.page_log2 >= 5) {          // the tile lies in one page
-    load_block<D, MODE>(c, block, off, 1, 16, g, i, x);
+    load_block<D, GROUPS>(c, block, off, 1, 16, g, i, x);
   } else {
     const int id1 = (unsigned)ids.id[1] < (unsigned)c.pages ? ids.id[1] : 0;
-    load_block<D, MODE>(c, (int64_t)id1 * c.heads + head, 0, 1, 0, g, i, x);
+    load_block<D, GROUPS>(c, (int64_t)id1 * c.heads + head, 0, 1, 0, g, i, x);
   }
 }
 
-// ROWS query rows a workgroup (16 or 32); FINE: fp16 queries, whose output's own
-// rounding is small enough to show that of an fp16 query, key or value
-template <int D, int MODE, bool FINE, int ROWS>
-__global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void kv4_attn_kernel(Kv4AttnArgs p) {
+// GROUPS: several scale groups a head; PREC: what the outputs can show; ROWS
+// query rows a workgroup (16 or 32)
+template <int D, bool GROUPS, int PREC, int ROWS>
+__global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv4_attn_kernel(Kv4AttnArgs p) {
   constexpr int NK = D / 32;             // matrix instructions over the dims
   constexpr int NC = D / 16;             // 16-dim slices of the output
   constexpr int LD = D + 4;              // row pitch of the exchange
   constexpr int RT = ROWS / 16;
-  constexpr int QT = FINE ? 2 : 1;       // fp16 terms of a query
-  typedef Tile<D, MODE> T;
+  constexpr int QT = PREC == kForBf16 ? 1 : 2;     // fp16 terms of a query, and of a scaled code
+  constexpr int PT = PREC == kForF32 ? 2 : 1;      // of a probability
+  // log2 units the scores may pass the running maximum by, and what the probabilities are lifted by
+  constexpr float SLACK = PREC == kForF32 ? 4.0f : 8.0f, LIFT = PREC == kForF32 ? 11.0f : 0.0f;
+  typedef Tile<D, GROUPS> T;
   __shared__ float o_lds[kAttnWaves][16][LD];
   __shared__ float m_lds[kAttnWaves][16], l_lds[kAttnWaves][16];
   const int lane = threadIdx.x & 63;
@@ -218,14 +214,13 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
   if (some) {
     ids = load_ids(p.c, table_row, t0, last);
     ids1 = load_ids(p.c, table_row, t0 + STEP, last);
-    load_tile<D, MODE>(p.c, ids, head, t0, last, g, i, x0);
+    load_tile<D, GROUPS>(p.c, ids, head, t0, last, g, i, x0);
   }
 
   // queries, 16 lanes a row as in the output: rotate, scale to [1, 2) by a power of two (kept in qf), round, and
   // through LDS into the right operand's layout
   constexpr int QP = D + 8;              // row pitch, 16-bit elements
-  constexpr int TERMS = MODE == kF32 ? 3 : QT;
-  static_assert(RT * TERMS * QP * 2 <= kAttnWaves * LD * 4, "the queries fit the exchange");
+  static_assert(RT * QT * QP * 2 <= kAttnWaves * LD * 4, "the queries fit the exchange");
   uint16_t* q_lds = reinterpret_cast<uint16_t*>(o_lds);
   float qf[RT];
   int my_lo[RT];
@@ -253,38 +248,29 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
 #pragma unroll
       for (int e = 0; e < NC; ++e) w[e] *= nf;
     }
-    int ex = 0;
-    if (MODE != kF32) {
-      float mx = 0.0f;
+    float mx = 0.0f;
 #pragma unroll
-      for (int e = 0; e < NC; ++e) mx = fmaxf(mx, fabsf(w[e]));
-      uint32_t u = umax_dpp<kQuadXor1>(__float_as_uint(mx));
-      u = umax_dpp<kQuadXor2>(u);
-      u = umax_dpp<kRowHalfMirror>(u);
-      ex = row_exponent(__uint_as_float(umax_dpp<kRowMirror>(u)));
-    }
+    for (int e = 0; e < NC; ++e) mx = fmaxf(mx, fabsf(w[e]));
+    uint32_t u = umax_dpp<kQuadXor1>(__float_as_uint(mx));
+    u = umax_dpp<kQuadXor2>(u);
+    u = umax_dpp<kRowHalfMirror>(u);
+    const int ex = row_exponent(__uint_as_float(umax_dpp<kRowMirror>(u)));
     if ((lane & 15) == 0) l_lds[rt][qrow] = ldexpf(p.scale * kLog2e, ex);
     // dim d of a row at place 8 (d / 8) + (the e with kOrder[e] = d % 8)
     constexpr int EN = NC < 8 ? NC : 8;
 #pragma unroll
-    for (int t = 0; t < TERMS; ++t) {
-      uint16_t* to_row = q_lds + ((rt * TERMS + t) * 16 + qrow) * QP;
+    for (int t = 0; t < QT; ++t) {
+      uint16_t* to_row = q_lds + ((rt * QT + t) * 16 + qrow) * QP;
 #pragma unroll
       for (int c = 0; c < (NC + 7) / 8; ++c) {
         uint16_t h[EN];
 #pragma unroll
         for (int e = 0; e < EN; ++e) {
           float& y = w[8 * c + e];
-          if (MODE == kF32) {
-            const __bf16 r = (__bf16)y;
-            y -= (float)r;
-            h[e] = __builtin_bit_cast(uint16_t, r);
-          } else {
-            if (t == 0) y = ldexpf(y, -ex);
-            const _Float16 r = (_Float16)y;
-            y -= (float)r;
-            h[e] = __builtin_bit_cast(uint16_t, r);
-          }
+          if (t == 0) y = ldexpf(y, -ex);
+          const _Float16 r = (_Float16)y;
+          y -= (float)r;
+          h[e] = __builtin_bit_cast(uint16_t, r);
         }
         if (NC >= 8) {
           u32x4 v;
@@ -305,19 +291,15 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
     my_span[rt] = my_end > my_lo[rt] ? my_end - my_lo[rt] : 0;
   }
   __syncthreads();
-  half8v qh[MODE == kF32 ? 1 : RT][QT][NK];
-  bf16x8v qb[MODE == kF32 ? RT : 1][3][NK];
+  half8v qh[RT][QT][NK];
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     qf[rt] = l_lds[rt][i];
 #pragma unroll
-    for (int t = 0; t < TERMS; ++t)
+    for (int t = 0; t < QT; ++t)
 #pragma unroll
-      for (int c = 0; c < NK; ++c) {
-        const u32x4 v = *reinterpret_cast<const u32x4*>(q_lds + ((rt * TERMS + t) * 16 + i) * QP + g * (D / 4) + 8 * c);
-        if (MODE == kF32) qb[rt][t][c] = __builtin_bit_cast(bf16x8v, v);
-        else qh[rt][t % QT][c] = __builtin_bit_cast(half8v, v);
-      }
+      for (int c = 0; c < NK; ++c)
+        qh[rt][t][c] = *reinterpret_cast<const half8v*>(q_lds + ((rt * QT + t) * 16 + i) * QP + g * (D / 4) + 8 * c);
   }
 
   f32x4 acc[RT][NC], accl[RT];
@@ -336,8 +318,6 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
   _Float16 vinv = (_Float16)1;
   const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
   const half8v ones_h = {(_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1};
-  const __bf16 one_b = (__bf16)1.0f;
-  const bf16x8v ones_b = {one_b, one_b, one_b, one_b, one_b, one_b, one_b, one_b};
 
   auto step = [&](const T& x, int t0) {
     // S^T
@@ -348,53 +328,23 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
       for (int rt = 0; rt < RT; ++rt) s[rt][t] = zero;
 #pragma unroll
       for (int c = 0; c < NK; ++c) {
-        half2v h[4];
+        half2v h[4], h1[4];
         codes8(x.k[t][c], h);
-        if (MODE == kOneGroup) {
-          const half8v k = join8(h);
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            if (FINE) s[rt][t] = mma(k, qh[rt][QT - 1][c], s[rt][t]);
-            s[rt][t] = mma(k, qh[rt][0][c], s[rt][t]);
-          }
-          continue;
-        }
-        const _Float16 sc = (c < 4 ? x.ks1[0] : x.ks1[T::NS - 1])[t];
-        if (MODE == kGroups) {
-          half2v k1[4];
+        if (GROUPS) {
+          const _Float16 sc = (c < 4 ? x.ks1[0] : x.ks1[T::NS - 1])[t];
 #pragma unroll
           for (int u = 0; u < 4; ++u) {
             const half2v y = h[u] * (half2v){sc, sc};
-            if (FINE) k1[u] = __builtin_elementwise_fma(h[u], (half2v){sc, sc}, -y);   // what the rounding left
+            if (QT == 2) h1[u] = __builtin_elementwise_fma(h[u], (half2v){sc, sc}, -y);   // what the rounding left
             h[u] = y;
           }
-          const half8v k = join8(h);
+        }
+        const half8v k = join8(h);
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            if (FINE) {
-              s[rt][t] = mma(join8(k1), qh[rt][0][c], s[rt][t]);
-              s[rt][t] = mma(k, qh[rt][QT - 1][c], s[rt][t]);
-            }
-            s[rt][t] = mma(k, qh[rt][0][c], s[rt][t]);
-          }
-        } else {
-          bf16x8v k0, k1;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            __bf16 y[2];
-            bf16_terms<2>((float)h[u >> 1][u & 1] * (float)sc, y);
-            k0[u] = y[0];
-            k1[u] = y[1];
-          }
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            f32x4& o = s[rt][t];
-            o = mma(k1, qb[rt][1][c], o);
-            o = mma(k0, qb[rt][2][c], o);
-            o = mma(k1, qb[rt][0][c], o);
-            o = mma(k0, qb[rt][1][c], o);
-            o = mma(k0, qb[rt][0][c], o);
-          }
+        for (int rt = 0; rt < RT; ++rt) {
+          if (GROUPS && QT == 2) s[rt][t] = mma(join8(h1), qh[rt][0][c], s[rt][t]);
+          if (QT == 2) s[rt][t] = mma(k, qh[rt][QT - 1][c], s[rt][t]);
+          s[rt][t] = mma(k, qh[rt][0][c], s[rt][t]);
         }
       }
     }
@@ -410,7 +360,7 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
         if (j < lo || j >= to) vs[u >> 2][u & 3] = (_Float16)0;    // never written: may hold anything
       }
     }
-    if (MODE == kOneGroup) {
+    if (!GROUPS) {
       // value scales go into the probabilities, relative to 2^vexp
       const half4v v4 = __builtin_elementwise_max(vs[0], vs[1]);
       const half2v v2 = __builtin_elementwise_max((half2v){v4[0], v4[1]}, (half2v){v4[2], v4[3]});
@@ -433,14 +383,13 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
       for (int t = 0; t < 2; ++t) vs[t] = vs[t] * (half4v){vinv, vinv, vinv, vinv};
     }
     // probabilities
-    half8v ph[RT], pv[RT];
-    bf16x8v pt[MODE == kF32 ? RT : 1][3];
+    half8v pv[RT][PT];
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       float z[8];      // scores of row i at tokens t0 + 16 t + 4 g + r
 #pragma unroll
       for (int u = 0; u < 8; ++u)
-        z[u] = MODE == kOneGroup ? s[rt][u >> 2][u & 3] * (float)x.ks4[u >> 2][u & 3] : s[rt][u >> 2][u & 3];
+        z[u] = !GROUPS ? s[rt][u >> 2][u & 3] * (float)x.ks4[u >> 2][u & 3] : s[rt][u >> 2][u & 3];
       if (edge) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
@@ -452,7 +401,7 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
 #pragma unroll
       for (int u = 1; u < 8; ++u) mx = fmaxf(mx, z[u]);
       mx *= qf[rt];
-      if (__builtin_amdgcn_ballot_w64(mx > m[rt] + kMaxSlack)) {
+      if (__builtin_amdgcn_ballot_w64(mx > m[rt] + SLACK)) {
         const float mn = fmaxf(m[rt], max_over_g(mx));
         const float f = mn > m[rt] ? exp2f(m[rt] - mn) : 1.0f;
         m[rt] = mn;
@@ -460,30 +409,27 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
         for (int c = 0; c < NC; ++c) acc[rt][c] *= f;
         accl[rt] *= f;
       }
-      const float mu = m[rt] == -__builtin_inff() ? 0.0f : m[rt];
+      const float mu = (m[rt] == -__builtin_inff() ? 0.0f : m[rt]) - LIFT;
       float pr[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) pr[u] = __builtin_amdgcn_exp2f(fmaf(z[u], qf[rt], -mu));
-      if (MODE == kF32) {
+      // the softmax sum takes them as rounded
+      half8v ph[PT];
+#pragma unroll
+      for (int t = 0; t < PT; ++t) {
+#pragma unroll
+        for (int u = 0; u < 8; ++u) ph[t][u] = (_Float16)(t ? pr[u] - (float)ph[0][u] : pr[u]);
+        accl[rt] = mma(ones_h, ph[t], accl[rt]);
+        pv[rt][t] = ph[t];
+      }
+      if (!GROUPS && PREC == kForBf16) {
+        pv[rt][0] = ph[0] * (half8v){vs[0][0], vs[0][1], vs[0][2], vs[0][3], vs[1][0], vs[1][1], vs[1][2], vs[1][3]};
+      } else if (!GROUPS) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          __bf16 t[3];
-          bf16_terms<3>(pr[u], t);
-#pragma unroll
-          for (int e = 0; e < 3; ++e) pt[rt][e][u] = t[e];
-        }
-#pragma unroll
-        for (int e = 2; e >= 0; --e) accl[rt] = mma(ones_b, pt[rt][e], accl[rt]);
-      } else {
-#pragma unroll
-        for (int u = 0; u < 8; ++u) ph[rt][u] = (_Float16)pr[u];
-        accl[rt] = mma(ones_h, ph[rt], accl[rt]);
-        pv[rt] = ph[rt];
-        if (MODE == kOneGroup && FINE) {
-#pragma unroll
-          for (int u = 0; u < 8; ++u) pv[rt][u] = (_Float16)(pr[u] * (float)vs[u >> 2][u & 3]);
-        } else if (MODE == kOneGroup) {
-          pv[rt] = ph[rt] * (half8v){vs[0][0], vs[0][1], vs[0][2], vs[0][3], vs[1][0], vs[1][1], vs[1][2], vs[1][3]};
+          const float y = pr[u] * (float)vs[u >> 2][u & 3];
+          pv[rt][0][u] = (_Float16)y;
+          if (PT == 2) pv[rt][PT - 1][u] = (_Float16)(y - (float)pv[rt][0][u]);
         }
       }
     }
@@ -497,41 +443,22 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const int c = 2 * bb + d;
-        if (MODE == kF32) {
-          bf16x8v v0, v1;
-#pragma unroll
-          for (int u = 0; u < 8; ++u) {
-            __bf16 y[2];
-            bf16_terms<2>((float)vv[d][u >> 1][u & 1] * (float)vs[u >> 2][u & 3], y);
-            v0[u] = y[0];
-            v1[u] = y[1];
-          }
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt) {
-            f32x4& o = acc[rt][c];
-            o = mma(v1, pt[rt][1], o);
-            o = mma(v0, pt[rt][2], o);
-            o = mma(v1, pt[rt][0], o);
-            o = mma(v0, pt[rt][1], o);
-            o = mma(v0, pt[rt][0], o);
-          }
-          continue;
-        }
         half2v v1[4];
-        if (MODE == kGroups) {
+        if (GROUPS) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
             const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
             const half2v y = vv[d][j] * sc;
-            if (FINE) v1[j] = __builtin_elementwise_fma(vv[d][j], sc, -y);
+            if (QT == 2) v1[j] = __builtin_elementwise_fma(vv[d][j], sc, -y);
             vv[d][j] = y;
           }
         }
         const half8v v = join8(vv[d]);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
-          if (MODE == kGroups && FINE) acc[rt][c] = mma(join8(v1), pv[rt], acc[rt][c]);
-          acc[rt][c] = mma(v, pv[rt], acc[rt][c]);
+          if (GROUPS && QT == 2) acc[rt][c] = mma(join8(v1), pv[rt][0], acc[rt][c]);
+          if (PT == 2) acc[rt][c] = mma(v, pv[rt][PT - 1], acc[rt][c]);
+          acc[rt][c] = mma(v, pv[rt][0], acc[rt][c]);
         }
       }
     }
@@ -541,12 +468,12 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
   if (some) {
     for (;;) {
       ids = load_ids(p.c, table_row, t0 + 2 * STEP, last);
-      load_tile<D, MODE>(p.c, ids1, head, t0 + STEP, last, g, i, x1);
+      load_tile<D, GROUPS>(p.c, ids1, head, t0 + STEP, last, g, i, x1);
       step(x0, t0);
       t0 += STEP;
       if (t0 >= to) break;
       ids1 = load_ids(p.c, table_row, t0 + 2 * STEP, last);
-      load_tile<D, MODE>(p.c, ids, head, t0 + STEP, last, g, i, x0);
+      load_tile<D, GROUPS>(p.c, ids, head, t0 + STEP, last, g, i, x0);
       step(x1, t0);
       t0 += STEP;
       if (t0 >= to) break;
@@ -555,7 +482,7 @@ __global__ __launch_bounds__(kAttnThreads, kv4_attn_waves(D, MODE, ROWS)) void k
 
   // join the waves, 16 rows at a time: lane (g, i) holds dims [g D/4, (g+1) D/4) of row i
   __syncthreads();           // the exchange held the queries
-  const float unit = MODE == kOneGroup ? ldexpf(1.0f, vexp) : 1.0f;
+  const float unit = !GROUPS ? ldexpf(1.0f, vexp) : 1.0f;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     if (rt) __syncthreads();
@@ -717,23 +644,26 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
   a->groups = segments * a->nsplit;
 }
 
-template <int D, int MODE, bool FINE>
-static void attn2(const Kv4AttnArgs& a, dim3 g, hipStream_t s) {
-  if (D <= 128 && MODE != kF32 && a.rows == 32)
-    hipLaunchKernelGGL((kv4_attn_kernel<D, MODE, FINE, D <= 128 && MODE != kF32 ? 32 : 16>), g, dim3(kAttnThreads), 0, s, a);
-  else
-    hipLaunchKernelGGL((kv4_attn_kernel<D, MODE, FINE, 16>), g, dim3(kAttnThreads), 0, s, a);
+template <int D, bool GROUPS, int PREC>
+static void attn2(const Kv4AttnArgs& a, hipStream_t s) {
+  constexpr int MORE = D <= 128 && PREC != kForF32 ? 32 : 16;
+  const dim3 g((unsigned)a.groups);
+  if (a.rows == MORE) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, MORE>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, 16>), g, dim3(256), 0, s, a);
+}
+
+template <int D, bool GROUPS>
+static void attn3(const Kv4AttnArgs& a, hipStream_t s) {
+  if (a.dtype == kDtF32) attn2<D, GROUPS, kForF32>(a, s);
+  else if (a.dtype == kDtF16) attn2<D, GROUPS, kForF16>(a, s);
+  else attn2<D, GROUPS, kForBf16>(a, s);
 }
 
 template <int D>
 static void attn1(const Kv4AttnArgs& a, hipStream_t s) {
-  const dim3 g((unsigned)a.groups);
   if (a.rows >= 128) launch_kv4_prompt(a, s);
-  else if (a.dtype == kDtF32) attn2<D, kF32, false>(a, g, s);
-  else if (a.c.group == D && a.dtype == kDtF16) attn2<D, kOneGroup, true>(a, g, s);
-  else if (a.c.group == D) attn2<D, kOneGroup, false>(a, g, s);
-  else if (a.dtype == kDtF16) attn2<D, kGroups, true>(a, g, s);
-  else attn2<D, kGroups, false>(a, g, s);
+  else if (a.c.group == D) attn3<D, false>(a, s);
+  else attn3<D, true>(a, s);
   if (a.nsplit > kFewParts)
     hipLaunchKernelGGL((kv4_join_kernel<D, 16>), dim3((unsigned)(a.max_new * a.q_heads), a.batch), dim3(kAttnThreads), 0, s, a);
   else if (a.nsplit > 1)

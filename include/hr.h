@@ -519,9 +519,9 @@ typedef struct {
  * q = clamp(rint(y k), -7, 7), each step one fp32 operation rounded to nearest
  * even (with the rotation, k and 1 / sqrt(dim) are one factor, whose product is
  * rounded to an integer at once).
- * A (token, head) whose key or value is not finite, or needs a scale above the
- * fp16 range, is stored with zero codes and NaN scales in both: reading it, or
- * attending to it, gives NaN.
+ * A (token, head) whose key or value is not finite, or needs a scale above 9352
+ * (values past 65464, where fp16 ends), is stored with zero codes and NaN scales
+ * in both: reading it, or attending to it, gives NaN.
  *
  *   k, v      [tokens] rows of [heads][dim] of dtype (HR_F32, HR_BF16 or
  *             HR_F16), rows k_stride / v_stride elements apart (at least

@@ -36,8 +36,8 @@ def unrotate(y, signs):
 def quantize_plain(x, group):
     """The stored codes (int8) and fp16 scales of fp32 vectors [..., dim] without
     a rotation, every step in fp32: s = fp16(a / 7), k = 1 / s, q = rint(y k).
-    A vector that is not finite, or whose scale is not, gets zero codes and NaN
-    scales."""
+    A vector that is not finite, or needs a scale above 9352, gets zero codes and
+    NaN scales."""
     y = np.asarray(x, dtype=np.float32)
     g = y.reshape(*y.shape[:-1], -1, group)
     with np.errstate(all="ignore"):
@@ -45,7 +45,7 @@ def quantize_plain(x, group):
         f = s.astype(np.float32)[..., None]
         k = np.where(f > 0, np.float32(1) / np.where(f > 0, f, np.float32(1)), np.float32(0)).astype(np.float32)
         q = np.clip(np.rint((g * k).astype(np.float32)), -7, 7)
-    bad = ~(np.isfinite(y).all(-1) & np.isfinite(s).all(-1))
+    bad = ~(np.isfinite(y).all(-1) & (s <= np.float16(9352)).all(-1))
     q = np.where(bad[..., None, None], 0, q)
     s = np.where(bad[..., None], np.float16(np.nan), s)
     return q.reshape(y.shape).astype(np.int8), s

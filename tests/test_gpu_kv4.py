@@ -134,7 +134,7 @@ def test_append_lengths(tokens, page):
 @pytest.mark.parametrize("rotate", [False, True])
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_values_that_are_not_finite(rotate, dtype):
-    """A NaN, an infinity or (fp32) a scale past fp16 poisons its (token, head), key and value, and no other."""
+    """A NaN, an infinity or (fp32) a scale past 9352 poisons its (token, head), key and value, and no other."""
     rng = _rng(8)
     heads, dim, group, tokens = 2, 128, 32, 12
     cache = hr.kv4_cache(2, heads, dim, 16, group, rotate)
