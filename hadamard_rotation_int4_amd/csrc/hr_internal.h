@@ -173,6 +173,7 @@ struct Kv4AttnArgs {
   float2* part_ml;       // [total * q_heads][nsplit] (running max in log2 units, sum)
   // by kv4_attention_plan:
   int rows;              // of a row tile: 16, 32, or 128 or 256 (kv4_prompt.hip)
+  int waves;             // of a workgroup with 16 rows: 4 or 8
   int tiles;             // row tiles of a (sequence, key/value head)
   int nsplit, chunk;     // most parts of the token axis, tokens of a part
   int64_t groups;        // workgroups

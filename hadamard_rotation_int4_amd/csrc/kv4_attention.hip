@@ -10,7 +10,7 @@
 // The rotation is orthogonal, so this is attention over the keys and values
 // that the cache stands for, without ever rotating them back.
 //
-// kv4_attn_kernel.  One workgroup of 4 waves takes 16 query rows of one
+// kv4_attn_kernel.  One workgroup of 4 or 8 waves takes 16 query rows of one
 // (sequence, key/value head) -- the rep heads that share it times the new
 // tokens -- and one part of the token axis; its waves take 32-token tiles in
 // turn.  Both products are 16x16x32 matrix instructions in the transposed form
@@ -48,8 +48,6 @@
 
 namespace hr {
 
-constexpr int kAttnThreads = 256;
-constexpr int kAttnWaves = kAttnThreads / 64;
 constexpr int kFewParts = 8;
 
 // what the fp16 operands have to hold: enough for bf16, fp16 or fp32 outputs
@@ -165,9 +163,9 @@ __device__ __forceinline__ void load_tile(const Kv4Cache& c, Ids ids, int head, 
 }
 
 // GROUPS: several scale groups a head; PREC: what the outputs can show; ROWS
-// query rows a workgroup (16 or 32)
-template <int D, bool GROUPS, int PREC, int ROWS>
-__global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv4_attn_kernel(Kv4AttnArgs p) {
+// query rows a workgroup (16 or 32), W waves (4 or 8)
+template <int D, bool GROUPS, int PREC, int ROWS, int W>
+__global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv4_attn_kernel(Kv4AttnArgs p) {
   constexpr int NK = D / 32;             // matrix instructions over the dims
   constexpr int NC = D / 16;             // 16-dim slices of the output
   constexpr int LD = D + 4;              // row pitch of the exchange
@@ -177,8 +175,8 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
   // log2 units the scores may pass the running maximum by, and what the probabilities are lifted by
   constexpr float SLACK = PREC == kForF32 ? 4.0f : 8.0f, LIFT = PREC == kForF32 ? 11.0f : 0.0f;
   typedef Tile<D, GROUPS> T;
-  __shared__ float o_lds[kAttnWaves][16][LD];
-  __shared__ float m_lds[kAttnWaves][16], l_lds[kAttnWaves][16];
+  __shared__ float o_lds[W][16][LD];
+  __shared__ float m_lds[W][16], l_lds[W][16];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int g = lane >> 4, i = lane & 15;
@@ -205,7 +203,7 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
 
   // the first tile sets out before the queries are dealt with
   const int32_t* table_row = p.table + (int64_t)b * p.width;
-  constexpr int STEP = 32 * kAttnWaves;
+  constexpr int STEP = 32 * W;
   const int last = to - 1;
   int t0 = from + 32 * wave;
   const bool some = t0 < to;
@@ -220,13 +218,19 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
   // queries, 16 lanes a row as in the output: rotate, scale to [1, 2) by a power of two (kept in qf), round, and
   // through LDS into the right operand's layout
   constexpr int QP = D + 8;              // row pitch, 16-bit elements
-  static_assert(RT * QT * QP * 2 <= kAttnWaves * LD * 4, "the queries fit the exchange");
+  static_assert(RT * QT * QP * 2 <= W * LD * 4, "the queries fit the exchange");
   uint16_t* q_lds = reinterpret_cast<uint16_t*>(o_lds);
   float qf[RT];
   int my_lo[RT];
   unsigned my_span[RT];        // the row's tokens: [my_lo, my_lo + my_span)
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
+    const int mine = row0 + 16 * rt + i;
+    const int n_mine = (mine < q.rows ? mine : q.rows - 1) / p.rep;
+    my_lo[rt] = q.lo(n_mine);
+    const int my_end = q.hi(n_mine) < to ? q.hi(n_mine) : to;
+    my_span[rt] = my_end > my_lo[rt] ? my_end - my_lo[rt] : 0;
+    if (W > 4 && wave >= 4) continue;      // four waves are 16 rows
     const int qrow = threadIdx.x >> 4;
     const int la = p.c.rotate ? kv4_logical<16>(lane) : lane & 15;
     const int row = row0 + 16 * rt + qrow;
@@ -284,11 +288,6 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
         }
       }
     }
-    const int mine = row0 + 16 * rt + i;
-    const int n_mine = (mine < q.rows ? mine : q.rows - 1) / p.rep;
-    my_lo[rt] = q.lo(n_mine);
-    const int my_end = q.hi(n_mine) < to ? q.hi(n_mine) : to;
-    my_span[rt] = my_end > my_lo[rt] ? my_end - my_lo[rt] : 0;
   }
   __syncthreads();
   half8v qh[RT][QT][NK];
@@ -490,7 +489,7 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
     __syncthreads();
     float top = m_lds[0][i];
 #pragma unroll
-    for (int w = 1; w < kAttnWaves; ++w) top = fmaxf(top, m_lds[w][i]);
+    for (int w = 1; w < W; ++w) top = fmaxf(top, m_lds[w][i]);
     const float f = m[rt] == -__builtin_inff() ? 0.0f : exp2f(m[rt] - top);
     const float fu = f * unit;
     if (g == 0) l_lds[wave][i] = accl[rt][0] * f;
@@ -501,6 +500,7 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
         *reinterpret_cast<f32x4*>(&o_lds[wave][i][(4 * g + r) * NC + c]) =
             (f32x4){acc[rt][c][r] * fu, acc[rt][c + 1][r] * fu, acc[rt][c + 2][r] * fu, acc[rt][c + 3][r] * fu};
     __syncthreads();
+    if (W > 4 && wave >= 4) continue;
     // 16 lanes a row, D/16 consecutive dims each
     const int orow = threadIdx.x >> 4;
     const int la = kv4_logical<16>(lane);
@@ -508,7 +508,7 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
 #pragma unroll
     for (int e = 0; e < NC; ++e) y[e] = 0.0f;
 #pragma unroll
-    for (int v = 0; v < kAttnWaves; ++v) {
+    for (int v = 0; v < W; ++v) {
       l += l_lds[v][orow];
       mt = fmaxf(mt, m_lds[v][orow]);
 #pragma unroll
@@ -540,7 +540,7 @@ __global__ __launch_bounds__(256, kv4_attn_waves(D, GROUPS, ROWS, PREC)) void kv
 // rotates back.  One group a row where parts are few (a wave's work is then all
 // loads, and a workgroup does 16 rows), all 16 where they are many.
 template <int D, int GROUPS>
-__global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
+__global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
   constexpr int NC = D / 16;
   __shared__ float o_lds[GROUPS][D + 4];
   __shared__ float l_lds[GROUPS];
@@ -617,7 +617,9 @@ __global__ __launch_bounds__(kAttnThreads) void kv4_join_kernel(Kv4AttnArgs p) {
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
 // two and a half for several, whose lengths differ (64 sequences of 1100 to
 // 8192 tokens: 77.7 us; two a CU 84.6, six 80.7); no part under 256 tokens (two
-// tiles a wave), or 512 of the prompt kernel.  The prompt kernel gets as many
+// tiles a wave), or 512 of the prompt kernel.  Sequences of up to 1024 tokens, no
+// more than one workgroup a CU, are not divided: 8 waves take one (4 tiles a
+// wave) and no second launch follows.  The prompt kernel gets as many
 // workgroups as run at once.
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
@@ -631,7 +633,12 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
   const int64_t segments = (int64_t)a->batch * a->c.heads * a->tiles;
   const int64_t least = a->rows >= 128 ? 512 : 256;
-  const int64_t want = a->rows == 256 ? 256 : a->rows == 128 || a->batch == 1 ? 512 : 640;
+  int64_t want = a->rows == 256 ? 256 : a->rows == 128 || a->batch == 1 ? 512 : 640;
+  a->waves = 4;
+  if (a->rows == 16 && segments <= 256 && span <= 1024) {
+    a->waves = 8;
+    want = 1;
+  }
   int64_t n = segments > 0 ? (want + segments - 1) / segments : 1;
   const int64_t most = (span + least - 1) / least;
   if (n > most) n = most;
@@ -648,8 +655,9 @@ template <int D, bool GROUPS, int PREC>
 static void attn2(const Kv4AttnArgs& a, hipStream_t s) {
   constexpr int MORE = D <= 128 && PREC != kForF32 ? 32 : 16;
   const dim3 g((unsigned)a.groups);
-  if (a.rows == MORE) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, MORE>), g, dim3(256), 0, s, a);
-  else hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, 16>), g, dim3(256), 0, s, a);
+  if (a.waves == 8) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, 16, 8>), g, dim3(512), 0, s, a);
+  else if (a.rows == MORE) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, MORE, 4>), g, dim3(256), 0, s, a);
+  else hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, 16, 4>), g, dim3(256), 0, s, a);
 }
 
 template <int D, bool GROUPS>
@@ -665,10 +673,10 @@ static void attn1(const Kv4AttnArgs& a, hipStream_t s) {
   else if (a.c.group == D) attn3<D, false>(a, s);
   else attn3<D, true>(a, s);
   if (a.nsplit > kFewParts)
-    hipLaunchKernelGGL((kv4_join_kernel<D, 16>), dim3((unsigned)(a.max_new * a.q_heads), a.batch), dim3(kAttnThreads), 0, s, a);
+    hipLaunchKernelGGL((kv4_join_kernel<D, 16>), dim3((unsigned)(a.max_new * a.q_heads), a.batch), dim3(256), 0, s, a);
   else if (a.nsplit > 1)
     hipLaunchKernelGGL((kv4_join_kernel<D, 1>), dim3((unsigned)((a.max_new * a.q_heads + 15) / 16), a.batch),
-                       dim3(kAttnThreads), 0, s, a);
+                       dim3(256), 0, s, a);
 }
 
 hipError_t launch_kv4_attention(const Kv4AttnArgs& a, hipStream_t s) {
