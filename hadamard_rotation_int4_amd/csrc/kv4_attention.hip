@@ -543,7 +543,7 @@ template <int D, int GROUPS>
 __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
   constexpr int NC = D / 16;
   __shared__ float o_lds[GROUPS][D + 4];
-  __shared__ float l_lds[GROUPS];
+  __shared__ float l_lds[GROUPS], m_lds[GROUPS];
   const int lane = threadIdx.x & 63;
   const int grp = (threadIdx.x >> 4) % GROUPS;
   const int la = kv4_logical<16>(lane);
@@ -563,40 +563,53 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
   }
   if (GROUPS > 1 && parts == 1) return;      // the whole workgroup
   const int64_t first = out_row * p.nsplit;
-  float top = -__builtin_inff();
-  if (GROUPS > 1) {
-    for (int s = lane; s < parts; s += 64) top = fmaxf(top, p.part_ml[first + s].x);
-    top = wave_max(top);
-  } else if (parts > 1) {
-    for (int s = 0; s < parts; ++s) top = fmaxf(top, p.part_ml[first + s].x);
-  }
-  float w[NC], l = 0.0f;
+  // four parts asked for at once, against a maximum of the group's own
+  float w[NC], l = 0.0f, m = -__builtin_inff();
 #pragma unroll
   for (int e = 0; e < NC; ++e) w[e] = 0.0f;
   if (parts > 1) {
-    for (int s = grp; s < parts; s += GROUPS) {
-      const int64_t at = first + s;
-      const float2 v = p.part_ml[at];
-      const float f = v.x == -__builtin_inff() ? 0.0f : exp2f(v.x - top);
-      l += v.y * f;
-      float o[NC];
-      load_vec<kDtF32, NC>(p.part_o + at * D + la * NC, o);
+    for (int s0 = grp; s0 < parts; s0 += 4 * GROUPS) {
+      float2 v[4];
+      float o[4][NC];
 #pragma unroll
-      for (int e = 0; e < NC; ++e) w[e] = fmaf(o[e], f, w[e]);
+      for (int u = 0; u < 4; ++u) {
+        const int64_t at = first + (s0 + u * GROUPS < parts ? s0 + u * GROUPS : s0);
+        v[u] = p.part_ml[at];
+        load_vec<kDtF32, NC>(p.part_o + at * D + la * NC, o[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        if (s0 + u * GROUPS >= parts) continue;
+        const float mn = fmaxf(m, v[u].x);
+        const float f0 = m == -__builtin_inff() ? 0.0f : exp2f(m - mn);
+        const float f1 = v[u].x == -__builtin_inff() ? 0.0f : exp2f(v[u].x - mn);
+        m = mn;
+        l = l * f0 + v[u].y * f1;
+#pragma unroll
+        for (int e = 0; e < NC; ++e) w[e] = fmaf(o[u][e], f1, w[e] * f0);
+      }
     }
   }
   if (GROUPS > 1) {
     store_vec<kDtF32, NC>(&o_lds[grp][la * NC], w);
-    if (la == 0) l_lds[grp] = l;
+    if (la == 0) {
+      l_lds[grp] = l;
+      m_lds[grp] = m;
+    }
     __syncthreads();
     if (grp >= 4) return;      // the first wave goes on (all of it: the exchanges need whole rows)
+    float top = m_lds[0];
+#pragma unroll
+    for (int s = 1; s < GROUPS; ++s) top = fmaxf(top, m_lds[s]);
 #pragma unroll
     for (int e = 0; e < NC; ++e) w[e] = 0.0f;
     l = 0.0f;
+#pragma unroll 4
     for (int s = 0; s < GROUPS; ++s) {
-      l += l_lds[s];
+      const float f = m_lds[s] == -__builtin_inff() ? 0.0f : exp2f(m_lds[s] - top);
+      l = fmaf(l_lds[s], f, l);
 #pragma unroll
-      for (int e = 0; e < NC; ++e) w[e] += o_lds[s][la * NC + e];
+      for (int e = 0; e < NC; ++e) w[e] = fmaf(o_lds[s][la * NC + e], f, w[e]);
     }
   }
   finish_row<D>(p.c.rotate, p.c.signs, l, la, w);
