@@ -149,13 +149,18 @@ __device__ __forceinline__ void load_vec(const void* p, float* w) {
   }
 }
 
-// N consecutive fp32 values rounded to DT (nearest even) and stored.
-template <int DT, int N>
+// N consecutive fp32 values rounded to DT (nearest even) and stored; NT: with
+// the nontemporal hint (a branch on a run-time flag would be merged without it).
+template <int DT, int N, bool NT = false>
 __device__ __forceinline__ void store_vec(void* p, const float* w) {
   if (DT == kDtF32) {
 #pragma unroll
-    for (int i = 0; i < N; i += 4)
-      reinterpret_cast<f32x4*>(p)[i / 4] = (f32x4){w[i], w[i + 1], w[i + 2], w[i + 3]};
+    for (int i = 0; i < N; i += 4) {
+      const f32x4 v = {w[i], w[i + 1], w[i + 2], w[i + 3]};
+      f32x4* q = reinterpret_cast<f32x4*>(p) + i / 4;
+      if (NT) __builtin_nontemporal_store(v, q);
+      else *q = v;
+    }
     return;
   }
   uint32_t u[N / 2];
@@ -171,8 +176,12 @@ __device__ __forceinline__ void store_vec(void* p, const float* w) {
   }
   if (N % 8 == 0) {
 #pragma unroll
-    for (int i = 0; i < N / 8; ++i)
-      reinterpret_cast<u32x4*>(p)[i] = (u32x4){u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
+    for (int i = 0; i < N / 8; ++i) {
+      const u32x4 v = {u[4 * i], u[4 * i + 1], u[4 * i + 2], u[4 * i + 3]};
+      u32x4* q = reinterpret_cast<u32x4*>(p) + i;
+      if (NT) __builtin_nontemporal_store(v, q);
+      else *q = v;
+    }
   } else {
 #pragma unroll
     for (int i = 0; i < N / 4; ++i) reinterpret_cast<uint2*>(p)[i] = make_uint2(u[2 * i], u[2 * i + 1]);
