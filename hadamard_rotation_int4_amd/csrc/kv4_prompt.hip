@@ -172,13 +172,26 @@ __device__ __forceinline__ void store_values(const ValueShare<D>& x, char* buf, 
   }
 }
 
+// w := H_{2 E} w over a lane's E values and those of the lane 32 on.
+template <int E>
+__device__ __forceinline__ void fwht_halves(float* w, int h) {
+  fwht_regs<E>(w);
+  const float bh = h ? -1.0f : 1.0f;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
+    w[e] = fmaf(__uint_as_float(s[1]), bh, __uint_as_float(s[0]));
+  }
+}
+
+// Bits [0, n) set, n clamped to 0..32.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1u; }
+
 template <int D, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv4AttnArgs p) {
   typedef PromptLds<D> L;
   constexpr int NC = D / 16, NB = D / 32;
-  constexpr int LD = D + 4;
-  constexpr int LDS = W * 16 * LD * 4 > L::ALL ? W * 16 * LD * 4 : L::ALL;    // the output's way out needs less or a little more
-  __shared__ __attribute__((aligned(16))) char lds[LDS];
+  __shared__ __attribute__((aligned(16))) char lds[L::ALL];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int h = lane >> 5, n = lane & 31;
@@ -209,8 +222,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   const int row = wrow0 + n;
   const bool valid = row < q.rows;
   const int n_mine = valid ? row / p.rep : w_last;
+  const int q_head = head * p.rep + (valid ? row - n_mine * p.rep : 0);     // a row past the last reads one that is there
   const int my_lo = q.lo(n_mine), my_end = valid ? (q.hi(n_mine) < to ? q.hi(n_mine) : to) : 0;
-  const unsigned my_span = my_end > my_lo ? my_end - my_lo : 0;
 
   const int32_t* table_row = p.table + (int64_t)b * p.width;
   char* const kbuf = lds;
@@ -243,14 +256,10 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   {
     constexpr int E = D / 2;
     float w[E];
-    const int64_t at = (int64_t)(q.s0 + n_mine) * p.q_stride + (head * p.rep + (valid ? row - n_mine * p.rep : 0)) * D;
+    const int64_t at = (int64_t)(q.s0 + n_mine) * p.q_stride + q_head * D;
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (valid) load_vec<kDtBf16, 8>(reinterpret_cast<const uint16_t*>(p.q) + at + 16 * c + 8 * h, w + 8 * c);
-      else
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[8 * c + e] = 0.0f;
-    }
+    for (int c = 0; c < NC; ++c) load_vec<kDtBf16, 8>(reinterpret_cast<const uint16_t*>(p.q) + at + 16 * c + 8 * h, w + 8 * c);
+    float norm = 1.0f;
     if (p.c.rotate) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -259,24 +268,20 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
 #pragma unroll
         for (int e = 0; e < 8; ++e) w[8 * c + e] = flip(w[8 * c + e], sg[e]);
       }
-      fwht_regs<E>(w);
-      const float bh = h ? -1.0f : 1.0f;
-#pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
-        w[e] = fmaf(__uint_as_float(s[1]), bh, __uint_as_float(s[0])) * kv4_norm<D>();
-      }
+      fwht_halves<E>(w, h);
+      norm = kv4_norm<D>();
     }
     float mx = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(w[e]));
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-    const int ex = row_exponent(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])));
+    const int ex = row_exponent(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])) * norm);
     qs = ldexpf(qs, ex);
+    norm = ldexpf(norm, -ex);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qf[c][e] = (_Float16)ldexpf(w[8 * c + kOrder[e]], -ex);
+      for (int e = 0; e < 8; ++e) qf[c][e] = (_Float16)(w[8 * c + kOrder[e]] * norm);
   }
 
   f32x16 acc[NB];
@@ -317,15 +322,16 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   for (int t0 = from; t0 < to; t0 += kPromptTokens) {
     const int end = all_hi < to ? all_hi : to;
     if (t0 < all_lo || t0 + kPromptTokens > end) {
-      // tokens [my_lo, my_lo + my_span) by one comparison
-      const int t4 = t0 + 4 * h - my_lo;
+      // the row's tokens as bits, one of them spread over a score at a time
 #pragma unroll
-      for (int st = 0; st < 2; ++st)
+      for (int st = 0; st < 2; ++st) {
+        const uint32_t seen = (low_bits(my_end - t0 - 32 * st) & ~low_bits(my_lo - t0 - 32 * st)) >> (4 * h);
 #pragma unroll
         for (int r = 0; r < 16; ++r) {
-          const unsigned j = (unsigned)(t4 + (32 * st + 8 * (r >> 2) + (r & 3)));
-          s[st][r] = j < my_span ? s[st][r] : -__builtin_inff();
+          const uint32_t k = (uint32_t)__builtin_amdgcn_sbfe(seen, 8 * (r >> 2) + (r & 3), 1);
+          s[st][r] = __uint_as_float((__float_as_uint(s[st][r]) & k) | (~k & 0xFF800000u));
         }
+      }
     }
     float mx = s[0][0];
 #pragma unroll
@@ -389,49 +395,38 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(l), __float_as_uint(l), false, false);
     l = __uint_as_float(sw[0]) + __uint_as_float(sw[1]);
   }
-  const bool is_part = parts > 1 && p.nsplit > 1;
-  const float weight = is_part ? l : l == 0.0f ? 0.0f : 1.0f / l;
-
-  // output: 16 rows at a time through the wave's own piece of LDS
-  float* o_lds = reinterpret_cast<float*>(lds) + wave * 16 * LD;
-  const int la = kv4_logical<16>(lane);
+  if (!valid) return;
+  // output: lane (h, n) holds dims u NC + c of row n, u = 8 (i / 4) + 4 h + i % 4 (i < 8): turned back as the
+  // queries were turned
+  float w[D / 2];
 #pragma unroll
-  for (int half = 0; half < 2; ++half) {
-    if ((n >> 4) == half) {
+  for (int i = 0; i < 8; ++i)
 #pragma unroll
-      for (int db = 0; db < NB; ++db)
+    for (int c = 0; c < NC; ++c) w[i * NC + c] = acc[c >> 1][8 * (c & 1) + i];
+  const int64_t out_row = (int64_t)(q.s0 + n_mine) * p.q_heads + q_head;
+  if (parts > 1 && p.nsplit > 1) {
+    const int64_t at = out_row * p.nsplit + part;
 #pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const int pos = 32 * db + 8 * (r >> 2) + 4 * h + (r & 3);
-          o_lds[(n & 15) * LD + (pos & 15) * NC + (pos >> 4)] = acc[db][r];
-        }
+    for (int i = 0; i < 8; ++i) store_vec<kDtF32, NC>(p.part_o + at * D + (8 * (i >> 2) + 4 * h + (i & 3)) * NC, w + i * NC);
+    if (h == 0) p.part_ml[at] = make_float2(m, l);
+    return;
+  }
+  float f = l == 0.0f ? 0.0f : 1.0f / l;
+  if (p.c.rotate) {
+    fwht_halves<D / 2>(w, h);
+    f *= kv4_norm<D>();
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int dim = (8 * (i >> 2) + 4 * h + (i & 3)) * NC;
+    uint32_t sg[NC];
+    if (p.c.rotate) load_signs<NC>(p.c.signs, dim, sg);
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      w[i * NC + c] *= f;
+      if (p.c.rotate) w[i * NC + c] = flip(w[i * NC + c], sg[c]);
     }
-    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
-#pragma unroll
-    for (int step = 0; step < 4; ++step) {
-      const int r16 = 4 * step + (lane >> 4);
-      float w[NC];
-      load_vec<kDtF32, NC>(o_lds + r16 * LD + la * NC, w);
-      const int from_lane = 16 * half + r16;
-      const float lr = __shfl(weight, from_lane, 64), mr = __shfl(m, from_lane, 64);
-      const int r2 = wrow0 + 16 * half + r16;
-      const bool store = r2 < q.rows;
-      const int n2 = store ? r2 / p.rep : 0;
-      const int64_t out_row = (int64_t)(q.s0 + n2) * p.q_heads + head * p.rep + (store ? r2 - n2 * p.rep : 0);
-      if (is_part) {
-        if (store) {
-          const int64_t at = out_row * p.nsplit + part;
-          store_vec<kDtF32, NC>(p.part_o + at * D + la * NC, w);
-          if (la == 0) p.part_ml[at] = make_float2(mr, lr);
-        }
-      } else {
-        turn_back<D>(p.c.rotate, p.c.signs, lr, la, w);
-        if (store) store_vec<kDtBf16, NC>(reinterpret_cast<uint16_t*>(p.out) + out_row * D + la * NC, w);
-      }
-    }
-    __builtin_amdgcn_wave_barrier();
+    store_vec<kDtBf16, NC>(reinterpret_cast<uint16_t*>(p.out) + out_row * D + dim, w + i * NC);
   }
 }
 
