@@ -20,8 +20,15 @@
 // covers 512 / dim consecutive tokens of one head: their codes are contiguous
 // in a page, and so are their scales.  Heads vary fastest over the grid, so
 // the workgroups in flight read whole token rows.  Everything stays in
-// registers: no LDS.  Bound by memory when there are many tokens and by the
-// launch when there are few.
+// registers: no LDS.
+//
+// Bound by memory when there are many tokens: 32768 of 8 heads of 128 in bf16
+// (169 MB either way) are written in 42 us, 4.1 TB/s, and read back in 35 us,
+// 4.8 TB/s, where a large copy reaches 5.0.  Writing also issues some 400 vector
+// instructions for 2 KB of input a wave, a quarter of them the transform; a
+// transform on 4-point dot products, more sets a wave and nontemporal loads left
+// its time as it was.  Bound by the launch when there are few: one token 3.7 and
+// 3.4 us, 1237 plain fp32 ones of 8 heads of 64 3.9 and 4.8.
 #include "kv4_device.h"
 
 namespace hr {

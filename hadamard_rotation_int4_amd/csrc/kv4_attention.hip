@@ -43,7 +43,21 @@
 // the same, and probabilities in two terms too, lifted by 2^11 so that small
 // ones keep their bits: all products above 2^-22 of the whole are there.
 //
-// Rows of parts are joined by kv4_join_kernel, in the order of the parts.
+// Bound by memory for single tokens: 64 sequences of 1100 to 8192 tokens, 32
+// heads on 8 of 128 dims (311 MB of cache) 74 us, 4.2 TB/s, one of 131071 (138
+// MB) 32 us, 4.4 TB/s, where a large read reaches 5.7.  The first without its
+// arithmetic takes 63 to 72, without its loads 44.  With several rows a sequence
+// (12 sequences of up to 6000 tokens, 5 new ones each, 40 heads on 8, two groups
+// a head) it is vector instructions, some 360 a tile and wave beside 34 matrix
+// ones, and the chain from the sequence's length over its page ids to its codes,
+// which no other wave hides when a workgroup has seven tiles a wave: 26 us.
+// What was measured and not kept: equal shares of all tokens for every
+// workgroup (each then looks for its place first: slower), 8 waves everywhere,
+// other orders of the workgroups, deeper prefetch (registers), keys left as
+// codes plus an offset taken back by a sum of the queries (1 to 2%).
+//
+// Rows of parts are joined by kv4_join_kernel, in the order of the parts: 4 to 6
+// us, mostly a launch and three loads that wait for each other.
 #include "kv4_attention.h"
 
 namespace hr {
@@ -618,22 +632,25 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 
 // Which kernel, and into how many parts of the token axis.
 //
-// Rows: 16 a workgroup of the kernel above; 32 where there are more than 16
-// and the registers allow (the codes of a tile are then made fp16 once for
-// both halves); past 32 bf16 ones, 128 of the prompt kernel, or 256 of it for 128 dims
-// and more than 128 rows (2048 tokens, 32 heads on 8, over 8192: 276 against
-// 292 us; 64 dims lose the third workgroup a CU, 127 against 101 us, and 256
-// dims the registers).  The prompt kernel's keys and values are rounded to
+// Rows: 16 a workgroup of the kernel above; 32 where there are more than 16 and
+// the registers allow (the codes of a tile are then made fp16 once for both
+// halves); past 32 bf16 ones, 128 of the prompt kernel, or 256 of it for 128
+// dims and more than 128 rows (2048 tokens, 32 heads on 8, over 8192: 276
+// against 292 us; 64 dims lose the third workgroup a CU, 127 against 101 us, and
+// 256 dims the registers).  The prompt kernel's keys and values are rounded to
 // fp16, which an fp16 output would show (its error 5.5e-4 where the rounding of
 // the output alone is 2.1e-4, against 2.4e-4 here, at 372 against 446 us).
+//
 // Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
-// two and a half for several, whose lengths differ (64 sequences of 1100 to
-// 8192 tokens: 77.7 us; two a CU 84.6, six 80.7); no part under 256 tokens (two
-// tiles a wave), or 512 of the prompt kernel.  Sequences of up to 1024 tokens, no
-// more than one workgroup a CU, are not divided: 8 waves take one (4 tiles a
-// wave) and no second launch follows.  The prompt kernel gets as many
-// workgroups as run at once.
+// two and a half for several, whose lengths differ (64 sequences of 1100 to 8192
+// tokens: 77.9 us; two a CU 84.6, five 80.5.  12 sequences of 5 new tokens:
+// 30.6; 480 workgroups 35.7, five a CU 41.0); no part under 256 tokens (two
+// tiles a wave), or 512 of the prompt kernel, which gets as many workgroups as
+// run at once.  Sequences of up to 1024 tokens, no more than one workgroup a CU,
+// are not divided: 8 waves take one (4 tiles a wave) and no second launch follows
+// (1024 tokens of one sequence: 10.5 against 12.7 us; up to 2048 of 16, 64 dims:
+// 14.3 undivided, 13.4 in parts).
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
   a->rows = 16;
