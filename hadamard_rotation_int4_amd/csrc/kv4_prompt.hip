@@ -14,6 +14,12 @@
 // leave their lane, and the softmax needs one exchange (between the two halves
 // of a wave), and that only when the running maximum moves.
 //
+// Queries are scaled by the softmax scale and log2(e) before they are rounded, so
+// that scores come out as exponents.  Keys, scaled, and queries are rounded to
+// fp16: a score is good to 2^-11 of its terms' sizes (of keys that are all alike
+// the rounding does not average out), where the row kernel holds keys of one
+// group exactly.
+//
 // LDS holds scaled fp16, in 16-byte pieces that a wave reads contiguously:
 //   keys    [dim / 8][64 tokens] pieces of 8 dims (in nibble order; the
 //           queries are laid out to match), one piece of padding a row so that
@@ -198,6 +204,10 @@ template <int D, int W>
 __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv4AttnArgs p) {
   typedef PromptLds<D> L;
   constexpr int NC = D / 16, NB = D / 32;
+  // The products start from minus the running maximum instead of 0 and need no subtraction (128 dims, the case
+  // above: 278 against 285 us).  At 64 dims the sixteen registers that holds cost the third workgroup a CU or spills
+  // (97.0 against 94.7 us, the ragged case), and scores are made relative after the products.
+  constexpr bool RELATIVE = D != 64;
   __shared__ __attribute__((aligned(16))) char lds[L::ALL];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -259,14 +269,14 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
 
   // queries: lane (h, n) holds dims 16 c + 8 h + e of row n
   half8v qf[NC];
-  float qs = p.scale * kLog2e;
+  float qs;
   {
     constexpr int E = D / 2;
     float w[E];
     const int64_t at = (int64_t)(q.s0 + n_mine) * p.q_stride + q_head * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) load_vec<kDtBf16, 8>(reinterpret_cast<const uint16_t*>(p.q) + at + 16 * c + 8 * h, w + 8 * c);
-    float norm = 1.0f;
+    float norm = p.scale * kLog2e;
     if (p.c.rotate) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -276,33 +286,38 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
         for (int e = 0; e < 8; ++e) w[8 * c + e] = flip(w[8 * c + e], sg[e]);
       }
       fwht_halves<E>(w, h);
-      norm = kv4_norm<D>();
+      norm *= kv4_norm<D>();
     }
     float mx = 0.0f;
 #pragma unroll
     for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(w[e]));
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-    const int ex = row_exponent(fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])) * norm);
-    qs = ldexpf(qs, ex);
+    // in log2 units they are fp16 numbers as they are, but for rows that would leave its normal range: those by a
+    // power of two, made good at the scores
+    const float top = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])) * fabsf(norm);
+    const int ex = top > 0x1p-10f && top < 0x1p15f ? 0 : row_exponent(top);
+    qs = ldexpf(1.0f, ex);
     norm = ldexpf(norm, -ex);
 #pragma unroll
     for (int c = 0; c < NC; ++c)
 #pragma unroll
       for (int e = 0; e < 8; ++e) qf[c][e] = (_Float16)(w[8 * c + kOrder[e]] * norm);
   }
+  const bool shifted = !RELATIVE || __builtin_amdgcn_ballot_w64(qs != 1.0f) != 0;
 
   f32x16 acc[NB];
 #pragma unroll
   for (int db = 0; db < NB; ++db)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[db][r] = 0.0f;
-  float m = -__builtin_inff(), l = 0.0f;
+  // scores are made relative to the running maximum m; with nothing seen yet, to 0
+  float m = 0.0f, slack = -__builtin_inff(), l = 0.0f;
+  f32x16 minus;
+#pragma unroll
+  for (int r = 0; r < 16; ++r) minus[r] = 0.0f;
 
   auto scores = [&](const char* buf, f32x16* s) {
-#pragma unroll
-    for (int st = 0; st < 2; ++st)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) s[st][r] = 0.0f;
+    s[0] = s[1] = minus;
     // the two blocks' sums in turn, so that neither waits for itself
 #pragma unroll
     for (int c = 0; c < NC; ++c)
@@ -340,22 +355,34 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
         }
       }
     }
+    if (shifted) {
+#pragma unroll
+      for (int st = 0; st < 2; ++st)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s[st][r] = fmaf(s[st][r], qs, -m);
+    }
     float mx = s[0][0];
 #pragma unroll
     for (int st = 0; st < 2; ++st)
 #pragma unroll
       for (int r = 0; r < 16; ++r) mx = fmaxf(mx, s[st][r]);
-    mx *= qs;
-    if (__builtin_amdgcn_ballot_w64(mx > m + kMaxSlack)) {
+    if (__builtin_amdgcn_ballot_w64(mx > slack)) {
       const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
-      const float mn = fmaxf(m, fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1])));
-      const float f = mn > m ? exp2f(m - mn) : 1.0f;
-      m = mn;
+      const float up = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
+      const bool first = slack < 0.0f, some = up > -__builtin_inff();
+      const float by = first ? (some ? up : 0.0f) : fmaxf(up, 0.0f);
+      const float f = first ? 1.0f : exp2f(-by);
+      if (some) slack = kMaxSlack;
+      m += by;
       l *= f;
 #pragma unroll
       for (int db = 0; db < NB; ++db) acc[db] *= f;
+      s[0] -= by;
+      s[1] -= by;
+      const float mm = shifted ? 0.0f : -m;
+#pragma unroll
+      for (int r = 0; r < 16; ++r) minus[r] = mm;
     }
-    const float mu = m == -__builtin_inff() ? 0.0f : m;
     // what is asked for at the end of this turn; its page id is read early
     const Place pv = ahead;
     ahead = place_of<D>(p.c, table_row, head, t0 + 3 * kPromptTokens + blk, last);
@@ -369,8 +396,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     for (int t = 0; t < 4; ++t)
 #pragma unroll
       for (int i = 0; i < 8; i += 2) {
-        const float e0 = __builtin_amdgcn_exp2f(fmaf(s[t >> 1][8 * (t & 1) + i], qs, -mu));
-        const float e1 = __builtin_amdgcn_exp2f(fmaf(s[t >> 1][8 * (t & 1) + i + 1], qs, -mu));
+        const float e0 = __builtin_amdgcn_exp2f(s[t >> 1][8 * (t & 1) + i]);
+        const float e1 = __builtin_amdgcn_exp2f(s[t >> 1][8 * (t & 1) + i + 1]);
         const half2v e = {(_Float16)e0, (_Float16)e1};
         ph[t][i] = e[0];
         ph[t][i + 1] = e[1];
@@ -415,7 +442,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     const int64_t at = out_row * p.nsplit + part;
 #pragma unroll
     for (int i = 0; i < 8; ++i) store_vec<kDtF32, NC>(p.part_o + at * D + (8 * (i >> 2) + 4 * h + (i & 3)) * NC, w + i * NC);
-    if (h == 0) p.part_ml[at] = make_float2(m, l);
+    if (h == 0) p.part_ml[at] = make_float2(slack < 0.0f ? -__builtin_inff() : m, l);
     return;
   }
   float f = l == 0.0f ? 0.0f : 1.0f / l;

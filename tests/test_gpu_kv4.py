@@ -349,6 +349,47 @@ def test_sizes_of_queries(qsize):
     _close(_num(out), f.want(_num(q), np.array([0, 1]), 0.088 / qsize), TOL["bf16"])
 
 
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("news", [40, 150])
+def test_prompt_rows_of_different_sizes(dim, news):
+    """Rows side by side whose queries lie within fp16's range, above it and below it."""
+    rng = _rng(8)
+    f = Filled(rng, [news + 60], 2, dim, dim, 16, True, size=1e-6)
+    q = rng.standard_normal((news, 4, dim)) * rng.choice([1e6, 1.0, 1e-6, 0.0], (news, 4, 1))
+    q = _t(q.astype(np.float32)).to(torch.bfloat16)
+    starts = np.array([0, news], dtype=np.int32)
+    out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news)
+    _close(_num(out), f.want(_num(q), starts), TOL["bf16"])
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+@pytest.mark.parametrize("side", [-1, 1])
+@pytest.mark.parametrize("news", [1, 40, 150])
+def test_running_maximum_far_from_zero(dim, side, news):
+    """All scores of a row near -150 or 150 (in log2 units, 128 dims): only their differences count.  Keys are
+    multiples of their scale, 1/2, so fp16 holds them; what rounding the queries does is alike for all tokens but for
+    2^-12 / sqrt(3) of 3 times the 0.4 by which keys differ, 2e-4; fp32 sums of 2^7 are good to 2^-16."""
+    rng = _rng(9)
+    n, heads, page = news + 90, 2, 16
+    base = rng.choice([-1.0, 1.0], (1, heads, dim))
+    k = base * rng.choice([2.5, 3.0, 3.5], (n, heads, dim))
+    v = rng.standard_normal((n, heads, dim))
+    pages = -(-n // page)
+    cache = hr.kv4_cache(pages, heads, dim, page, dim, rotate=False)
+    at = [_t(x.astype(np.float32)).to(torch.bfloat16) for x in (k, v)]
+    hr.kv4_append(cache, at[0], at[1], torch.arange(n, device=DEV))
+    vals = [oracle.kv4.values(_num(c), _num(s)) for c, s in ((cache.k_codes, cache.k_scales),
+                                                             (cache.v_codes, cache.v_scales))]
+    assert np.array_equal(vals[0].transpose(0, 2, 1, 3).reshape(-1, heads, dim)[:n], k)
+    q = 3 * side * np.repeat(base, 2, 1) + 0.3 * rng.standard_normal((news, 2 * heads, dim))
+    q = _t(q.astype(np.float32)).to(torch.bfloat16)
+    table, lens = np.arange(pages, dtype=np.int32)[None], np.array([n], dtype=np.int32)
+    starts = np.array([0, news], dtype=np.int32)
+    out = hr.kv4_attention(cache, q, _t(table), _t(lens), starts=_t(starts), max_new=news)
+    want = oracle.kv4.attention(_num(q), vals[0], vals[1], table, lens, starts, dim ** -0.5, None, False, True, 0)
+    _close(_num(out), want, TOL["bf16"])
+
+
 def test_append_then_attend_end_to_end():
     """Attention over what append wrote is near attention over the keys and values themselves."""
     rng = _rng(7)
