@@ -5,6 +5,7 @@
 #include <stdarg.h>
 #include <stdio.h>
 
+#include <algorithm>
 #include <string>
 
 #include "hr.h"
@@ -667,8 +668,14 @@ int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, in
   a.max_new = max_new;
   a.max_len = max_len;
   a.window = window;
-  hr::kv4_attention_plan(&a);
-  return kv4_workspace(a);
+  // the plan also looks at whether a head has several scale groups: enough for either
+  int64_t need = 0;
+  for (int group : {dim, dim / 2}) {
+    a.c.group = group;
+    hr::kv4_attention_plan(&a);
+    need = std::max(need, kv4_workspace(a));
+  }
+  return need;
 }
 
 int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype, int64_t q_stride, int64_t total,

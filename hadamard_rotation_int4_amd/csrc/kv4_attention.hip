@@ -46,11 +46,11 @@
 // Bound by memory for single tokens: 64 sequences of 1100 to 8192 tokens, 32
 // heads on 8 of 128 dims (311 MB of cache) 74 us, 4.2 TB/s, one of 131071 (138
 // MB) 32 us, 4.4 TB/s, where a large read reaches 5.7.  The first without its
-// arithmetic takes 63 to 72, without its loads 44.  With several rows a sequence
-// (12 sequences of up to 6000 tokens, 5 new ones each, 40 heads on 8, two groups
-// a head) it is vector instructions, some 360 a tile and wave beside 34 matrix
-// ones, and the chain from the sequence's length over its page ids to its codes,
-// which no other wave hides when a workgroup has seven tiles a wave: 26 us.
+// arithmetic takes 63 to 72, without its loads 44.  With several new tokens a
+// sequence it is the wait for the chain from a sequence's length over its page
+// ids to its codes, in workgroups of few tiles a wave: 12 sequences of up to 6000
+// tokens, 5 new ones each, 40 heads on 8, two groups a head, 24 us, where 57% of
+// the waves' cycles were waits with 32 rows a workgroup and half the workgroups.
 // What was measured and not kept: equal shares of all tokens for every
 // workgroup (each then looks for its place first: slower), 8 waves everywhere,
 // other orders of the workgroups, deeper prefetch (registers), keys left as
@@ -632,38 +632,44 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 
 // Which kernel, and into how many parts of the token axis.
 //
-// Rows: 16 a workgroup of the kernel above; 32 where there are more than 16 and
-// the registers allow (the codes of a tile are then made fp16 once for both
-// halves); past 32 bf16 ones, 128 of the prompt kernel, or 256 of it for 128
-// dims and more than 128 rows (2048 tokens, 32 heads on 8, over 8192: 276
-// against 292 us; 64 dims lose the third workgroup a CU, 127 against 101 us, and
-// 256 dims the registers).  The prompt kernel's keys and values are rounded to
-// fp16, which an fp16 output would show (its error 5.5e-4 where the rounding of
-// the output alone is 2.1e-4, against 2.4e-4 here, at 372 against 446 us).
+// Rows: 16 a workgroup of the kernel above, and fp16 ones 32 where that still
+// makes two workgroups a CU (the codes of a tile are then made fp16 once for
+// both halves: 1024 tokens, 32 heads on 8, over 4096 197 against 224 us; where
+// there are fewer, twice the workgroups wait less: 64 sequences of 3 new tokens,
+// 64 heads on 8, 48 against 60); past 32 bf16 ones, 128 of the prompt kernel, or
+// 256 of it for 128 dims and more than 128 rows (2048 tokens, 32 heads on 8, over
+// 8192: 276 against 292 us; 64 dims lose the third workgroup a CU, 127 against
+// 101 us, and 256 dims the registers).  The prompt kernel's keys and values are
+// rounded to fp16, which an fp16 output would show (its error 5.5e-4 where the
+// rounding of the output alone is 2.1e-4, against 2.4e-4 here, at 372 against
+// 446 us).
 //
 // Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
 // two and a half for several, whose lengths differ (64 sequences of 1100 to 8192
-// tokens: 77.9 us; two a CU 84.6, five 80.5.  12 sequences of 5 new tokens:
-// 30.6; 480 workgroups 35.7, five a CU 41.0); no part under 256 tokens (two
-// tiles a wave), or 512 of the prompt kernel, which gets as many workgroups as
-// run at once.  Sequences of up to 1024 tokens, no more than one workgroup a CU,
-// are not divided: 8 waves take one (4 tiles a wave) and no second launch follows
-// (1024 tokens of one sequence: 10.5 against 12.7 us; up to 2048 of 16, 64 dims:
-// 14.3 undivided, 13.4 in parts).
+// tokens: 77.9 us; two a CU 84.6, five 80.5); no part under 256 tokens (two tiles
+// a wave), or 512 of the prompt kernel, which gets as many workgroups as run at
+// once.  Several row tiles of several sequences share their tokens in L2 and are
+// bound by waiting: five workgroups a CU and no part under 512, where three run at
+// once (12 sequences of up to 6000 tokens, 5 new ones each, 40 heads on 8, two
+// groups a head: 29.0 us; four a CU 30.6, two and a half 36.9, six 32.1; but 38.5
+// against 32.5 for 256 dims, of which two run).  Sequences of up to 1024 tokens,
+// no more than one workgroup a CU, are not divided: 8 waves take one (4 tiles a
+// wave) and no second launch follows (1024 tokens of one sequence: 10.5 against
+// 12.7 us; up to 2048 of 16, 64 dims: 14.3 undivided, 13.4 in parts).
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
   a->rows = 16;
-  if (a->dtype != kDtF32) {
-    if (rows > 32 && a->dtype == kDtBf16) a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
-    else if (rows > 16 && a->c.dim <= 128) a->rows = 32;
-  }
+  if (rows > 32 && a->dtype == kDtBf16) a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
+  if (a->dtype == kDtF16 && a->c.dim <= 128 && (int64_t)a->batch * a->c.heads * ((rows + 31) / 32) >= 512) a->rows = 32;
   a->tiles = (int)((rows + a->rows - 1) / a->rows);
   int64_t span = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
   const int64_t segments = (int64_t)a->batch * a->c.heads * a->tiles;
-  const int64_t least = a->rows >= 128 ? 512 : 256;
-  int64_t want = a->rows == 256 ? 256 : a->rows == 128 || a->batch == 1 ? 512 : 640;
+  const int prec = a->dtype == kDtBf16 ? kForBf16 : a->dtype == kDtF16 ? kForF16 : kForF32;
+  const bool several = a->rows == 16 && a->tiles > 1 && kv4_attn_waves(a->c.dim, a->c.group != a->c.dim, 16, prec) == 3;
+  const int64_t least = a->rows >= 128 || several ? 512 : 256;
+  int64_t want = a->rows == 256 ? 256 : a->rows == 128 || a->batch == 1 ? 512 : several ? 1280 : 640;
   a->waves = 4;
   if (a->rows == 16 && segments <= 256 && span <= 1024) {
     a->waves = 8;
@@ -683,7 +689,7 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
 
 template <int D, bool GROUPS, int PREC>
 static void attn2(const Kv4AttnArgs& a, hipStream_t s) {
-  constexpr int MORE = D <= 128 && PREC != kForF32 ? 32 : 16;
+  constexpr int MORE = D <= 128 && PREC == kForF16 ? 32 : 16;
   const dim3 g((unsigned)a.groups);
   if (a.waves == 8) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, 16, 8>), g, dim3(512), 0, s, a);
   else if (a.rows == MORE) hipLaunchKernelGGL((kv4_attn_kernel<D, GROUPS, PREC, MORE, 4>), g, dim3(256), 0, s, a);

@@ -269,6 +269,15 @@ def test_several_new_tokens(news, causal, dim, group, dtype):
     _attend(f, rng, news, 4, dtype, causal=causal)
 
 
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (128, 64)])
+def test_fp16_prompt(dim, group):
+    """Enough rows of two sequences to fill the chip 32 at a time; the first in two parts."""
+    rng = _rng(dim + group)
+    f = Filled(rng, [700, 290], 8, dim, group, 32, True)
+    _attend(f, rng, [255, 131], 32, "f16")
+    _attend(f, rng, [390, 131], 32, "f16")
+
+
 @pytest.mark.parametrize("lens,news", [([3, 0, 40], [10, 4, 40]), ([1], [33]), ([100], [160])])
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 def test_rows_that_see_nothing(lens, news, dtype):
