@@ -37,12 +37,12 @@
 // the fp16 work, the exponentials and the LDS reads the rest of the loop takes
 // 199 of 290 us (2048 tokens, 32 heads on 8, 128 dims, over 8192; 4 waves), which
 // is the rate of a large library product; making fp16 costs 65 of it (8 waves
-// halve that), the LDS reads 22, the exponentials 16.  With 8 waves 275 us, 0.87
+// halve that), the LDS reads 22, the exponentials 16.  With 8 waves 272 us, 0.88
 // PFLOP/s where a large library product reaches 1.23.
 // At 64 dims a score costs half the products and the same softmax, and vector
 // instructions bind it: 210 a tile and wave (32 exponentials of 16 cycles among
 // them) beside 16 matrix ones of 32.  6 ragged sequences of up to 1500 tokens, a
-// window of 1024: 89 us.  Outputs used to go through LDS, 16 rows at a time; turned
+// window of 1024: 94 us a call.  Outputs used to go through LDS, 16 rows at a time; turned
 // back in registers like the queries they cost 700 fewer instructions a wave, 94.4
 // against 98.4 us a call.
 //
