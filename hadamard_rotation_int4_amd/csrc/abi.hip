@@ -10,6 +10,7 @@
 
 #include "hr.h"
 #include "hr_internal.h"
+#include "kv4.h"
 
 namespace {
 

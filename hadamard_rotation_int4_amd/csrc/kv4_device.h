@@ -20,7 +20,7 @@
 #pragma once
 
 #include "hr_device.h"
-#include "hr_internal.h"
+#include "kv4.h"
 #include "fwht2048.h"
 
 namespace hr {
