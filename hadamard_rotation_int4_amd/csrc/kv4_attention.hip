@@ -636,13 +636,20 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 // makes two workgroups a CU (the codes of a tile are then made fp16 once for
 // both halves: 1024 tokens, 32 heads on 8, over 4096 197 against 224 us; where
 // there are fewer, twice the workgroups wait less: 64 sequences of 3 new tokens,
-// 64 heads on 8, 48 against 60); past 32 bf16 ones, 128 of the prompt kernel, or
-// 256 of it for 128 dims and more than 128 rows (2048 tokens, 32 heads on 8, over
-// 8192: 276 against 292 us; 64 dims lose the third workgroup a CU, 127 against
-// 101 us, and 256 dims the registers).  The prompt kernel's keys and values are
-// rounded to fp16, which an fp16 output would show (its error 5.5e-4 where the
-// rounding of the output alone is 2.1e-4, against 2.4e-4 here, at 372 against
-// 446 us).
+// 64 heads on 8, 48 against 60).
+//
+// bf16 calls of more than 64 rows a key/value head and enough work take the
+// prompt kernel, whose fewer, larger workgroups cost less a score but start
+// later: enough is 16-row tiles times tokens past 8192 dim (32 heads on 8 of 128
+// dims, prompt kernel against 16 rows: 4 sequences, 64 new tokens over 4000 43
+// against 50 us; 1 of 256 over 2048 43 against 26, 1 of 512 alone 30 against 16, 1
+// of 64 over 8192 45 against 32; 64 dims, 4 of 32 over 4000 22 against 26, 1 of 32
+// over 8192 22 against 18; up to 64 rows, 64 sequences of 10 new tokens 150 against
+// 74).  128 rows of it, or 256 for 128 dims and more than 128 rows (2048 tokens
+// over 8192: 276 against 292 us; 64 dims lose the third workgroup a CU, 127 against
+// 101 us, and 256 dims the registers).  Its keys and values are rounded to fp16,
+// which an fp16 output would show (its error 5.5e-4 where the rounding of the
+// output alone is 2.1e-4, against 2.4e-4 here, at 372 against 446 us).
 //
 // Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
@@ -659,13 +666,15 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 // 12.7 us; up to 2048 of 16, 64 dims: 14.3 undivided, 13.4 in parts).
 void kv4_attention_plan(Kv4AttnArgs* a) {
   const int64_t rows = (int64_t)a->max_new * a->rep;
-  a->rows = 16;
-  if (rows > 32 && a->dtype == kDtBf16) a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
-  if (a->dtype == kDtF16 && a->c.dim <= 128 && (int64_t)a->batch * a->c.heads * ((rows + 31) / 32) >= 512) a->rows = 32;
-  a->tiles = (int)((rows + a->rows - 1) / a->rows);
   int64_t span = a->max_len;
   if (a->window > 0 && (int64_t)a->window + a->max_new + 31 < span) span = (int64_t)a->window + a->max_new + 31;
-  const int64_t segments = (int64_t)a->batch * a->c.heads * a->tiles;
+  const int64_t pairs = (int64_t)a->batch * a->c.heads;
+  a->rows = 16;
+  if (a->dtype == kDtBf16 && rows > 64 && pairs * ((rows + 15) / 16) > 8192 * (int64_t)a->c.dim / (span > 0 ? span : 1))
+    a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
+  if (a->dtype == kDtF16 && a->c.dim <= 128 && pairs * ((rows + 31) / 32) >= 512) a->rows = 32;
+  a->tiles = (int)((rows + a->rows - 1) / a->rows);
+  const int64_t segments = pairs * a->tiles;
   const int prec = a->dtype == kDtBf16 ? kForBf16 : a->dtype == kDtF16 ? kForF16 : kForF32;
   const bool several = a->rows == 16 && a->tiles > 1 && kv4_attn_waves(a->c.dim, a->c.group != a->c.dim, 16, prec) == 3;
   const int64_t least = a->rows >= 128 || several ? 512 : 256;

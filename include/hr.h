@@ -559,7 +559,7 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  * (window > 0); 0 for a row that sees none.
  * Sums and softmax statistics are fp32.  For bf16 rows, queries and
  * probabilities are rounded to fp16, and so are scaled keys and values where a
- * head has several groups or a call more than 32 rows a key/value head: a score
+ * head has several groups or a call many rows: a score
  * is good to 2^-11 of its terms' sizes.  For fp16 and fp32 rows they are held in
  * more bits than the output shows.
  *

@@ -358,6 +358,61 @@ def test_sizes_of_queries(qsize):
     _close(_num(out), f.want(_num(q), np.array([0, 1]), 0.088 / qsize), TOL["bf16"])
 
 
+# A max_len far above the sequences' lengths makes a call's work look large: many rows then take the form for prompts
+# whatever their number of tokens.
+FAR = 1 << 20
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 128),
+                                       (256, 256)])
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("news", [[70], [40, 64, 20], [130, 200, 129], [1, 0, 97]])
+def test_prompt_types(dim, group, rotate, news):
+    rng = _rng(dim + group + len(news))
+    f = Filled(rng, [n + int(rng.integers(0, 300)) for n in news], 2, dim, group, 16, rotate)
+    _attend(f, rng, news, 4, "bf16", max_len=FAR, extra=64)
+
+
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("window", [0, 1, 31, 64, 100, 5000])
+@pytest.mark.parametrize("dim,rep", [(128, 3), (64, 1), (128, 17)])
+def test_prompt_masks(causal, window, dim, rep):
+    rng = _rng(window + rep)
+    f = Filled(rng, [150, 333, 90], 2, dim, dim, 64, True)
+    _attend(f, rng, [70, 150, 90], 2 * rep, "bf16", causal, window, max_len=FAR)
+
+
+@pytest.mark.parametrize("lens,news", [([3, 0, 40], [80, 90, 40]), ([33], [133]), ([100], [160])])
+def test_prompt_rows_that_see_nothing(lens, news):
+    rng = _rng(12)
+    f = Filled(rng, lens, 2, 128, 64, 16, True)
+    out, _, starts = _attend(f, rng, news, 4, "bf16", max_len=FAR)
+    for b, n in enumerate(lens):
+        if news[b] > n:
+            assert not _num(out)[starts[b]:starts[b] + news[b] - n].any()
+
+
+@pytest.mark.parametrize("dim", [64, 128, 256])
+def test_prompt_poisoned_token(dim):
+    rng = _rng(13)
+    f = Filled(rng, [200], 2, dim, dim, 16, True)
+    place = f.table[0, 170 // 16], 1, slice(None), 170 % 16
+    for kv, t in ((0, f.cache.k_scales), (1, f.cache.v_scales)):
+        t[place] = float("nan")
+        f.scales[kv][place] = np.nan
+    out, _, _ = _attend(f, rng, [150], 4, "bf16", max_len=FAR)
+    out = _num(out)
+    assert np.isnan(out[-1, 2:]).all() and np.isfinite(out[:, :2]).all() and np.isfinite(out[:120]).all()
+
+
+@pytest.mark.parametrize("dim,batch,news,n", [(128, 1, 600, 3600), (64, 2, 300, 2000), (256, 1, 600, 4200),
+                                              (128, 9, 24, 2500)])
+def test_prompt_split_over_the_tokens(dim, batch, news, n):
+    rng = _rng(14)
+    f = Filled(rng, [n - 7 * b for b in range(batch)], 2, dim, dim, 64, True)
+    _attend(f, rng, [news] * batch, 8, "bf16")
+
+
 @pytest.mark.parametrize("dim", [64, 128, 256])
 @pytest.mark.parametrize("news", [40, 150])
 def test_prompt_rows_of_different_sizes(dim, news):
@@ -367,8 +422,9 @@ def test_prompt_rows_of_different_sizes(dim, news):
     q = rng.standard_normal((news, 4, dim)) * rng.choice([1e6, 1.0, 1e-6, 0.0], (news, 4, 1))
     q = _t(q.astype(np.float32)).to(torch.bfloat16)
     starts = np.array([0, news], dtype=np.int32)
-    out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news)
-    _close(_num(out), f.want(_num(q), starts), TOL["bf16"])
+    for bound in (None, FAR):
+        out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news, max_len=bound)
+        _close(_num(out), f.want(_num(q), starts), TOL["bf16"])
 
 
 @pytest.mark.parametrize("dim", [64, 128, 256])
@@ -394,9 +450,10 @@ def test_running_maximum_far_from_zero(dim, side, news):
     q = _t(q.astype(np.float32)).to(torch.bfloat16)
     table, lens = np.arange(pages, dtype=np.int32)[None], np.array([n], dtype=np.int32)
     starts = np.array([0, news], dtype=np.int32)
-    out = hr.kv4_attention(cache, q, _t(table), _t(lens), starts=_t(starts), max_new=news)
     want = oracle.kv4.attention(_num(q), vals[0], vals[1], table, lens, starts, dim ** -0.5, None, False, True, 0)
-    _close(_num(out), want, TOL["bf16"])
+    for bound in (None, FAR):
+        out = hr.kv4_attention(cache, q, _t(table), _t(lens), starts=_t(starts), max_new=news, max_len=bound)
+        _close(_num(out), want, TOL["bf16"])
 
 
 def test_append_then_attend_end_to_end():
