@@ -10,7 +10,7 @@
 // The rotation is orthogonal, so this is attention over the keys and values
 // that the cache stands for, without ever rotating them back.
 //
-// kv4_attn_kernel.  One workgroup of 4 or 8 waves takes 16 query rows of one
+// kv4_attn_kernel.  One workgroup of 4 or 8 waves takes 16 (or 32) query rows of one
 // (sequence, key/value head) -- the rep heads that share it times the new
 // tokens -- and one part of the token axis; its waves take 32-token tiles in
 // turn.  Both products are 16x16x32 matrix instructions in the transposed form

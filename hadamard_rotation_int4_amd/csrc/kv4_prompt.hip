@@ -1,7 +1,7 @@
 // Attention over the 4-bit key/value cache for many query rows (prompts and
 // chunks of prompts), bf16 queries.  The mathematics is kv4_attention.hip's;
 // here it is the matrix products that count, so a workgroup shares each tile's
-// codes-to-fp16 work among 128 query rows through LDS.
+// codes-to-fp16 work among 128 or 256 query rows through LDS.
 //
 // One workgroup of 4 or 8 waves takes 32 query rows a wave of one (sequence,
 // key/value head), row = new token * rep + head of the group, and walks over
