@@ -649,6 +649,10 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
   return from_hip(hr::launch_kv4_read(a, static_cast<hipStream_t>(stream)), fn);
 }
 
+// A window past every cached length hides nothing.  Without it the kernels' 32-bit positions cannot wrap: a first
+// visible token that did would lead to page ids read far outside the table.
+static int32_t kv4_window(int32_t window) { return window < hr::kKv4MaxLen ? window : 0; }
+
 // Workspace of a planned call: partial sums, then (max, sum) pairs.
 static int64_t kv4_workspace(const hr::Kv4AttnArgs& a) {
   return a.nsplit > 1 ? a.total * a.q_heads * a.nsplit * (4 * (int64_t)a.c.dim + 8) : 0;
@@ -668,7 +672,7 @@ int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, in
   a.rep = q_heads / heads;
   a.max_new = max_new;
   a.max_len = max_len;
-  a.window = window;
+  a.window = kv4_window(window);
   // the plan also looks at whether a head has several scale groups: enough for either
   int64_t need = 0;
   for (int group : {dim, dim / 2}) {
@@ -726,7 +730,7 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
   a.max_len = max_len;
   a.scale = scale;
   a.causal = causal;
-  a.window = window;
+  a.window = kv4_window(window);
   a.out = out;
   hr::kv4_attention_plan(&a);
   if (a.groups > (1 << 22))

@@ -37,7 +37,8 @@ struct Kv4Seq {
     news = s1 - s0;
     rows = news * p.rep;
   }
-  // new token n sees tokens [lo(n), hi(n)); both grow with n
+  // new token n sees tokens [lo(n), hi(n)); both grow with n.  In 32 bits: the host keeps windows and lengths to 2^30
+  // and new tokens to 2^26.
   __device__ __forceinline__ int lo(int n) const {
     const int v = len - news + n - window + 1;
     return window > 0 && v > 0 ? v : 0;

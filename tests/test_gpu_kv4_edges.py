@@ -1,0 +1,84 @@
+"""The 4-bit key/value cache on the GPU where the other tests of it do not reach: masks and arguments at the ends of
+their ranges, softmax weights and values far apart, and every form of the attention kernels over many tokens.
+
+Tolerances are those of test_gpu_kv4.py, whose oracle and comparison are used here too; what a test allows beyond them
+is derived in its docstring.
+"""
+import numpy as np
+import pytest
+import torch
+
+import hadamard_rotation_int4_amd as hr
+import oracle
+from test_gpu_kv4 import DEV, FAR, TOL, TYPES, Filled, _attend, _close, _num, _rng, _t
+
+pytestmark = pytest.mark.gpu
+
+
+class Held:
+    """A cache (one sequence, pages in any order) that holds the given keys and values, fp32 [tokens][heads][dim],
+    quantized without a rotation."""
+
+    def __init__(self, rng, k, v, group, page):
+        n, heads, dim = k.shape
+        pages = -(-n // page)
+        self.table = rng.permutation(pages).astype(np.int32)[None]
+        self.lens = np.array([n], dtype=np.int32)
+        self.heads, self.dim = heads, dim
+        j = np.arange(n)
+        at = self.table[0, j // page], slice(None), j % page
+        parts, self.vals = [], []
+        for x in (k, v):
+            q, s = oracle.kv4.quantize_plain(x.astype(np.float32), group)
+            codes = np.zeros((pages, heads, page, dim // 2), dtype=np.uint8)
+            scales = np.zeros((pages, heads, dim // group, page), dtype=np.float16)
+            codes[at] = oracle.quant.pack_int4(q.reshape(-1, dim)).reshape(n, heads, dim // 2)
+            scales[self.table[0, j // page], :, :, j % page] = s
+            parts += [_t(codes), _t(scales)]
+            self.vals.append(oracle.kv4.values(codes, scales))
+        self.cache = hr.KV4Cache(*parts, rotate=False)
+
+    def attend(self, q, **kw):
+        """(got, want) of the last q.shape[0] tokens' queries."""
+        starts = np.array([0, len(q)], dtype=np.int32)
+        out = hr.kv4_attention(self.cache, q, _t(self.table), _t(self.lens), starts=_t(starts), max_new=len(q), **kw)
+        kw.pop("max_len", None)
+        scale = kw.pop("scale", self.dim ** -0.5)
+        return _num(out), dense(_num(q), *self.vals, self.table, self.lens, starts, scale, None, False, **kw)
+
+
+def dense(q, kvals, vvals, table, lens, starts, scale, signs=None, rotated=True, causal=True, window=0):
+    """oracle.kv4.attention with whole matrices of scores, for many rows (finite values only)."""
+    q = np.asarray(q, dtype=np.float64)
+    rep = q.shape[1] // kvals.shape[1]
+    qr = oracle.kv4.rotate(q, signs) if rotated else q
+    out = np.zeros_like(q)
+    for b, n in enumerate(int(n) for n in lens):
+        s0, s1 = int(starts[b]), int(starts[b + 1])
+        if n == 0 or s0 == s1:
+            continue
+        k, v = oracle.kv4.gather(kvals, table[b], n), oracle.kv4.gather(vvals, table[b], n)
+        pos, j = n - (s1 - s0) + np.arange(s1 - s0)[:, None], np.arange(n)
+        see = np.ones((s1 - s0, n), dtype=bool)
+        if causal:
+            see &= j <= pos
+        if window:
+            see &= j > pos - window
+        some = see.any(1)
+        for h in range(q.shape[1]):
+            z = np.where(see, scale * (qr[s0:s1, h] @ k[h // rep].T), -np.inf)
+            p = np.exp(z - np.where(some, z.max(1), 0.0)[:, None])
+            out[s0:s1, h] = p @ v[h // rep] / np.where(some, p.sum(1), 1.0)[:, None]
+    return oracle.kv4.unrotate(out, signs) if rotated else out
+
+
+@pytest.mark.parametrize("window", [2 ** 30 - 1, 2 ** 30, 2 ** 31 - 1])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("lens,news", [([5], [16]), ([3, 40, 0], [10, 4, 9]), ([33, 100], [133, 160])])
+def test_window_that_hides_nothing(window, causal, lens, news):
+    """The largest windows hide nothing, also from rows whose positions are negative."""
+    rng = _rng(21)
+    f = Filled(rng, lens, 2, 128, 128, 16, True)
+    for dtype in ("bf16", "f32"):
+        _attend(f, rng, news, 4, dtype, causal=causal, window=window)
+    _attend(f, rng, news, 4, "bf16", causal=causal, window=window, max_len=FAR)
