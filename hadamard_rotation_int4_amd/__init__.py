@@ -15,6 +15,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import operator
 import os
 
 import torch
@@ -707,6 +708,20 @@ def _kv4_ptr(cache, t, name: str) -> int:
     return t.data_ptr()
 
 
+_I32_MAX, _I64_MAX = 2 ** 31 - 1, 2 ** 63 - 1
+
+
+def _kv4_size(v, name: str, most: int) -> int:
+    """An integer of the C call's range: ctypes would cut off what does not fit."""
+    try:
+        n = operator.index(v)
+    except TypeError:
+        raise TypeError(f"{name}: expected an integer, got {type(v).__name__}") from None
+    if not 0 <= n <= most:
+        raise ValueError(f"{name}: {n} outside [0, {most}]")
+    return n
+
+
 # A size of sizes: step after step asks for the same.
 @functools.lru_cache(maxsize=256)
 def _kv4_workspace(*sizes) -> int:
@@ -824,6 +839,11 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
         max_len = min(width * cache.page, 1 << 30)
     if scale is None:
         scale = cache.dim ** -0.5
+    if not (type(max_new) is type(max_len) is type(window) is int and 0 <= max_new <= _I32_MAX and 0 <= max_len <= _I64_MAX
+            and 0 <= window <= _I32_MAX):
+        max_new = _kv4_size(max_new, "max_new", _I32_MAX)
+        max_len = _kv4_size(max_len, "max_len", _I64_MAX)
+        window = _kv4_size(window, "window", _I32_MAX)
     code = _KV4_TYPES[dtype]
     need = _kv4_workspace(cache.heads, cache.dim, code, total, batch, q_heads, max_new, max_len, window)
     if out is not None:

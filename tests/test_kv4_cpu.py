@@ -217,6 +217,18 @@ def test_binding_argument_checks():
         hr.kv4_attention(c, q, table, lens, out=q)
 
 
+@pytest.mark.parametrize("name,value,err", [
+    (name, value, err) for name, bits in (("window", 31), ("max_new", 31), ("max_len", 63))
+    for value, err in ((2 ** (bits + 1) + 5, ValueError), (2 ** (bits + 1), ValueError), (2 ** bits, ValueError),
+                       (-1, ValueError), (1.5, TypeError), ("1", TypeError))])
+def test_binding_integer_ranges(name, value, err):
+    """Sizes past the C types are refused, not cut to them."""
+    q = torch.zeros((3, 4, 64), dtype=torch.bfloat16)
+    table, lens = torch.zeros((3, 2), dtype=torch.int32), torch.zeros(3, dtype=torch.int32)
+    with pytest.raises(err, match=name):
+        hr.kv4_attention(_Stub(), q, table, lens, **{name: value})
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_oracle_rotation_is_orthogonal():
