@@ -26,14 +26,17 @@ struct Kv4Seq {
     const int cap32 = cap < kKv4MaxLen ? (int)cap : kKv4MaxLen;
     len = read_index(p.lens, b);
     len = len < 0 ? 0 : len > cap32 ? cap32 : len;
-    s0 = b * p.max_new;
-    int s1 = s0 + p.max_new;
+    int s1;
     if (p.starts) {
       s0 = read_index(p.starts, b);
       s1 = read_index(p.starts, b + 1);
+    } else {
+      s0 = b * p.max_new;
+      s1 = s0 + p.max_new;
     }
     if (s0 < 0) s0 = 0;
     if (s1 > (int)p.total) s1 = (int)p.total;
+    if (s1 < s0) s1 = s0;        // and s1 - s0 cannot wrap
     news = s1 - s0;
     rows = news * p.rep;
   }

@@ -567,7 +567,8 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  *             HR_F16), rows q_stride elements apart (at least q_heads * dim; a
  *             multiple of 16 bytes).
  *   starts    [batch + 1] int32, not decreasing, or NULL: max_new rows each
- *             (total = batch * max_new).
+ *             (total = batch * max_new).  A sequence that ends before it
+ *             starts has no rows; no row outside [0, total) is touched.
  *   table     [batch][width] int32 page ids; only entries of cached tokens are
  *             used.  An id outside [0, pages) is read as 0.
  *   lens      [batch] int32 (device), at most width * page.

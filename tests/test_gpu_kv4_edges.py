@@ -82,3 +82,18 @@ def test_window_that_hides_nothing(window, causal, lens, news):
     for dtype in ("bf16", "f32"):
         _attend(f, rng, news, 4, dtype, causal=causal, window=window)
     _attend(f, rng, news, 4, "bf16", causal=causal, window=window, max_len=FAR)
+
+
+@pytest.mark.parametrize("starts", [[4, -2 ** 31], [2 ** 31 - 1, 6], [2 ** 31 - 1, -2 ** 31], [5, 2], [-3, 0]])
+@pytest.mark.parametrize("n,bound", [(100, None), (4000, None), (100, FAR)])
+def test_starts_that_hold_no_rows(starts, n, bound):
+    """Starts that decrease or lie outside the queries: nothing is read or written for them."""
+    rng = _rng(27)
+    f = Filled(rng, [n], 1, 128, 128, 64, True)
+    for dtype in ("bf16", "f32"):
+        q = _t(rng.standard_normal((6, 4, 128)).astype(np.float32)).to(TYPES[dtype])
+        out = torch.full_like(q, 7.0)
+        for max_new in (1, 100):
+            hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=torch.tensor(starts, dtype=torch.int32, device=DEV),
+                             max_new=max_new, max_len=bound, out=out)
+            assert (out == 7.0).all()
