@@ -555,6 +555,10 @@ int32_t hr_w4a4_gemm_fp6(const uint8_t* a_f6, const void* a_scales, const uint8_
   return from_hip(hr::launch_gemm_fp6(a, static_cast<hipStream_t>(stream)), fn);
 }
 
+// Vectors of one call: a launch holds fewer than 2^32 threads.
+constexpr int64_t kKv4MaxVectors = int64_t(1) << 26;
+constexpr int32_t kKv4MaxHeads = 65535, kKv4MaxBatch = 65535;
+
 // Checks a cache description and fills the internal one.  The arrays may be
 // NULL only when no token is touched (`need` false).
 static int32_t kv4_cache(const char* fn, const hr_kv4_cache* c, bool need, hr::Kv4Cache* out) {
@@ -572,7 +576,7 @@ static int32_t kv4_cache(const char* fn, const hr_kv4_cache* c, bool need, hr::K
     return fail(HR_EUNSUPPORTED, "%s: group=%d invalid for dim=%d", fn, c->group, c->dim);
   if (!pow2(c->page) || c->page < 16 || c->page > (1 << 20))
     return fail(HR_EUNSUPPORTED, "%s: page=%d is not a power of two in [16, 2^20]", fn, c->page);
-  if (c->heads < 1 || c->heads > 65535)
+  if (c->heads < 1 || c->heads > kKv4MaxHeads)
     return fail(HR_EUNSUPPORTED, "%s: heads=%d outside [1, 65535]", fn, c->heads);
   if (c->pages > INT32_MAX) return fail(HR_EUNSUPPORTED, "%s: more than 2^31 - 1 pages", fn);
   *out = hr::Kv4Cache{};
@@ -589,9 +593,6 @@ static int32_t kv4_cache(const char* fn, const hr_kv4_cache* c, bool need, hr::K
   out->rotate = c->rotate;
   return HR_OK;
 }
-
-// Vectors of one call: a launch holds fewer than 2^32 threads.
-constexpr int64_t kKv4MaxVectors = int64_t(1) << 26;
 
 static bool kv4_dtype(int32_t dt) { return dt == HR_F32 || dt == HR_BF16 || dt == HR_F16; }
 
@@ -660,7 +661,10 @@ static int64_t kv4_workspace(const hr::Kv4AttnArgs& a) {
 
 int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, int64_t total, int32_t batch,
                                    int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window) {
-  if (heads < 1 || dim < 1 || total < 1 || batch < 1 || q_heads < heads || max_new < 1 || max_len < 0 || window < 0)
+  // nothing that the call itself refuses: the plan's products then stay in 64 bits
+  if (heads < 1 || heads > kKv4MaxHeads || (dim != 64 && dim != 128 && dim != 256) || !kv4_dtype(dtype) || q_heads < 1 ||
+      q_heads % heads || total < 1 || total > kKv4MaxVectors / q_heads || batch < 1 || batch > kKv4MaxBatch || max_new < 1 ||
+      max_new > kKv4MaxVectors / q_heads || max_len < 0 || max_len > hr::kKv4MaxLen || window < 0)
     return 0;
   hr::Kv4AttnArgs a{};
   a.c.heads = heads;
@@ -712,7 +716,8 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
     return fail(HR_EINVAL, "%s: without starts, total must be batch * max_new", fn);
   if (total > kKv4MaxVectors / q_heads || max_new > kKv4MaxVectors / q_heads)
     return fail(HR_EUNSUPPORTED, "%s: rows * q_heads above 2^26", fn);
-  if (batch > 65535) return fail(HR_EUNSUPPORTED, "%s: batch=%d above 65535", fn, batch);
+  if (batch > kKv4MaxBatch) return fail(HR_EUNSUPPORTED, "%s: batch=%d above %d", fn, batch, kKv4MaxBatch);
+  if (width > INT32_MAX) return fail(HR_EUNSUPPORTED, "%s: width above 2^31 - 1", fn);
   if (max_len > hr::kKv4MaxLen) return fail(HR_EUNSUPPORTED, "%s: max_len above 2^30", fn);
   if (!some || max_new == 0) return ok();
   a.q = q;

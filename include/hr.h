@@ -573,9 +573,13 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  *             used.  An id outside [0, pages) is read as 0.
  *   lens      [batch] int32 (device), at most width * page.
  *   q_heads   a multiple of heads; total * q_heads is at most 2^26.
+ *             batch is at most 65535, width at most 2^31 - 1.
  *   max_new, max_len  upper bounds of a sequence's query rows and cached
  *             length, for the launch; rows past max_new are not computed.  A
- *             max_len below a sequence's length costs time only.
+ *             max_len below a sequence's length costs time only.  max_new *
+ *             q_heads is at most 2^26, max_len at most 2^30; a call of
+ *             more than 2^22 workgroups is refused (none is with up to 2^22
+ *             times 16 rows, max_new * q_heads / heads of each sequence and head).
  *   scale     multiplies q . k; 1 / sqrt(dim) usually.
  *   causal    0 or 1;  window >= 0 (0: none).
  *   out       [total][q_heads][dim] of dtype; rows of no sequence are left.
@@ -589,7 +593,7 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
                          void* stream);
 
 /* Bytes of workspace of an hr_kv4_attention call of these sizes (0: none;
- * negative sizes give 0). */
+ * sizes that the call refuses give 0). */
 int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, int64_t total, int32_t batch,
                                    int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window);
 

@@ -229,6 +229,21 @@ def test_binding_integer_ranges(name, value, err):
         hr.kv4_attention(_Stub(), q, table, lens, **{name: value})
 
 
+def test_workspace_of_sizes_the_call_refuses():
+    f = hr.lib.hr_kv4_attention_workspace
+    top32, top64 = 2 ** 31 - 1, 2 ** 63 - 1
+    for bad in ((1, 128, 1, 1 << 62, 1, 1, 1, 1 << 30, 0), (1, 128, 1, 1, 1, 1, 1, top64, 0),
+                (top32, 128, 1, 1, top32, top32, top32, 1 << 20, 0), (1, top32, 1, 1, 1, 1, 1, 1 << 20, 0),
+                (1, 128, 1, 1, 1, 1, top32, 1 << 20, 0), (1, 128, 7, 1, 1, 1, 1, 1 << 20, 0),
+                (2, 128, 1, 1, 1, 3, 1, 1 << 20, 0)):
+        assert f(*bad) == 0
+
+
+def test_attention_width_past_32_bits():
+    assert _attend(width=1 << 31) == hr.HR_EUNSUPPORTED
+    assert _attend(width=1 << 62) == hr.HR_EUNSUPPORTED
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_oracle_rotation_is_orthogonal():
