@@ -273,7 +273,9 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
     u = umax_dpp<kQuadXor2>(u);
     u = umax_dpp<kRowHalfMirror>(u);
     const int ex = row_exponent(__uint_as_float(umax_dpp<kRowMirror>(u)));
-    if ((lane & 15) == 0) l_lds[rt][qrow] = ldexpf(p.scale * kLog2e, ex);
+    // never 0, which would make NaN of a masked score; products of [1, 2) with keys are far below 2^100, so a factor
+    // this small makes all of them 0
+    if ((lane & 15) == 0) l_lds[rt][qrow] = fmaxf(ldexpf(p.scale, ex) * kLog2e, 0x1p-126f);
     // dim d of a row at place 8 (d / 8) + (the e with kOrder[e] = d % 8)
     constexpr int EN = NC < 8 ? NC : 8;
 #pragma unroll

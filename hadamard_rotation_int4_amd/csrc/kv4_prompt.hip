@@ -276,7 +276,13 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     const int64_t at = (int64_t)(q.s0 + n_mine) * p.q_stride + q_head * D;
 #pragma unroll
     for (int c = 0; c < NC; ++c) load_vec<kDtBf16, 8>(reinterpret_cast<const uint16_t*>(p.q) + at + 16 * c + 8 * h, w + 8 * c);
-    float norm = p.scale * kLog2e;
+    float norm = p.scale;
+    if (norm > 0x1p60f) {        // goes with tiny queries: half of it to them, so that no factor overflows
+#pragma unroll
+      for (int e = 0; e < E; ++e) w[e] *= 0x1p64f;
+      norm *= 0x1p-64f;
+    }
+    norm *= kLog2e;
     if (p.c.rotate) {
 #pragma unroll
       for (int c = 0; c < NC; ++c) {
@@ -293,9 +299,11 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     for (int e = 0; e < E; ++e) mx = fmaxf(mx, fabsf(w[e]));
     const auto s = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
     // in log2 units they are fp16 numbers as they are, but for rows that would leave its normal range: those by a
-    // power of two, made good at the scores
-    const float top = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])) * fabsf(norm);
-    const int ex = top > 0x1p-10f && top < 0x1p15f ? 0 : row_exponent(top);
+    // power of two, made good at the scores (of 2^-62 at least: rows smaller than that have no scores to tell apart, and
+    // neither factor may become 0 or infinite)
+    const float top = fmaxf(__uint_as_float(s[0]), __uint_as_float(s[1])) * norm;
+    int ex = top > 0x1p-10f && top < 0x1p15f ? 0 : row_exponent(top);
+    if (ex < -62) ex = -62;
     qs = ldexpf(1.0f, ex);
     norm = ldexpf(norm, -ex);
 #pragma unroll

@@ -97,3 +97,23 @@ def test_starts_that_hold_no_rows(starts, n, bound):
             hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=torch.tensor(starts, dtype=torch.int32, device=DEV),
                              max_new=max_new, max_len=bound, out=out)
             assert (out == 7.0).all()
+
+
+@pytest.mark.parametrize("dtype,qsize,scale", [("f32", 1e-42, None), ("f32", 1e-8, 1e-38), ("f32", 1e-45, 1e-3),
+                                               ("bf16", 1e-39, None), ("bf16", 1e-8, 1e-38), ("f16", 1e-7, 1e-38),
+                                               ("bf16", 2e-39, 3e38), ("f32", 2e-39, 3e38)])
+@pytest.mark.parametrize("rotate", [False, True])
+@pytest.mark.parametrize("news", [1, 3, 40])
+def test_tiny_queries_and_scales(dtype, qsize, scale, rotate, news):
+    """Scores that fp32 holds as subnormal numbers or not at all, beside masked ones: every visible token counts alike.
+    Tiny queries under a huge scale are ordinary ones: rotated to 2^-150, scores move by 2^-19.5 (3e38 times 2^-150 /
+    sqrt(3) times 11 for 128 dims)."""
+    rng = _rng(24)
+    f = Filled(rng, [news + 50], 2, 128, 128, 16, rotate)
+    starts = np.array([0, news], dtype=np.int32)
+    q = _t((rng.standard_normal((news, 4, 128)) * qsize).astype(np.float32)).to(TYPES[dtype])
+    want = f.want(_num(q), starts, scale)
+    for bound in (None, FAR):
+        out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news, max_len=bound,
+                               scale=scale)
+        _close(_num(out), want, TOL[dtype])
