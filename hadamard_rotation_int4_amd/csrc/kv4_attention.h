@@ -8,7 +8,10 @@
 namespace hr {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kMaxSlack = 8.0f;    // log2 units the scores may pass the running maximum by
+// Probabilities are fp16 numbers 2^kLift times exp2(score - running maximum): small ones keep their 11 bits down to 2^-25
+// of the largest (17 nats below it), which count where the largest belong to tokens of small values.  Scores may pass the
+// running maximum by kMaxSlack, in log2 units, before it moves; the two together stay within fp16.
+constexpr float kLift = 11.0f, kMaxSlack = 4.0f;
 
 // The query rows of one sequence, and the tokens they see.  Row and token
 // indices fit 32 bits (the host checks); offsets into the cache do not.

@@ -31,17 +31,19 @@
 // 1024 times a power of two, for the nibble above) and subtracting.
 // Scales multiply S (one group a head) or the fp16 keys; values are scaled in
 // fp16.  Sums, the running maximum and the softmax sum are fp32; the
-// probabilities are rounded to fp16 (2^-12, an eighth of a bf16 output's own
-// rounding) and summed as rounded, by a product with ones.
-// The running maximum moves only when some score passes it by 2^8, so most
+// probabilities are rounded to fp16 (2^-12 of those down to 2^-25 of the largest,
+// an eighth of a bf16 output's own rounding; see kLift) and summed as rounded, by a
+// product with ones.
+// The running maximum moves only when some score passes it by 2^4, so most
 // tiles need neither the exchange between lanes nor the rescale.
 //
 // fp16 outputs would show the rounding of the queries and keys (4.5e-4 and 4e-4
 // rms of an output, where its own is 2.1e-4): for fp16 queries these are two
 // fp16 terms each, queries always, keys and values where several groups make a
-// scaled code more than 11 bits (two terms hold it exactly).  fp32 queries do
-// the same, and probabilities in two terms too, lifted by 2^11 so that small
-// ones keep their bits: all products above 2^-22 of the whole are there.
+// scaled code more than 11 bits (two terms hold it exactly).  Probabilities stay
+// one term, whose rounding averages out over the tokens: with it outputs are off by
+// 2.3e-4 to 2.7e-4.  fp32 queries have the two terms too, and probabilities in two
+// terms: all products above 2^-22 of the whole are there.
 //
 // Bound by memory for single tokens: 64 sequences of 1100 to 8192 tokens, 32
 // heads on 8 of 128 dims (311 MB of cache) 74 us, 4.2 TB/s, one of 131071 (138
@@ -186,8 +188,6 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
   constexpr int RT = ROWS / 16;
   constexpr int QT = PREC == kForBf16 ? 1 : 2;     // fp16 terms of a query, and of a scaled code
   constexpr int PT = PREC == kForF32 ? 2 : 1;      // of a probability
-  // log2 units the scores may pass the running maximum by, and what the probabilities are lifted by
-  constexpr float SLACK = PREC == kForF32 ? 4.0f : 8.0f, LIFT = PREC == kForF32 ? 11.0f : 0.0f;
   typedef Tile<D, GROUPS> T;
   __shared__ float o_lds[W][16][LD];
   __shared__ float m_lds[W][16], l_lds[W][16];
@@ -416,7 +416,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
 #pragma unroll
       for (int u = 1; u < 8; ++u) mx = fmaxf(mx, z[u]);
       mx *= qf[rt];
-      if (__builtin_amdgcn_ballot_w64(mx > m[rt] + SLACK)) {
+      if (__builtin_amdgcn_ballot_w64(mx > m[rt] + kMaxSlack)) {
         const float mn = fmaxf(m[rt], max_over_g(mx));
         const float f = mn > m[rt] ? exp2f(m[rt] - mn) : 1.0f;
         m[rt] = mn;
@@ -424,7 +424,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
         for (int c = 0; c < NC; ++c) acc[rt][c] *= f;
         accl[rt] *= f;
       }
-      const float mu = (m[rt] == -__builtin_inff() ? 0.0f : m[rt]) - LIFT;
+      const float mu = (m[rt] == -__builtin_inff() ? 0.0f : m[rt]) - kLift;
       float pr[8];
 #pragma unroll
       for (int u = 0; u < 8; ++u) pr[u] = __builtin_amdgcn_exp2f(fmaf(z[u], qf[rt], -mu));

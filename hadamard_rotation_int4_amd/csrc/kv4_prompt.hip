@@ -18,7 +18,8 @@
 // that scores come out as exponents.  Keys, scaled, and queries are rounded to
 // fp16: a score is good to 2^-11 of its terms' sizes (of keys that are all alike
 // the rounding does not average out), where the row kernel holds keys of one
-// group exactly.
+// group exactly.  Probabilities are fp16 too, 2^-12 of those down to 2^-25 of the
+// largest (kLift).
 //
 // LDS holds scaled fp16, in 16-byte pieces that a wave reads contiguously:
 //   keys    [dim / 8][64 tokens] pieces of 8 dims (in nibble order; the
@@ -318,7 +319,7 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
   for (int db = 0; db < NB; ++db)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[db][r] = 0.0f;
-  // scores are made relative to the running maximum m; with nothing seen yet, to 0
+  // scores are made relative to m, the running maximum less kLift; with nothing seen yet, to 0
   float m = 0.0f, slack = -__builtin_inff(), l = 0.0f;
   f32x16 minus;
 #pragma unroll
@@ -378,9 +379,9 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
       const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(mx), __float_as_uint(mx), false, false);
       const float up = fmaxf(__uint_as_float(sw[0]), __uint_as_float(sw[1]));
       const bool first = slack < 0.0f, some = up > -__builtin_inff();
-      const float by = first ? (some ? up : 0.0f) : fmaxf(up, 0.0f);
+      const float by = first ? (some ? up - kLift : 0.0f) : fmaxf(up - kLift, 0.0f);
       const float f = first ? 1.0f : exp2f(-by);
-      if (some) slack = kMaxSlack;
+      if (some) slack = kLift + kMaxSlack;
       m += by;
       l *= f;
 #pragma unroll

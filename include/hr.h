@@ -557,11 +557,12 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  *   out = sum_j softmax_j(scale q . k_j) v_j
  * over the tokens j < lens[b] with j <= pos (causal) and j > pos - window
  * (window > 0); 0 for a row that sees none.
- * Sums and softmax statistics are fp32.  For bf16 rows, queries and
- * probabilities are rounded to fp16, and so are scaled keys and values where a
- * head has several groups or a call many rows: a score
- * is good to 2^-11 of its terms' sizes.  For fp16 and fp32 rows they are held in
- * more bits than the output shows.
+ * Sums and softmax statistics are fp32.  Probabilities are rounded to fp16
+ * (2^-12; those below 2^-25 of the largest, 17 nats, lose bits).  For bf16 rows
+ * queries are too, and scaled keys and values where a head has several groups
+ * or a call many rows: a score is good to 2^-11 of its terms' sizes.  fp16 rows
+ * hold queries, keys and values in more bits than the output shows, fp32 rows
+ * the probabilities as well.
  *
  *   q         [total] rows of [q_heads][dim] of dtype (HR_F32, HR_BF16 or
  *             HR_F16), rows q_stride elements apart (at least q_heads * dim; a

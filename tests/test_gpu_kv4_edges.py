@@ -99,6 +99,35 @@ def test_starts_that_hold_no_rows(starts, n, bound):
             assert (out == 7.0).all()
 
 
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (128, 32), (256, 256), (256, 64)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("size", [2.5, 3.25, 3.75])
+@pytest.mark.parametrize("n,news", [(600, 1), (3000, 1), (600, 150)])
+def test_sink(dim, group, dtype, size, n, news):
+    """One token takes nearly all of the softmax and its value is zero, so the output is what the small probabilities
+    make of the others.  Its key is 7 size in dim 0, every query 8 there, the other keys 0: with a scale of 1/8 in log2
+    units it is 7 size (12, 16 or 18 nats) above scores of 0 +- 1 nat, exactly in fp16 as well.  The outputs' weights
+    are then those of scores near +1 nat, 2^-25 of the largest at the least; values of 1000 keep fp16 outputs (2e-3 to
+    1) normal numbers.  fp32: the difference of scores, 26 in log2 units, is good to 26 times 2^-23, 2^-18.3 in the
+    probabilities: 2^-17 + 2^-18 allowed."""
+    rng = _rng(22)
+    heads = 2
+    k, v = rng.standard_normal((2, n, heads, dim))
+    k *= np.sqrt(128 / dim)
+    k[..., 0] = 0.0
+    v *= 1000.0
+    k[0], v[0] = 0.0, 0.0
+    k[0, :, 0] = 7 * size
+    f = Held(rng, k, v, group, 32)
+    q = rng.standard_normal((news, 2 * heads, dim))
+    q[..., 0] = 8.0
+    q = _t(q.astype(np.float32)).to(TYPES[dtype])
+    tol = TOL[dtype] + (2.0 ** -18 if dtype == "f32" else 0.0)
+    for bound in (None, FAR) if news > 1 and dtype == "bf16" else (None,):
+        got, want = f.attend(q, scale=0.125 / np.log2(np.e), max_len=bound)
+        _close(got, want, tol)
+
+
 @pytest.mark.parametrize("dtype,qsize,scale", [("f32", 1e-42, None), ("f32", 1e-8, 1e-38), ("f32", 1e-45, 1e-3),
                                                ("bf16", 1e-39, None), ("bf16", 1e-8, 1e-38), ("f16", 1e-7, 1e-38),
                                                ("bf16", 2e-39, 3e38), ("f32", 2e-39, 3e38)])
