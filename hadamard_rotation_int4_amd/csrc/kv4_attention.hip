@@ -76,8 +76,8 @@ enum { kForBf16 = 0, kForF16 = 1, kForF32 = 2 };
 constexpr int kv4_attn_waves(int dim, bool groups, int rows, int prec) {
   return dim == 256 || rows > 16 || (dim == 128 && (prec == kForF32 || (groups && prec == kForF16))) ? 2 : 3;
 }
-// Smallest exponent of the unit of value scales: its reciprocal is an fp16 number.
-constexpr int kMinScaleExp = -15;
+// Smallest exponent of the unit of value scales: fp16's own.
+constexpr int kMinScaleExp = -24;
 
 // max over the four lanes that hold the same query row (lanes i + 16 g)
 __device__ __forceinline__ float max_over_g(float v) {
@@ -330,7 +330,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
   // one group a head: acc is in units of 2^vexp, at most which every value scale so far was
   int vexp = kMinScaleExp;
   float vcap = 0.0f;
-  _Float16 vinv = (_Float16)1;
+  float vinv = 1.0f;
   const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
   const half8v ones_h = {(_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1};
 
@@ -376,7 +376,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
       }
     }
     if (!GROUPS) {
-      // value scales go into the probabilities, relative to 2^vexp
+      // value scales go into the probabilities, relative to 2^vexp, and are multiplied in fp32: one far larger than the
+      // others, which some row may not even see, would make fp16's subnormals or zeros of them
       const half4v v4 = __builtin_elementwise_max(vs[0], vs[1]);
       const half2v v2 = __builtin_elementwise_max((half2v){v4[0], v4[1]}, (half2v){v4[2], v4[3]});
       const float vm = fmaxf((float)v2[0], (float)v2[1]);
@@ -392,10 +393,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
           vexp = e;
         }
         vcap = ldexpf(1.0f, vexp);
-        vinv = (_Float16)ldexpf(1.0f, -vexp);
+        vinv = ldexpf(1.0f, -vexp);
       }
-#pragma unroll
-      for (int t = 0; t < 2; ++t) vs[t] = vs[t] * (half4v){vinv, vinv, vinv, vinv};
     }
     // probabilities
     half8v pv[RT][PT];
@@ -437,12 +436,10 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
         accl[rt] = mma(ones_h, ph[t], accl[rt]);
         pv[rt][t] = ph[t];
       }
-      if (!GROUPS && PREC == kForBf16) {
-        pv[rt][0] = ph[0] * (half8v){vs[0][0], vs[0][1], vs[0][2], vs[0][3], vs[1][0], vs[1][1], vs[1][2], vs[1][3]};
-      } else if (!GROUPS) {
+      if (!GROUPS) {
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float y = pr[u] * (float)vs[u >> 2][u & 3];
+          const float y = pr[u] * ((float)vs[u >> 2][u & 3] * vinv);
           pv[rt][0][u] = (_Float16)y;
           if (PT == 2) pv[rt][PT - 1][u] = (_Float16)(y - (float)pv[rt][0][u]);
         }

@@ -128,6 +128,25 @@ def test_sink(dim, group, dtype, size, n, news):
         _close(got, want, tol)
 
 
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 128), (128, 32), (256, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("size", [0.01, 1.0])
+def test_huge_value_in_a_masked_place(dim, group, dtype, size):
+    """The first row sees a token of the largest values there are, the window hides it from the others: theirs are as
+    good as without it."""
+    rng = _rng(23)
+    n, news, heads, window = 700, 24, 2, 600
+    k, v = rng.standard_normal((2, n, heads, dim))
+    v *= size
+    v[n - news - window + 1] = 6e4 * rng.choice([-1.0, 1.0], (heads, dim))      # the first that row 0 sees
+    f = Held(rng, k, v, group, 64)
+    q = _t(rng.standard_normal((news, 2 * heads, dim)).astype(np.float32)).to(TYPES[dtype])
+    for bound in (None, FAR) if dtype == "bf16" else (None,):
+        got, want = f.attend(q, window=window, max_len=bound)
+        _close(got[1:], want[1:], TOL[dtype])
+        _close(got[:1], want[:1], TOL[dtype])
+
+
 @pytest.mark.parametrize("dtype,qsize,scale", [("f32", 1e-42, None), ("f32", 1e-8, 1e-38), ("f32", 1e-45, 1e-3),
                                                ("bf16", 1e-39, None), ("bf16", 1e-8, 1e-38), ("f16", 1e-7, 1e-38),
                                                ("bf16", 2e-39, 3e38), ("f32", 2e-39, 3e38)])
