@@ -76,8 +76,6 @@ enum { kForBf16 = 0, kForF16 = 1, kForF32 = 2 };
 constexpr int kv4_attn_waves(int dim, bool groups, int rows, int prec) {
   return dim == 256 || rows > 16 || (dim == 128 && (prec == kForF32 || (groups && prec == kForF16))) ? 2 : 3;
 }
-// Smallest exponent of the unit of value scales: fp16's own.
-constexpr int kMinScaleExp = -24;
 
 // max over the four lanes that hold the same query row (lanes i + 16 g)
 __device__ __forceinline__ float max_over_g(float v) {
@@ -188,6 +186,14 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
   constexpr int RT = ROWS / 16;
   constexpr int QT = PREC == kForBf16 ? 1 : 2;     // fp16 terms of a query, and of a scaled code
   constexpr int PT = PREC == kForF32 ? 2 : 1;      // of a probability
+  // Of a probability's two terms the second is held 2^11 times as large, against values 2^-11 as large: it would
+  // otherwise be 0 for probabilities under 2^-25 of the largest.  The values of 2^-11 keep their bits because they are
+  // codes (one group a head: the value scales are in the probabilities) or scaled up before.
+  // Value scales, where they are in the probabilities or there are two terms, are relative to a power of two, the unit,
+  // that the largest so far sets.
+  constexpr bool UNIT = !GROUPS || PREC == kForF32;
+  constexpr int UNIT_MIN = GROUPS ? -15 : -24;     // its reciprocal an fp16 number; fp16's smallest exponent
+  constexpr int UNIT_BELOW = GROUPS ? 12 : 0;      // log2 of the largest scale in units (7 times 2^12 is an fp16 number)
   typedef Tile<D, GROUPS> T;
   __shared__ float o_lds[W][16][LD];
   __shared__ float m_lds[W][16], l_lds[W][16];
@@ -327,11 +333,10 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
     accl[rt] = zero;
     m[rt] = -__builtin_inff();
   }
-  // one group a head: acc is in units of 2^vexp, at most which every value scale so far was
-  int vexp = kMinScaleExp;
-  float vcap = 0.0f;
-  float vinv = 1.0f;
+  int vexp = UNIT_MIN;                   // acc is in units of 2^vexp
+  float vcap = 0.0f, vinv = 1.0f;        // the largest scale that the unit is for; 2^-vexp
   const half4v zero4 = {(_Float16)0, (_Float16)0, (_Float16)0, (_Float16)0};
+  const half2v down = {(_Float16)0x1p-11f, (_Float16)0x1p-11f};
   const half8v ones_h = {(_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1, (_Float16)1};
 
   auto step = [&](const T& x, int t0) {
@@ -375,15 +380,21 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
         if (j < lo || j >= to) vs[u >> 2][u & 3] = (_Float16)0;    // never written: may hold anything
       }
     }
-    if (!GROUPS) {
-      // value scales go into the probabilities, relative to 2^vexp, and are multiplied in fp32: one far larger than the
-      // others, which some row may not even see, would make fp16's subnormals or zeros of them
+    half4v vd[2] = {zero4, zero4};      // 2^-11 of the scales
+    if (UNIT) {
       const half4v v4 = __builtin_elementwise_max(vs[0], vs[1]);
       const half2v v2 = __builtin_elementwise_max((half2v){v4[0], v4[1]}, (half2v){v4[2], v4[3]});
       const float vm = fmaxf((float)v2[0], (float)v2[1]);
       if (__builtin_amdgcn_ballot_w64(vm > vcap)) {
-        int e = __builtin_amdgcn_frexp_expf(max_over_g(vm));
-        e = __builtin_amdgcn_readfirstlane(e < kMinScaleExp ? kMinScaleExp : e);
+        uint32_t u = __float_as_uint(max_over_g(vm));
+        if (GROUPS) {        // lanes of a row hold different groups
+          u = umax_dpp<kQuadXor1>(u);
+          u = umax_dpp<kQuadXor2>(u);
+          u = umax_dpp<kRowHalfMirror>(u);
+          u = umax_dpp<kRowMirror>(u);
+        }
+        int e = __builtin_amdgcn_readfirstlane(__builtin_amdgcn_frexp_expf(__uint_as_float(u))) - UNIT_BELOW;
+        if (e < UNIT_MIN) e = UNIT_MIN;
         if (e > vexp) {
           const float f = ldexpf(1.0f, vexp - e);
 #pragma unroll
@@ -392,8 +403,16 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
             for (int c = 0; c < NC; ++c) acc[rt][c] *= f;
           vexp = e;
         }
-        vcap = ldexpf(1.0f, vexp);
+        vcap = ldexpf(1.0f, vexp + UNIT_BELOW);
         vinv = ldexpf(1.0f, -vexp);
+      }
+      if (GROUPS) {
+        const _Float16 up = (_Float16)vinv;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          vs[t] = vs[t] * (half4v){up, up, up, up};
+          vd[t] = vs[t] * (half4v){down[0], down[0], down[0], down[0]};
+        }
       }
     }
     // probabilities
@@ -432,16 +451,18 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
 #pragma unroll
       for (int t = 0; t < PT; ++t) {
 #pragma unroll
-        for (int u = 0; u < 8; ++u) ph[t][u] = (_Float16)(t ? pr[u] - (float)ph[0][u] : pr[u]);
-        accl[rt] = mma(ones_h, ph[t], accl[rt]);
+        for (int u = 0; u < 8; ++u) ph[t][u] = (_Float16)(t ? (pr[u] - (float)ph[0][u]) * 0x1p11f : pr[u]);
+        accl[rt] = mma(t ? ones_h * (_Float16)0x1p-11f : ones_h, ph[t], accl[rt]);
         pv[rt][t] = ph[t];
       }
       if (!GROUPS) {
+        // multiplied in fp32: a scale far larger than the others, which some row may not even see, would make fp16's
+        // subnormals or zeros of them
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
           const float y = pr[u] * ((float)vs[u >> 2][u & 3] * vinv);
           pv[rt][0][u] = (_Float16)y;
-          if (PT == 2) pv[rt][PT - 1][u] = (_Float16)(y - (float)pv[rt][0][u]);
+          if (PT == 2) pv[rt][PT - 1][u] = (_Float16)((y - (float)pv[rt][0][u]) * 0x1p11f);
         }
       }
     }
@@ -455,11 +476,13 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
 #pragma unroll
       for (int d = 0; d < 2; ++d) {
         const int c = 2 * bb + d;
-        half2v v1[4];
-        if (GROUPS) {
+        half2v v1[4], v2[4];
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
+        for (int j = 0; j < 4; ++j) {
+          const half2v sc = {vs[j >> 1][2 * (j & 1)], vs[j >> 1][2 * (j & 1) + 1]};
+          const half2v sd = {vd[j >> 1][2 * (j & 1)], vd[j >> 1][2 * (j & 1) + 1]};
+          if (PT == 2) v2[j] = vv[d][j] * (GROUPS ? sd : down);
+          if (GROUPS) {
             const half2v y = vv[d][j] * sc;
             if (QT == 2) v1[j] = __builtin_elementwise_fma(vv[d][j], sc, -y);
             vv[d][j] = y;
@@ -469,7 +492,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt) {
           if (GROUPS && QT == 2) acc[rt][c] = mma(join8(v1), pv[rt][0], acc[rt][c]);
-          if (PT == 2) acc[rt][c] = mma(v, pv[rt][PT - 1], acc[rt][c]);
+          if (PT == 2) acc[rt][c] = mma(join8(v2), pv[rt][PT - 1], acc[rt][c]);
           acc[rt][c] = mma(v, pv[rt][0], acc[rt][c]);
         }
       }
@@ -494,7 +517,7 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
 
   // join the waves, 16 rows at a time: lane (g, i) holds dims [g D/4, (g+1) D/4) of row i
   __syncthreads();           // the exchange held the queries
-  const float unit = !GROUPS ? ldexpf(1.0f, vexp) : 1.0f;
+  const float unit = UNIT ? ldexpf(1.0f, vexp) : 1.0f;
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt) {
     if (rt) __syncthreads();

@@ -100,7 +100,7 @@ def test_starts_that_hold_no_rows(starts, n, bound):
 
 
 @pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (128, 32), (256, 256), (256, 64)])
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("size", [2.5, 3.25, 3.75])
 @pytest.mark.parametrize("n,news", [(600, 1), (3000, 1), (600, 150)])
 def test_sink(dim, group, dtype, size, n, news):
@@ -129,7 +129,7 @@ def test_sink(dim, group, dtype, size, n, news):
 
 
 @pytest.mark.parametrize("dim,group", [(64, 64), (128, 128), (128, 32), (256, 256)])
-@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("size", [0.01, 1.0])
 def test_huge_value_in_a_masked_place(dim, group, dtype, size):
     """The first row sees a token of the largest values there are, the window hides it from the others: theirs are as
