@@ -812,15 +812,17 @@ def kv4_read(cache: KV4Cache, slots: torch.Tensor, dtype=torch.bfloat16, k: torc
 
 
 def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: torch.Tensor,
-                  starts: torch.Tensor | None = None, max_new: int = 1, max_len: int | None = None,
+                  starts: torch.Tensor | None = None, max_new: int | None = None, max_len: int | None = None,
                   scale: float | None = None, causal: bool = True, window: int = 0,
                   out: torch.Tensor | None = None, workspace: torch.Tensor | None = None) -> torch.Tensor:
     """Attention of query rows over the cache (hr_kv4_attention).  q: [total]
     [q_heads][dim] bf16, fp16 or fp32, rows may be strided; table: int32
     [batch][width] page ids; lens: int32 [batch] cached tokens of each sequence,
     its new ones among them; starts: int32 [batch + 1] first row of each
-    sequence in q, or None when each has max_new rows.  max_new and max_len
-    (width * page if None) bound the rows and the lengths; scale defaults to
+    sequence in q, or None when each has max_new rows.  max_new (1 without
+    starts; with them all of q's rows, which is far more work than the sequences'
+    own bound) and max_len (width * page) bound the rows and the lengths: rows
+    past max_new of a sequence, and rows of none, are not written.  scale defaults to
     1/sqrt(dim); window > 0 sees only that many tokens back.  workspace: uint8,
     kept by a caller that captures the call in a graph; allocated when None.
     Returns out [total][q_heads][dim] of q's dtype, 0 in a row that sees no
@@ -835,6 +837,8 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
         _kv4_index(starts, "starts", torch.int32, (batch + 1,))
     if q_heads < 1 or q_heads % cache.heads:
         raise ValueError(f"q: {q_heads} heads are not a multiple of the cache's {cache.heads}")
+    if max_new is None:
+        max_new = 1 if starts is None else total
     if max_len is None:
         max_len = min(width * cache.page, 1 << 30)
     if scale is None:

@@ -165,3 +165,15 @@ def test_tiny_queries_and_scales(dtype, qsize, scale, rotate, news):
         out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news, max_len=bound,
                                scale=scale)
         _close(_num(out), want, TOL[dtype])
+
+
+@pytest.mark.parametrize("news", [[5], [40, 3], [1, 130]])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_starts_without_max_new(news, dtype):
+    """With starts alone, every row of every sequence is computed."""
+    rng = _rng(25)
+    f = Filled(rng, [n + 100 for n in news], 2, 128, 128, 16, True)
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    q = _t(rng.standard_normal((starts[-1], 4, 128)).astype(np.float32)).to(TYPES[dtype])
+    out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts))
+    _close(_num(out), f.want(_num(q), starts), TOL[dtype])
