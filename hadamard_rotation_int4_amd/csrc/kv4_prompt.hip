@@ -396,7 +396,8 @@ __global__ __launch_bounds__(64 * W, D == 256 ? 1 : 2) void kv4_prompt_kernel(Kv
     const Place pv = ahead;
     ahead = place_of<D>(p.c, table_row, head, t0 + 3 * kPromptTokens + blk, last);
 
-    // the next tile's scores, and this one's probabilities
+    // the next tile's scores, and this one's probabilities; their sum takes them as rounded, and like the matrix
+    // instructions the dot product keeps fp16's subnormals (both checked against exact sums)
     f32x16 sn[2];
     scores(kbuf + (cur ^ 1) * L::KEYS, sn);
     half8v ph[4];

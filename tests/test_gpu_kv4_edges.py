@@ -177,3 +177,82 @@ def test_starts_without_max_new(news, dtype):
     q = _t(rng.standard_normal((starts[-1], 4, 128)).astype(np.float32)).to(TYPES[dtype])
     out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts))
     _close(_num(out), f.want(_num(q), starts), TOL[dtype])
+
+
+# ------------------------------------------------------------------ every form, over many tokens
+
+def _parts(f, total, q_heads, dtype, max_new, window=0):
+    """Parts of the token axis that a call's workspace is for: which form a call takes shows in them."""
+    need = hr.lib.hr_kv4_attention_workspace(f.heads, f.dim, hr.__dict__[f"HR_{dtype.upper()}"], total, len(f.lens), q_heads,
+                                             max_new, f.width * f.page, window)
+    return need // (total * q_heads * (4 * f.dim + 8)) if need else 1
+
+
+def _attend_many(f, rng, news, q_heads, dtype, causal=True, window=0):
+    starts = np.concatenate([[0], np.cumsum(news)]).astype(np.int32)
+    q = _t(rng.standard_normal((starts[-1], q_heads, f.dim)).astype(np.float32)).to(TYPES[dtype])
+    out = hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=max(news), causal=causal,
+                           window=window)
+    vals = [np.nan_to_num(oracle.kv4.values(f.codes[i], f.scales[i]), posinf=0, neginf=0) for i in range(2)]
+    want = dense(_num(q), *vals, f.table, f.lens, starts, f.dim ** -0.5, f.signs, f.rotate, causal, window)
+    _close(_num(out), want, TOL[dtype])
+
+
+@pytest.mark.parametrize("dim,group", [(64, 32), (64, 64), (128, 32), (128, 64), (128, 128), (256, 32), (256, 128),
+                                       (256, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("page", [16, 64])
+def test_row_kernel_over_many_tokens(dim, group, dtype, page):
+    """16 rows on four waves: several tiles a wave, parts, pages that end between parts; one row tile, then two."""
+    rng = _rng(dim + group + page)
+    f = Filled(rng, [2900, 1300, 0], 2, dim, group, page, True)
+    assert _parts(f, 3, 8, dtype, 1) > 8
+    _attend_many(f, rng, [1, 1, 1], 8, dtype)
+    assert 1 < _parts(f, 13, 10, dtype, 5)
+    _attend_many(f, rng, [5, 5, 3], 10, dtype)
+    _attend_many(f, rng, [5, 5, 3], 10, dtype, causal=False)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("causal,window", [(True, 2100), (False, 2100), (False, 3001), (False, 0)])
+@pytest.mark.parametrize("news", [[1, 1], [6, 2]])
+def test_masks_with_parts(dim, group, dtype, causal, window, news):
+    rng = _rng(window + dim)
+    f = Filled(rng, [4700, 2450], 1, dim, group, 32, True)
+    assert _parts(f, sum(news), 4, dtype, max(news), window) > 4
+    _attend_many(f, rng, news, 4, dtype, causal, window)
+
+
+@pytest.mark.parametrize("dim,group,batch,heads,q_heads,news,n,parts", [
+    (64, 64, 1, 2, 8, 600, 2000, 5),            # 128 rows
+    (64, 32, 1, 2, 8, 600, 2000, 5),
+    (128, 128, 3, 8, 32, 32, 6000, 12),         # 128 rows, joined 16 groups a row
+    (128, 32, 3, 8, 32, 32, 6000, 12),
+    (128, 128, 9, 2, 8, 96, 2500, 6),           # 256 rows
+    (128, 64, 9, 2, 8, 96, 2500, 6),
+    (256, 256, 1, 2, 8, 1100, 4400, 8),         # 128 rows
+    (256, 64, 1, 2, 8, 1100, 4400, 8),
+])
+@pytest.mark.parametrize("causal,window", [(True, 0), (True, 1500), (False, 0)])
+def test_prompt_kernel_in_parts(dim, group, batch, heads, q_heads, news, n, parts, causal, window):
+    """The number of parts is the prompt kernel's: the row kernel would divide these calls otherwise."""
+    rng = _rng(dim + group)
+    f = Filled(rng, [n - 70 * b for b in range(batch)], heads, dim, group, 64, True)
+    if not window:
+        assert _parts(f, batch * news, q_heads, "bf16", news) == parts
+    _attend_many(f, rng, [news] * batch, q_heads, "bf16", causal, window)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 128), (128, 32), (256, 64)])
+@pytest.mark.parametrize("n,news", [(200, 1), (200, 60), (2600, 1), (2600, 7)])
+def test_poisoned_token_in_every_type(dtype, dim, group, n, news):
+    rng = _rng(26)
+    f = Filled(rng, [n], 2, dim, group, 16, True)
+    for h, j in ((0, n - 1), (1, n - 1 - news // 2)):
+        page, place = f.table[0, j // 16], j % 16
+        for kv, t in ((0, f.cache.k_scales), (1, f.cache.v_scales)):
+            t[page, h, :, place] = float("nan")
+            f.scales[kv][page, h, :, place] = np.nan
+    _attend(f, rng, [news], 4, dtype)
