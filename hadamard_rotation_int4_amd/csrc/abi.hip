@@ -558,6 +558,7 @@ int32_t hr_w4a4_gemm_fp6(const uint8_t* a_f6, const void* a_scales, const uint8_
 // Vectors of one call: a launch holds fewer than 2^32 threads.
 constexpr int64_t kKv4MaxVectors = int64_t(1) << 26;
 constexpr int32_t kKv4MaxHeads = 65535, kKv4MaxBatch = 65535;
+constexpr int32_t kKv4MaxQHeads = 1 << 22;   // times 256 dims: a row's elements are counted in 32 bits
 
 // Checks a cache description and fills the internal one.  The arrays may be
 // NULL only when no token is touched (`need` false).
@@ -663,7 +664,7 @@ int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, in
                                    int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window) {
   // nothing that the call itself refuses: the plan's products then stay in 64 bits
   if (heads < 1 || heads > kKv4MaxHeads || (dim != 64 && dim != 128 && dim != 256) || !kv4_dtype(dtype) || q_heads < 1 ||
-      q_heads % heads || total < 1 || total > kKv4MaxVectors / q_heads || batch < 1 || batch > kKv4MaxBatch || max_new < 1 ||
+      q_heads > kKv4MaxQHeads || q_heads % heads || total < 1 || total > kKv4MaxVectors / q_heads || batch < 1 || batch > kKv4MaxBatch || max_new < 1 ||
       max_new > kKv4MaxVectors / q_heads || max_len < 0 || max_len > hr::kKv4MaxLen || window < 0)
     return 0;
   hr::Kv4AttnArgs a{};
@@ -710,6 +711,7 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
     return fail(HR_EINVAL, "%s: starts, table and lens must be 4-byte aligned", fn);
   if (q_heads < 1 || q_heads % cache->heads)
     return fail(HR_EUNSUPPORTED, "%s: q_heads=%d is not a multiple of heads=%d", fn, q_heads, cache->heads);
+  if (q_heads > kKv4MaxQHeads) return fail(HR_EUNSUPPORTED, "%s: q_heads=%d above 2^22", fn, q_heads);
   if (!kv4_stride(q_stride, (int64_t)q_heads * cache->dim, dtype))
     return fail(HR_EINVAL, "%s: q_stride must be at least q_heads * dim and a multiple of 16 bytes", fn);
   if (!starts && (int64_t)batch * max_new != total)

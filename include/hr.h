@@ -573,7 +573,7 @@ int32_t hr_kv4_read(const hr_kv4_cache* cache, const int64_t* slots, int64_t tok
  *   table     [batch][width] int32 page ids; only entries of cached tokens are
  *             used.  An id outside [0, pages) is read as 0.
  *   lens      [batch] int32 (device), at most width * page.
- *   q_heads   a multiple of heads; total * q_heads is at most 2^26.
+ *   q_heads   a multiple of heads, at most 2^22; total * q_heads is at most 2^26.
  *             batch is at most 65535, width at most 2^31 - 1.
  *   max_new, max_len  upper bounds of a sequence's query rows and cached
  *             length, for the launch; rows past max_new are not computed.  A

@@ -244,6 +244,13 @@ def test_attention_width_past_32_bits():
     assert _attend(width=1 << 62) == hr.HR_EUNSUPPORTED
 
 
+def test_attention_query_heads_past_32_bits_of_elements():
+    f = hr.lib.hr_kv4_attention_workspace
+    for q_heads in (1 << 23, 1 << 26):
+        assert _attend(q_heads=q_heads, qs=q_heads * 128, total=1, batch=1) == hr.HR_EUNSUPPORTED
+        assert f(2, 128, hr.HR_BF16, 1, 1, q_heads, 1, 1 << 20, 0) == 0
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_oracle_rotation_is_orthogonal():
