@@ -460,7 +460,8 @@ __global__ __launch_bounds__(64 * W, W == 8 ? 2 : kv4_attn_waves(D, GROUPS, ROWS
         // subnormals or zeros of them
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-          const float y = pr[u] * ((float)vs[u >> 2][u & 3] * vinv);
+          float y = pr[u] * ((float)vs[u >> 2][u & 3] * vinv);
+          if (PT == 2) asm("" : "+v"(y));      // one fp32 number for both terms: a mixed-precision fma rounds its own way
           pv[rt][0][u] = (_Float16)y;
           if (PT == 2) pv[rt][PT - 1][u] = (_Float16)((y - (float)pv[rt][0][u]) * 0x1p11f);
         }

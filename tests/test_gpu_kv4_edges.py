@@ -256,3 +256,20 @@ def test_poisoned_token_in_every_type(dtype, dim, group, n, news):
             t[page, h, :, place] = float("nan")
             f.scales[kv][page, h, :, place] = np.nan
     _attend(f, rng, [news], 4, dtype)
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 128), (256, 256), (128, 32)])
+def test_every_fp32_row(dim, group):
+    """Each of 80000 rows by itself: one weight of a row off by half a unit of fp16 (2^-12), in one row of thousands, does
+    not show in the whole.  The weights of 40 tokens, none above a half or so, are good to 2^-20 (scores of up to 10 in
+    log2 units): 2^-17 allowed, as for the whole."""
+    rng = _rng(28)
+    n, batch, heads = 40, 64, 8
+    f = Filled(rng, [n] * batch, heads, dim, group, 64, True)
+    starts = n * np.arange(batch + 1, dtype=np.int32)
+    q = _t(rng.standard_normal((n * batch, 4 * heads, dim)).astype(np.float32))
+    got = _num(hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=n, causal=False))
+    vals = [np.nan_to_num(oracle.kv4.values(f.codes[i], f.scales[i]), posinf=0, neginf=0) for i in range(2)]
+    want = dense(_num(q), *vals, f.table, f.lens, starts, dim ** -0.5, f.signs, True, False)
+    off = np.linalg.norm(got - want, axis=-1) / np.linalg.norm(want, axis=-1)
+    assert off.max() <= TOL["f32"], f"a row is {off.max():.3g} off, the median {np.median(off):.3g}"
