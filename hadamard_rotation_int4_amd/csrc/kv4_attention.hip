@@ -655,11 +655,13 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 
 // Which kernel, and into how many parts of the token axis.
 //
-// Rows: 16 a workgroup of the kernel above, and fp16 ones 32 where that still
-// makes two workgroups a CU (the codes of a tile are then made fp16 once for
-// both halves: 1024 tokens, 32 heads on 8, over 4096 197 against 224 us; where
-// there are fewer, twice the workgroups wait less: 64 sequences of 3 new tokens,
-// 64 heads on 8, 48 against 60).
+// Rows: 16 a workgroup of the kernel above, and fp16 calls of more than 16 rows a
+// key/value head 32 where that still makes two workgroups a CU (the codes of a
+// tile are then made fp16 once for both halves: 1024 tokens, 32 heads on 8, over
+// 4096 197 against 224 us; where there are fewer, twice the workgroups wait less:
+// 64 sequences of 3 new tokens, 64 heads on 8, 48 against 60).  Up to 16 rows half
+// of such a workgroup would be empty (64 sequences of up to 8192 tokens, one new
+// token, 32 on 8: 81 against 110).
 //
 // bf16 calls of more than 64 rows a key/value head and enough work take the
 // prompt kernel, whose fewer, larger workgroups cost less a score but start
@@ -695,7 +697,7 @@ void kv4_attention_plan(Kv4AttnArgs* a) {
   a->rows = 16;
   if (a->dtype == kDtBf16 && rows > 64 && pairs * ((rows + 15) / 16) > 8192 * (int64_t)a->c.dim / (span > 0 ? span : 1))
     a->rows = a->c.dim == 128 && rows > 128 ? 256 : 128;
-  if (a->dtype == kDtF16 && a->c.dim <= 128 && pairs * ((rows + 31) / 32) >= 512) a->rows = 32;
+  if (a->dtype == kDtF16 && rows > 16 && a->c.dim <= 128 && pairs * ((rows + 31) / 32) >= 512) a->rows = 32;
   a->tiles = (int)((rows + a->rows - 1) / a->rows);
   const int64_t segments = pairs * a->tiles;
   const int prec = a->dtype == kDtBf16 ? kForBf16 : a->dtype == kDtF16 ? kForF16 : kForF32;

@@ -273,3 +273,12 @@ def test_every_fp32_row(dim, group):
     want = dense(_num(q), *vals, f.table, f.lens, starts, dim ** -0.5, f.signs, True, False)
     off = np.linalg.norm(got - want, axis=-1) / np.linalg.norm(want, axis=-1)
     assert off.max() <= TOL["f32"], f"a row is {off.max():.3g} off, the median {np.median(off):.3g}"
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (64, 32), (128, 128), (128, 64)])
+@pytest.mark.parametrize("news", [1, 4, 5])
+def test_fp16_rows_of_many_sequences(dim, group, news):
+    """Enough pairs of a sequence and a head for 32 rows a workgroup, around the 16 rows from which they are taken."""
+    rng = _rng(29)
+    f = Filled(rng, list(range(news, news + 64)), 8, dim, group, 16, True)
+    _attend_many(f, rng, [news] * 64, 32, "f16")
