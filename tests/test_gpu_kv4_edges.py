@@ -282,3 +282,25 @@ def test_fp16_rows_of_many_sequences(dim, group, news):
     rng = _rng(29)
     f = Filled(rng, list(range(news, news + 64)), 8, dim, group, 16, True)
     _attend_many(f, rng, [news] * 64, 32, "f16")
+
+
+@pytest.mark.parametrize("dim,group", [(64, 64), (128, 32), (256, 256)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("n,news", [(90, 3), (200, 70), (3000, 3)])
+@pytest.mark.parametrize("rotate", [False, True])
+def test_queries_that_are_not_finite(dim, group, dtype, n, news, rotate):
+    """A query that is not finite makes its own row NaN and leaves those beside it as they are."""
+    rng = _rng(30)
+    f = Filled(rng, [n], 2, dim, group, 16, rotate)
+    x = rng.standard_normal((news, 4, dim)).astype(np.float32)
+    starts = np.array([0, news], dtype=np.int32)
+    want = f.want(_num(_t(x).to(TYPES[dtype])), starts)
+    x[0, 1, 3], x[news - 1, 2] = np.nan, np.nan
+    x[1, 0] = np.inf
+    bad = np.zeros((news, 4), dtype=bool)
+    bad[0, 1] = bad[news - 1, 2] = bad[1, 0] = True
+    q = _t(x).to(TYPES[dtype])
+    for bound in (None, FAR) if dtype == "bf16" and news > 3 else (None,):
+        got = _num(hr.kv4_attention(f.cache, q, _t(f.table), _t(f.lens), starts=_t(starts), max_new=news, max_len=bound))
+        assert np.isnan(got[bad].astype(np.float64)).all()
+        _close(got[~bad], want[~bad], TOL[dtype])
