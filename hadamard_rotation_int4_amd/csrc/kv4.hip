@@ -23,12 +23,12 @@
 // registers: no LDS.
 //
 // Bound by memory when there are many tokens: 32768 of 8 heads of 128 in bf16
-// (169 MB either way) are written in 40 us, 4.2 TB/s, and read back in 34 us,
-// 4.9 TB/s, where a large copy reaches 5.0.  Writing also issues some 400 vector
+// (169 MB either way) are written in 39 us, 4.3 TB/s, and read back in 33 us,
+// 5.1 TB/s, where a large copy reaches 5.0.  Writing also issues some 400 vector
 // instructions for 2 KB of input a wave, a quarter of them the transform; a
 // transform on 4-point dot products and nontemporal loads left its time as it
 // was.  Bound by the launch when there are few: one token 3.3 and
-// 3.1 us, 1237 plain fp32 ones of 8 heads of 64 3.5 and 4.3.
+// 3.0 us, 1237 plain fp32 ones of 8 heads of 64 3.4 and 4.3.
 #include "kv4_device.h"
 
 namespace hr {

@@ -10,7 +10,9 @@ namespace hr {
 constexpr float kLog2e = 1.4426950408889634f;
 // Probabilities are fp16 numbers 2^kLift times exp2(score - running maximum): small ones keep their 11 bits down to 2^-25
 // of the largest (17 nats below it), which count where the largest belong to tokens of small values.  Scores may pass the
-// running maximum by kMaxSlack, in log2 units, before it moves; the two together stay within fp16.
+// running maximum by kMaxSlack, in log2 units, before it moves; the two together stay within fp16.  7 and 8 reach 14.6
+// nats and cost prompts less (2048 tokens over 8192, 32 heads on 8 of 128: 273 against 275 us, 270 with no lift; 1024 of
+// 256 dims 237 against 245), other calls the same.
 constexpr float kLift = 11.0f, kMaxSlack = 4.0f;
 
 // The query rows of one sequence, and the tokens they see.  Row and token

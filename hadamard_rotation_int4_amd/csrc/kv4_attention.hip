@@ -45,20 +45,22 @@
 // 2.3e-4 to 2.7e-4.  fp32 queries have the two terms too, and probabilities in two
 // terms: all products above 2^-22 of the whole are there.
 //
-// Bound by memory for single tokens: 64 sequences of 1100 to 8192 tokens, 32
-// heads on 8 of 128 dims (311 MB of cache) 74 us, 4.2 TB/s, one of 131071 (138
-// MB) 32 us, 4.4 TB/s, where a large read reaches 5.7.  The first without its
-// arithmetic takes 63 to 72, without its loads 44.  With several new tokens a
+// Single tokens: 64 sequences of 1100 to 8192 tokens, 32 heads on 8 of 128 dims (311
+// MB of cache) 75 us, 4.1 TB/s, one of 131071 (138 MB) 29 us, 4.7 TB/s, where a
+// large read reaches 5.7.  The first without its arithmetic took 63 to 72 of 74,
+// without its loads 44; its parts are cut from the bound on the lengths, and only
+// 1.6 waves a SIMD are there on average where three fit.  With several new tokens a
 // sequence it is the wait for the chain from a sequence's length over its page
 // ids to its codes, in workgroups of few tiles a wave: 12 sequences of up to 6000
-// tokens, 5 new ones each, 40 heads on 8, two groups a head, 24 us, where 57% of
-// the waves' cycles were waits with 32 rows a workgroup and half the workgroups.
+// tokens, 5 new ones each, 40 heads on 8, two groups a head, 25 us, where 57% of
+// the waves' cycles were waits with 32 rows a workgroup and half the workgroups, and
+// 43% are now.
 // What was measured and not kept: equal shares of all tokens for every
 // workgroup (each then looks for its place first: slower), 8 waves everywhere,
 // other orders of the workgroups, deeper prefetch (registers), keys left as
 // codes plus an offset taken back by a sum of the queries (1 to 2%).
 //
-// Rows of parts are joined by kv4_join_kernel, in the order of the parts: 4 to 6
+// Rows of parts are joined by kv4_join_kernel, in the order of the parts: 4 to 5
 // us, mostly a launch and three loads that wait for each other.
 #include "kv4_attention.h"
 
@@ -72,7 +74,9 @@ enum { kForBf16 = 0, kForF16 = 1, kForF32 = 2 };
 // Waves a SIMD the registers are kept for.  At two or more the compiler takes
 // at most 256 registers and leaves the accumulators among the ordinary ones
 // (with more it moves them to and from the accumulation registers, 112 moves a
-// tile).
+// tile).  Some forms then spill: 50 registers with 128 dims, several groups, fp16, 32
+// rows, 2 with bf16 and 16 rows; with 256 dims 20 to 62 with several groups (9 to 11
+// fp32), up to 10 with one.
 constexpr int kv4_attn_waves(int dim, bool groups, int rows, int prec) {
   return dim == 256 || rows > 16 || (dim == 128 && (prec == kForF32 || (groups && prec == kForF16))) ? 2 : 3;
 }

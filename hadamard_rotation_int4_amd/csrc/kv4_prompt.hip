@@ -34,18 +34,20 @@
 // of t + 2 and the values of t + 1 become fp16; one barrier a turn.  With 8
 // waves four deal with the keys and four with the values.
 //
-// At 128 dims bound by the matrix instructions at the clock they leave: without
-// the fp16 work, the exponentials and the LDS reads the rest of the loop takes
-// 199 of 290 us (2048 tokens, 32 heads on 8, 128 dims, over 8192; 4 waves), which
-// is the rate of a large library product; making fp16 costs 65 of it (8 waves
-// halve that), the LDS reads 22, the exponentials 16.  With 8 waves 272 us, 0.88
-// PFLOP/s where a large library product reaches 1.23.
-// At 64 dims a score costs half the products and the same softmax, and vector
-// instructions bind it: 210 a tile and wave (32 exponentials of 16 cycles among
-// them) beside 16 matrix ones of 32.  6 ragged sequences of up to 1500 tokens, a
-// window of 1024: 94 us a call.  Outputs used to go through LDS, 16 rows at a time; turned
-// back in registers like the queries they cost 700 fewer instructions a wave, 94.4
-// against 98.4 us a call.
+// 2048 tokens, 32 heads on 8, 128 dims, over 8192, 8 waves: 272 us, 0.88 PFLOP/s
+// where a large library product reaches 1.23; the matrix pipe is busy 37% of the
+// time, vector instructions 46%.  There is one workgroup a CU, and the first rows' see
+// 6208 tokens where the last rows' see 8192, so the mean is 0.88 of the longest.
+// Inside one (4 waves, 290 us): without the fp16 work, the exponentials and the LDS
+// reads the loop takes 199, the library product's rate; making fp16 costs 65 (8 waves
+// halve that), the LDS reads 22, the exponentials 16.
+// At 64 dims a score costs half the products and the same softmax: 210 vector
+// instructions a tile and wave (32 exponentials of 16 cycles among them) beside 16
+// matrix ones of 32.  6 ragged sequences of up to 1500 tokens, a window of 1024: 94 us
+// a call, vector instructions 58% of the time and two waves a SIMD where three fit:
+// with at most 17 tiles, what comes before and after the loop counts.  Outputs
+// used to go through LDS, 16 rows at a time; turned back in registers like the
+// queries they cost 700 fewer instructions a wave, 94.4 against 98.4 us a call.
 //
 // Heads vary fastest over the grid, so that with 8 heads the workgroups of one
 // head share an XCD's L2; the last rows, which see most, go first.
@@ -56,7 +58,6 @@ namespace hr {
 constexpr int kPromptTokens = 64;           // of a tile
 
 typedef float f32x16 __attribute__((ext_vector_type(16)));
-
 
 __device__ __forceinline__ f32x16 mma32(half8v a, half8v b, f32x16 c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_f16(a, b, c, 0, 0, 0);
