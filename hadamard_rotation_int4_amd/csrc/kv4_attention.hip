@@ -42,7 +42,7 @@
 // fp16 terms each, queries always, keys and values where several groups make a
 // scaled code more than 11 bits (two terms hold it exactly).  Probabilities stay
 // one term, whose rounding averages out over the tokens: with it outputs are off by
-// 2.3e-4 to 2.7e-4.  fp32 queries have the two terms too, and probabilities in two
+// 2.2e-4 to 2.5e-4.  fp32 queries have the two terms too, and probabilities in two
 // terms: all products above 2^-22 of the whole are there.
 //
 // Single tokens: 64 sequences of 1100 to 8192 tokens, 32 heads on 8 of 128 dims (311
@@ -678,7 +678,7 @@ __global__ __launch_bounds__(256) void kv4_join_kernel(Kv4AttnArgs p) {
 // over 8192: 276 against 292 us; 64 dims lose the third workgroup a CU, 127 against
 // 101 us, and 256 dims the registers).  Its keys and values are rounded to fp16,
 // which an fp16 output would show (its error 5.5e-4 where the rounding of the
-// output alone is 2.1e-4, against 2.4e-4 here, at 372 against 446 us).
+// output alone is 2.1e-4, against 2.4e-4 here, at 372 us where this takes 407).
 //
 // Parts: two workgroups a CU for one sequence, whose parts are all alike (131071
 // tokens, 8 heads: 35.7 us; three a CU 37.6, four 39.9, one and a half 40.8),
