@@ -1,7 +1,8 @@
 """Python binding of libhr.so (ctypes): randomized Hadamard rotation, fused
 int4 / int8 quantization, HARP-style butterfly and mixed-radix processor, int4
-dequant, the W4A4 / W4A8 / W8A8 GEMMs, the online-rotation decode GEMM, and the
-4-bit key/value cache with the attention over it, on MI355X (gfx950).
+dequant, the W4A4 / W4A8 / W8A8 GEMMs, the online-rotation decode GEMM, the
+4-bit key/value cache with the attention over it, MXFP4 quantization and its
+GEMM, and the norms between two blocks of a layer, on MI355X (gfx950).
 
 Argument marshalling only: every step runs in the library's HIP kernels on
 torch's current stream.  Every tensor argument is checked (dtype, shape,
@@ -27,6 +28,8 @@ __all__ = ["HRError", "rotate", "rotate_quant_int4", "rotate_quant_int8", "quant
            "dequant_int4", "w4a4_gemm", "w4a8_gemm", "w8a8_gemm", "rotate_quant_w4a4_gemm",
            "fp6_rows", "w4a4_to_fp6", "rotate_quant_fp6", "w4a4_gemm_fp6",
            "KV4Cache", "kv4_cache", "kv4_append", "kv4_read", "kv4_attention",
+           "quant_mxfp4", "rotate_quant_mxfp4", "dequant_mxfp4", "mxfp4_gemm",
+           "norm_residual", "norm_residual_quant_mxfp4",
            "lib", "LIB_PATH", "SYMBOLS",
            "HR_OK", "HR_EINVAL", "HR_EUNSUPPORTED", "HR_EDEVICE", "HR_F32", "HR_BF16", "HR_F16"]
 
@@ -43,6 +46,14 @@ class _CacheStruct(ctypes.Structure):
     _fields_ = [("k_codes", _vp), ("k_scales", _vp), ("v_codes", _vp), ("v_scales", _vp), ("signs", _vp),
                 ("pages", _i64), ("heads", _i32), ("dim", _i32), ("page", _i32), ("group", _i32),
                 ("rotate", _i32)]
+
+
+class _NormStruct(ctypes.Structure):
+    """hr_norm of include/hr.h."""
+    _fields_ = [("x", _vp), ("block_out", _vp), ("post_weight", _vp), ("gate", _vp), ("weight", _vp),
+                ("rows", _i64), ("x_stride", _i64), ("block_stride", _i64), ("gates", _i64),
+                ("n", _i32), ("x_dtype", _i32), ("dtype", _i32), ("post_norm", _i32),
+                ("scale", _f32), ("eps", _f32)]
 
 
 # name -> (restype, argtypes); mirrors include/hr.h
@@ -74,6 +85,12 @@ SYMBOLS = {
     "hr_kv4_attention": (_i32, [_vp, _vp, _i32, _i64, _i64, _vp, _vp, _i64, _vp, _i32, _i32, _i32, _i64, _f32,
                                 _i32, _i32, _vp, _vp, _i64, _vp]),
     "hr_kv4_attention_workspace": (_i64, [_i32, _i32, _i32, _i64, _i32, _i32, _i32, _i64, _i32]),
+    "hr_quant_mxfp4": (_i32, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _vp, _vp]),
+    "hr_rotate_quant_mxfp4": (_i32, [_vp, _i32, _i64, _i64, _i32, _i32, _vp, _i32, _vp, _vp, _vp]),
+    "hr_dequant_mxfp4": (_i32, [_vp, _vp, _i64, _i32, _i32, _vp, _i32, _vp, _vp]),
+    "hr_mxfp4_gemm": (_i32, [_vp, _vp, _vp, _vp, _i64, _i64, _i64, _i32, _vp, _vp]),
+    "hr_norm_residual": (_i32, [_vp, _vp, _i64, _vp, _vp]),
+    "hr_norm_residual_quant_mxfp4": (_i32, [_vp, _vp, _i64, _i32, _vp, _i32, _vp, _vp, _vp]),
 }
 
 
@@ -869,3 +886,269 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
     if st:
         raise HRError(st, "hr_kv4_attention")
     return out
+
+
+# ------------------------------------------------------------------ MXFP4 and the norms between two blocks
+
+_MX_RULES = {"floor": 0, "ceil": 1}
+_MX_ORDERS = (32, 64, 128, 256)
+_get_device = getattr(torch._C, "_cuda_getDevice", None)
+
+
+def _call(index: int, fn: str, *args) -> None:
+    """A C call on the current stream of device `index`, made while that is the current device."""
+    if _get_device is not None and _get_device() == index:
+        st = getattr(lib, fn)(*args, _raw_stream(index) if _raw_stream is not None else _stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = getattr(lib, fn)(*args, _stream(index))
+    if st:
+        raise HRError(st, fn)
+
+
+def _ptr(index: int, t, name: str) -> int:
+    """Device pointer of a tensor that must be on device `index`."""
+    if t.get_device() != index:
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensor must live on the GPU")
+        raise ValueError(f"{name}: on {t.device}, expected cuda:{index}")
+    return t.data_ptr()
+
+
+def _strided(t, name: str, dtypes):
+    """Check [rows][n] rows that may be strided; returns (rows, n, row stride, dtype)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor, got {type(t).__name__}")
+    dtype = t.dtype
+    if dtype not in dtypes:
+        raise TypeError(f"{name}: dtype {dtype} not in {[_DT_NAME[d] for d in dtypes]}")
+    shape = t.shape
+    if len(shape) != 2:
+        raise ValueError(f"{name}: expected a 2-D [rows][n] tensor, got shape {tuple(shape)}")
+    rows, n = shape
+    step, last = t.stride()
+    if (last != 1 and n > 1 and rows) or (rows > 1 and step < n):
+        raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
+    return rows, n, step if rows > 1 else n, dtype
+
+
+def _mx_sizes(n: int, order: int, signs) -> None:
+    if n <= 0 or n % 32:
+        raise ValueError(f"rows of {n} elements are not whole blocks of 32")
+    if order:
+        if order not in _MX_ORDERS or n % order:
+            raise ValueError(f"order={order} not in {_MX_ORDERS} or not dividing the row length {n}")
+        if signs is not None:
+            _kv4_index(signs, "signs", torch.int8, (n,))
+    elif signs is not None:
+        raise ValueError("signs go with an order")
+
+
+def _mx_rule(rule) -> int:
+    if rule not in _MX_RULES:
+        raise ValueError(f"rule={rule!r} not in {tuple(_MX_RULES)}")
+    return _MX_RULES[rule]
+
+
+def _mx_outputs(rows: int, n: int, codes, scales, device):
+    if codes is None:
+        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=device)
+    else:
+        _kv4_index(codes, "codes", torch.uint8, (rows, n // 2))
+    if scales is None:
+        scales = torch.empty((rows, n // 32), dtype=torch.uint8, device=device)
+    else:
+        _kv4_index(scales, "scales", torch.uint8, (rows, n // 32))
+    return codes, scales
+
+
+def _mx_quant(fn, x, order, signs, rule, codes, scales):
+    rows, n, step, dtype = _strided(x, "x", _KV4_TYPES)
+    _mx_sizes(n, order, signs)
+    rule = _mx_rule(rule)
+    index = x.get_device()
+    px = _ptr(index, x, "x") if index >= 0 else _ptr(0, x, "x")
+    codes, scales = _mx_outputs(rows, n, codes, scales, x.device)
+    pc, ps = _ptr(index, codes, "codes"), _ptr(index, scales, "scales")
+    if order:
+        _call(index, fn, px, _KV4_TYPES[dtype], step, rows, n, order, None if signs is None else _ptr(index, signs, "signs"),
+              rule, pc, ps)
+    else:
+        _call(index, fn, px, _KV4_TYPES[dtype], step, rows, n, rule, pc, ps)
+    return codes, scales
+
+
+def quant_mxfp4(x: torch.Tensor, rule: str = "floor", codes: torch.Tensor | None = None,
+                scales: torch.Tensor | None = None):
+    """Quantize rows to MXFP4 (hr_quant_mxfp4).  x: [rows][n] bf16, fp16 or
+    fp32, n a multiple of 32, rows may be strided (a multiple of 16 bytes);
+    rule: "floor" (the format's, saturating) or "ceil" (nothing saturates).
+    Returns (codes uint8 [rows][n/2], scales uint8 [rows][n/32])."""
+    return _mx_quant("hr_quant_mxfp4", x, 0, None, rule, codes, scales)
+
+
+def rotate_quant_mxfp4(x: torch.Tensor, order: int = 128, signs: torch.Tensor | None = None, rule: str = "floor",
+                       codes: torch.Tensor | None = None, scales: torch.Tensor | None = None):
+    """quant_mxfp4 of rows rotated by Hadamard blocks of `order` (32, 64, 128 or
+    256) elements, y = (I kron H)(d * x)/sqrt(order) (hr_rotate_quant_mxfp4);
+    signs: int8 [n] of +-1, or None."""
+    if order not in _MX_ORDERS:
+        raise ValueError(f"order={order} not in {_MX_ORDERS}")
+    return _mx_quant("hr_rotate_quant_mxfp4", x, order, signs, rule, codes, scales)
+
+
+def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, order: int | None = None,
+                  signs: torch.Tensor | None = None, dtype=torch.float32,
+                  out: torch.Tensor | None = None) -> torch.Tensor:
+    """The rows that MXFP4 codes uint8 [rows][n/2] and scales uint8 [rows][n/32]
+    stand for, rotated back if an order (and its signs) is given
+    (hr_dequant_mxfp4): [rows][n] of dtype."""
+    _kv4_index(codes, "codes", torch.uint8, _ANY_2D)
+    rows, half = codes.shape
+    n, order = 2 * half, order or 0
+    _mx_sizes(n, order, signs)
+    _kv4_index(scales, "scales", torch.uint8, (rows, n // 32))
+    if dtype not in _KV4_TYPES:
+        raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
+    index = codes.get_device()
+    pc = _ptr(max(index, 0), codes, "codes")
+    ps = _ptr(index, scales, "scales")
+    if out is None:
+        out = torch.empty((rows, n), dtype=dtype, device=codes.device)
+    else:
+        _kv4_index(out, "out", dtype, (rows, n))
+    _call(index, "hr_dequant_mxfp4", pc, ps, rows, n, order, None if signs is None else _ptr(index, signs, "signs"),
+          _KV4_TYPES[dtype], _ptr(index, out, "out"))
+    return out
+
+
+def mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Tensor, w_scales: torch.Tensor,
+               dtype=torch.float32, out: torch.Tensor | None = None) -> torch.Tensor:
+    """C = A W^T of MXFP4 operands (hr_mxfp4_gemm): a_codes uint8 [M][K/2],
+    a_scales uint8 [M][K/32], w_codes [N][K/2], w_scales [N][K/32]; any M and N,
+    K a multiple of 32.  fp32 sums, C [M][N] of dtype (bf16, fp16 or fp32)."""
+    _kv4_index(a_codes, "a_codes", torch.uint8, _ANY_2D)
+    _kv4_index(w_codes, "w_codes", torch.uint8, _ANY_2D)
+    M, half = a_codes.shape
+    N = w_codes.shape[0]
+    if half == 0 or half % 16:
+        raise ValueError(f"a_codes: rows of {2 * half} codes are not whole blocks of 32")
+    if w_codes.shape[1] != half:
+        raise ValueError(f"w_codes: rows of {2 * w_codes.shape[1]} codes, but a_codes has {2 * half}")
+    _kv4_index(a_scales, "a_scales", torch.uint8, (M, half // 16))
+    _kv4_index(w_scales, "w_scales", torch.uint8, (N, half // 16))
+    if dtype not in _KV4_TYPES:
+        raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
+    index = a_codes.get_device()
+    pa = _ptr(max(index, 0), a_codes, "a_codes")
+    pw, psa, psw = _ptr(index, w_codes, "w_codes"), _ptr(index, a_scales, "a_scales"), _ptr(index, w_scales, "w_scales")
+    if out is None:
+        out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
+    else:
+        _kv4_index(out, "out", dtype, (M, N))
+    _call(index, "hr_mxfp4_gemm", pa, psa, pw, psw, M, N, 2 * half, _KV4_TYPES[dtype], _ptr(index, out, "out"))
+    return out
+
+
+def _norm_weight(t, name: str, n: int, index: int):
+    if t is None:
+        return None
+    _kv4_index(t, name, torch.float32, (n,))
+    return _ptr(index, t, name)
+
+
+def _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, dtype, residual, alone):
+    """Checks of the two calls below; returns (struct, device index, residual
+    tensor, its pointer and stride, rows, n, dtype)."""
+    rows, n, step, xt = _strided(x, "x", _KV4_TYPES)
+    if n < 1:
+        raise ValueError("x: rows of no elements")
+    if dtype is None:
+        dtype = xt if block_out is None else getattr(block_out, "dtype", None)
+    if dtype not in _KV4_TYPES:
+        raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
+    if xt is not torch.float32 and dtype is not xt:
+        raise TypeError(f"dtype {dtype}: must be x's ({xt}) unless that is float32")
+    index = x.get_device()
+    px = _ptr(max(index, 0), x, "x")
+    po = pg = pr = None
+    bstep = rstep = n
+    gates = 1
+    if block_out is not None:
+        brows, bn, bstep, _ = _strided(block_out, "block_out", (dtype,))
+        if brows != rows or bn != n:
+            raise ValueError(f"block_out: shape {tuple(block_out.shape)}, expected {(rows, n)}")
+        po = _ptr(index, block_out, "block_out")
+        if post_weight is not None and not post_norm:
+            raise ValueError("post_weight goes with post_norm")
+        if gate is not None:
+            _kv4_index(gate, "gate", dtype, (-1, n))
+            gates = gate.shape[0]
+            if gates < 1 or rows % gates:
+                raise ValueError(f"gate: {gates} rows do not divide the {rows} of x")
+            pg = _ptr(index, gate, "gate")
+        if residual is None:
+            residual = torch.empty((rows, n), dtype=xt, device=x.device)
+        else:
+            rrows, rn, rstep, _ = _strided(residual, "residual", (xt,))
+            if rrows != rows or rn != n:
+                raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {(rows, n)}")
+        pr = _ptr(index, residual, "residual")
+    elif post_norm or post_weight is not None or gate is not None or residual is not None:
+        raise ValueError("post_norm, post_weight, gate and residual go with block_out")
+    elif alone:
+        raise ValueError("neither block_out nor h: nothing to compute")
+    p = _NormStruct(px, po, _norm_weight(post_weight, "post_weight", n, index), pg,
+                    _norm_weight(weight, "weight", n, index), rows, step, bstep, gates, n, _KV4_TYPES[xt],
+                    _KV4_TYPES[dtype], 1 if post_norm else 0, scale, eps)
+    return p, index, x if block_out is None else residual, pr, rstep, rows, n, dtype
+
+
+def norm_residual(x: torch.Tensor, block_out: torch.Tensor | None = None, weight: torch.Tensor | None = None,
+                  post_norm: bool = False, post_weight: torch.Tensor | None = None,
+                  gate: torch.Tensor | None = None, scale: float = 1.0, eps: float = 1e-6, dtype=None,
+                  want_h: bool = True, residual: torch.Tensor | None = None, out: torch.Tensor | None = None):
+    """The end of one block and the norm of the next (hr_norm_residual):
+    u = block_out, or with post_norm post_weight * block_out / rms(block_out);
+    r = x + scale * gate * u; h = weight * r / rms(r), rms(v) = sqrt(mean(v^2) +
+    eps).  x: [rows][n] bf16, fp16 or fp32, the residual stream; block_out:
+    [rows][n] of dtype, or None (r = x); gate: [gates][n] of dtype, each for
+    rows / gates rows; weight, post_weight: fp32 [n], or None (all 1).  x,
+    block_out and residual may be strided.  dtype (block_out's or x's by
+    default) is that of h: x's, or any for an fp32 x.  residual may be x (in
+    place).  Returns (r, h); h is None with want_h=False."""
+    p, index, res, pr, rstep, rows, n, dtype = _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps,
+                                                     dtype, residual, not want_h)
+    if not want_h:
+        if out is not None:
+            raise ValueError("out goes with want_h")
+        _call(index, "hr_norm_residual", ctypes.addressof(p), pr, rstep, None)
+        return res, None
+    if out is None:
+        out = torch.empty((rows, n), dtype=dtype, device=x.device)
+    else:
+        _kv4_index(out, "out", dtype, (rows, n))
+    _call(index, "hr_norm_residual", ctypes.addressof(p), pr, rstep, _ptr(index, out, "out"))
+    return res, out
+
+
+def norm_residual_quant_mxfp4(x: torch.Tensor, block_out: torch.Tensor | None = None,
+                              weight: torch.Tensor | None = None, post_norm: bool = False,
+                              post_weight: torch.Tensor | None = None, gate: torch.Tensor | None = None,
+                              scale: float = 1.0, eps: float = 1e-6, order: int | None = None,
+                              signs: torch.Tensor | None = None, rule: str = "floor",
+                              residual: torch.Tensor | None = None, codes: torch.Tensor | None = None,
+                              scales: torch.Tensor | None = None):
+    """norm_residual with h quantized to MXFP4, rotated on the way if an order is
+    given (hr_norm_residual_quant_mxfp4): the activation operand of mxfp4_gemm.
+    Returns (r, codes uint8 [rows][n/2], scales uint8 [rows][n/32])."""
+    p, index, res, pr, rstep, rows, n, _ = _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, None,
+                                                 residual, False)
+    order = order or 0
+    _mx_sizes(n, order, signs)
+    rule = _mx_rule(rule)
+    codes, scales = _mx_outputs(rows, n, codes, scales, x.device)
+    _call(index, "hr_norm_residual_quant_mxfp4", ctypes.addressof(p), pr, rstep, order,
+          None if signs is None else _ptr(index, signs, "signs"), rule, _ptr(index, codes, "codes"),
+          _ptr(index, scales, "scales"))
+    return res, codes, scales

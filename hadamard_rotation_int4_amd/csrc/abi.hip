@@ -11,6 +11,7 @@
 #include "hr.h"
 #include "hr_internal.h"
 #include "kv4.h"
+#include "mx4.h"
 
 namespace {
 
@@ -750,6 +751,204 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
     a.part_ml = reinterpret_cast<float2*>(a.part_o + total * q_heads * a.nsplit * cache->dim);
   }
   return from_hip(hr::launch_kv4_attention(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ---------------------------------------------------------------- MXFP4
+
+static bool mx_order(int32_t order) { return order == 32 || order == 64 || order == 128 || order == 256; }
+
+// What quantizing rows and reading them back have in common.
+static int32_t mx_rows(const char* fn, int64_t rows, int32_t n, int32_t order, const int8_t* signs) {
+  if (rows < 0) return fail(HR_EINVAL, "%s: rows < 0", fn);
+  if (!aligned16(signs)) return fail(HR_EINVAL, "%s: signs must be 16-byte aligned", fn);
+  if (n <= 0 || n % hr::kMxBlock || n > hr::kMxMaxN)
+    return fail(HR_EUNSUPPORTED, "%s: n=%d is not a multiple of 32 in [32, 2^18]", fn, n);
+  if (order != 0 && (!mx_order(order) || n % order))
+    return fail(HR_EUNSUPPORTED, "%s: order=%d not in {32,64,128,256} or not dividing n=%d", fn, order, n);
+  if (rows > (int64_t(1) << 34) / n) return fail(HR_EUNSUPPORTED, "%s: rows * n above 2^34", fn);
+  return HR_OK;
+}
+
+static int32_t mx_quant(const char* fn, const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n,
+                        int32_t order, const int8_t* signs, int32_t rule, uint8_t* codes, uint8_t* scales,
+                        void* stream) {
+  const int32_t st = mx_rows(fn, rows, n, order, signs);
+  if (st) return st;
+  if (!kv4_dtype(x_dtype)) return fail(HR_EINVAL, "%s: x_dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  if (rule != HR_MX_FLOOR && rule != HR_MX_CEIL)
+    return fail(HR_EINVAL, "%s: rule must be HR_MX_FLOOR or HR_MX_CEIL", fn);
+  if (rows > 0 && (!x || !codes || !scales)) return fail(HR_EINVAL, "%s: x, codes and scales are required", fn);
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales))
+    return fail(HR_EINVAL, "%s: x, codes and scales must be 16-byte aligned", fn);
+  if (!kv4_stride(x_stride, n, x_dtype))
+    return fail(HR_EINVAL, "%s: x_stride must be at least n and a multiple of 16 bytes", fn);
+  if (rows == 0) return ok();
+  hr::Mx4QuantArgs a{};
+  a.x = x;
+  a.dtype = x_dtype;
+  a.x_stride = x_stride;
+  a.rows = rows;
+  a.n = n;
+  a.order = order;
+  a.signs = signs;
+  a.ceil = rule == HR_MX_CEIL;
+  a.codes = codes;
+  a.scales = scales;
+  return from_hip(hr::launch_mx4_quant(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int32_t hr_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n, int32_t rule,
+                       uint8_t* codes, uint8_t* scales, void* stream) {
+  return mx_quant("hr_quant_mxfp4", x, x_dtype, x_stride, rows, n, 0, nullptr, rule, codes, scales, stream);
+}
+
+int32_t hr_rotate_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n,
+                              int32_t order, const int8_t* signs, int32_t rule, uint8_t* codes, uint8_t* scales,
+                              void* stream) {
+  if (!mx_order(order))
+    return fail(HR_EUNSUPPORTED, "hr_rotate_quant_mxfp4: order=%d not in {32,64,128,256}", order);
+  return mx_quant("hr_rotate_quant_mxfp4", x, x_dtype, x_stride, rows, n, order, signs, rule, codes, scales, stream);
+}
+
+int32_t hr_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t n, int32_t order,
+                         const int8_t* signs, int32_t dtype, void* out, void* stream) {
+  const char* fn = "hr_dequant_mxfp4";
+  const int32_t st = mx_rows(fn, rows, n, order, signs);
+  if (st) return st;
+  if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  if (order == 0 && signs) return fail(HR_EINVAL, "%s: signs go with an order", fn);
+  if (rows > 0 && (!codes || !scales || !out)) return fail(HR_EINVAL, "%s: codes, scales and out are required", fn);
+  if (!aligned16(codes) || !aligned16(scales) || !aligned16(out))
+    return fail(HR_EINVAL, "%s: codes, scales and out must be 16-byte aligned", fn);
+  if (rows == 0) return ok();
+  hr::Mx4DequantArgs a{};
+  a.codes = codes;
+  a.scales = scales;
+  a.rows = rows;
+  a.n = n;
+  a.order = order;
+  a.signs = signs;
+  a.dtype = dtype;
+  a.y = out;
+  return from_hip(hr::launch_mx4_dequant(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int32_t hr_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                      const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, int32_t dtype, void* c, void* stream) {
+  const char* fn = "hr_mxfp4_gemm";
+  if (M < 0 || N < 0) return fail(HR_EINVAL, "%s: negative size", fn);
+  if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  if (K <= 0 || K % hr::kMxBlock || K > hr::kMxMaxN)
+    return fail(HR_EUNSUPPORTED, "%s: K=%lld is not a multiple of 32 in [32, 2^18]", fn, (long long)K);
+  if (M > (1 << 24) || N > (1 << 24) || (M + 15) / 16 * ((N + 15) / 16) > INT32_MAX)
+    return fail(HR_EUNSUPPORTED, "%s: M=%lld, N=%lld too large", fn, (long long)M, (long long)N);
+  const bool some = M > 0 && N > 0;
+  if (some && (!a_codes || !a_scales || !w_codes || !w_scales || !c))
+    return fail(HR_EINVAL, "%s: codes, scales and c are required", fn);
+  if (!aligned16(a_codes) || !aligned16(a_scales) || !aligned16(w_codes) || !aligned16(w_scales) || !aligned16(c))
+    return fail(HR_EINVAL, "%s: every pointer must be 16-byte aligned", fn);
+  if (!some) return ok();
+  hr::Mx4GemmArgs a{};
+  a.a = a_codes;
+  a.sa = a_scales;
+  a.w = w_codes;
+  a.sw = w_scales;
+  a.M = M;
+  a.N = N;
+  a.K = (int)K;
+  a.dtype = dtype;
+  a.c = c;
+  return from_hip(hr::launch_mx4_gemm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+// ---------------------------------------------------------------- norms
+
+// Checks of hr_norm_residual and its quantizing form; fills the internal arguments.
+static int32_t norm_args(const char* fn, const hr_norm* p, void* residual, int64_t residual_stride, hr::NormArgs* out) {
+  if (!p) return fail(HR_EINVAL, "%s: the description is NULL", fn);
+  if (p->rows < 0) return fail(HR_EINVAL, "%s: rows < 0", fn);
+  if (!kv4_dtype(p->x_dtype) || !kv4_dtype(p->dtype))
+    return fail(HR_EINVAL, "%s: x_dtype and dtype must be HR_F32, HR_BF16 or HR_F16", fn);
+  if (p->x_dtype != HR_F32 && p->x_dtype != p->dtype)
+    return fail(HR_EUNSUPPORTED, "%s: dtype must be x_dtype unless that is HR_F32", fn);
+  if (p->post_norm != 0 && p->post_norm != 1) return fail(HR_EINVAL, "%s: post_norm must be 0 or 1", fn);
+  if (!(p->eps >= 0.0f) || !(p->eps <= 3.4028235e38f) || !(fabsf(p->scale) <= 3.4028235e38f))
+    return fail(HR_EINVAL, "%s: eps must be finite and not negative, scale finite", fn);
+  if (p->n < 1 || p->n > hr::kNormMaxN) return fail(HR_EUNSUPPORTED, "%s: n=%d outside [1, %d]", fn, p->n, hr::kNormMaxN);
+  if (p->rows > (1 << 24)) return fail(HR_EUNSUPPORTED, "%s: more than 2^24 rows", fn);
+  if (p->rows > 0 && !p->x) return fail(HR_EINVAL, "%s: x is NULL", fn);
+  if (p->block_out) {
+    if (!residual) return fail(HR_EINVAL, "%s: residual is NULL", fn);
+    if (p->block_stride < p->n || residual_stride < p->n)
+      return fail(HR_EINVAL, "%s: block_stride and residual_stride must be at least n", fn);
+    if (p->gate && (p->gates < 1 || p->rows % p->gates))
+      return fail(HR_EINVAL, "%s: gates=%lld does not divide rows", fn, (long long)p->gates);
+    if (p->post_weight && !p->post_norm) return fail(HR_EINVAL, "%s: post_weight goes with post_norm", fn);
+  } else if (p->rows > 0 && (residual || p->gate || p->post_norm || p->post_weight)) {
+    return fail(HR_EINVAL, "%s: residual, gate and post_norm go with block_out", fn);
+  }
+  if (p->x_stride < p->n) return fail(HR_EINVAL, "%s: x_stride must be at least n", fn);
+  const uintptr_t xs = p->x_dtype == HR_F32 ? 3u : 1u, ds = p->dtype == HR_F32 ? 3u : 1u;
+  if (((reinterpret_cast<uintptr_t>(p->x) | reinterpret_cast<uintptr_t>(residual)) & xs) ||
+      ((reinterpret_cast<uintptr_t>(p->block_out) | reinterpret_cast<uintptr_t>(p->gate)) & ds) ||
+      ((reinterpret_cast<uintptr_t>(p->weight) | reinterpret_cast<uintptr_t>(p->post_weight)) & 3u))
+    return fail(HR_EINVAL, "%s: every array must be aligned to its elements", fn);
+  *out = hr::NormArgs{};
+  out->x = p->x;
+  out->block = p->block_out;
+  out->post_weight = p->post_weight;
+  out->gate = p->gate;
+  out->weight = p->weight;
+  out->x_stride = p->x_stride;
+  out->block_stride = p->block_stride;
+  out->residual_stride = residual_stride;
+  out->rows = p->rows;
+  out->gate_rows = p->gate && p->gates > 0 && p->rows > 0 ? p->rows / p->gates : 1;
+  out->n = p->n;
+  out->x_dtype = p->x_dtype;
+  out->dtype = p->dtype;
+  out->post_norm = p->post_norm;
+  out->scale = p->scale;
+  out->eps = p->eps;
+  out->residual = residual;
+  return HR_OK;
+}
+
+int32_t hr_norm_residual(const hr_norm* p, void* residual, int64_t residual_stride, void* h, void* stream) {
+  const char* fn = "hr_norm_residual";
+  hr::NormArgs a{};
+  const int32_t st = norm_args(fn, p, residual, residual_stride, &a);
+  if (st) return st;
+  if (reinterpret_cast<uintptr_t>(h) & (p->dtype == HR_F32 ? 3u : 1u))
+    return fail(HR_EINVAL, "%s: h must be aligned to its elements", fn);
+  if (p->rows > 0 && !h && !p->block_out) return fail(HR_EINVAL, "%s: neither block_out nor h", fn);
+  if (p->rows == 0) return ok();
+  a.h = h;
+  return from_hip(hr::launch_norm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+int32_t hr_norm_residual_quant_mxfp4(const hr_norm* p, void* residual, int64_t residual_stride, int32_t order,
+                                     const int8_t* signs, int32_t rule, uint8_t* codes, uint8_t* scales,
+                                     void* stream) {
+  const char* fn = "hr_norm_residual_quant_mxfp4";
+  hr::NormArgs a{};
+  int32_t st = norm_args(fn, p, residual, residual_stride, &a);
+  if (st) return st;
+  st = mx_rows(fn, p->rows, p->n, order, signs);
+  if (st) return st;
+  if (rule != HR_MX_FLOOR && rule != HR_MX_CEIL)
+    return fail(HR_EINVAL, "%s: rule must be HR_MX_FLOOR or HR_MX_CEIL", fn);
+  if (order == 0 && signs) return fail(HR_EINVAL, "%s: signs go with an order", fn);
+  if (p->rows > 0 && (!codes || !scales)) return fail(HR_EINVAL, "%s: codes and scales are required", fn);
+  if (!aligned16(codes) || !aligned16(scales))
+    return fail(HR_EINVAL, "%s: codes and scales must be 16-byte aligned", fn);
+  if (p->rows == 0) return ok();
+  a.order = order;
+  a.signs = signs;
+  a.ceil = rule == HR_MX_CEIL;
+  a.codes = codes;
+  a.scales = scales;
+  return from_hip(hr::launch_norm(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

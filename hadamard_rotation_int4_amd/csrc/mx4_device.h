@@ -1,0 +1,101 @@
+// Device helpers of the MXFP4 format: blocks of 32 consecutive elements of a
+// row, each an e2m1 code (sign bit over the magnitudes 0, 0.5, 1, 1.5, 2, 3, 4,
+// 6), and a scale byte b a block that stands for 2^(b - 127).
+//
+// A lane holds 8 consecutive elements (an octet), a block is the 4 lanes of a
+// quad, and a Hadamard block of `order` elements is L = order / 8 lanes in the
+// labelling of kv4_device.h (kv4_logical), which keeps quads together.
+#pragma once
+
+#include "kv4_device.h"
+#include "mx4.h"
+
+namespace hr {
+
+// 1 / sqrt(8 L)
+template <int L>
+__device__ __forceinline__ constexpr float mx4_norm() {
+  return L == 4 ? 0.17677669529663687f : L == 8 ? 0.125f : L == 16 ? 0.08838834764831845f : 0.0625f;
+}
+
+// This lane's octet among the lanes of its wave (L = 0: no rotation).
+template <int L>
+__device__ __forceinline__ int mx4_lane(int lane) {
+  return L >= 8 ? (lane & ~(L - 1)) | kv4_logical<L>(lane) : lane;
+}
+
+// Factor that makes w after mx4_fwht the rotated values: 1 / sqrt(order) and
+// the lane's sign.
+template <int L>
+__device__ __forceinline__ float mx4_factor(int a) {
+  return (__popc(a & (L >= 16 ? 15 : L - 1)) & 1) ? -mx4_norm<L>() : mx4_norm<L>();
+}
+
+// w[0..7] := +-H_{8 L} w over L lanes, a the lane's octet in its block.
+template <int L>
+__device__ __forceinline__ void mx4_fwht(float* w, int a) {
+  if (L >= 8) {
+    fwht_lanes<8, L>(w, a);
+    return;
+  }
+  fwht_regs<8>(w);
+  const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = fmaf(dpp<kQuadXor1>(w[e]), b0, w[e]);
+#pragma unroll
+  for (int e = 0; e < 8; ++e) w[e] = fmaf(dpp<kQuadXor2>(w[e]), b1, w[e]);
+}
+
+// Largest magnitude of 8 elements; NaN if one is.
+__device__ __forceinline__ float mx4_absmax(const float* w) {
+  float m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(w[0]), fabsf(w[1])), fabsf(w[2]));
+  m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(w[3])), fabsf(w[4]));
+  m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(m, fabsf(w[5])), fabsf(w[6]));
+  return __builtin_elementwise_maximum(m, fabsf(w[7]));
+}
+
+// Scale byte of the block of this quad, from the lane's own largest magnitude
+// m.  The exponent of the largest less that of 4 (the largest binade of e2m1),
+// so that it scales to [4, 8) and what is over 6 saturates; with `ceil` one
+// more where it is over 6.  Not below 2^-127; 255 when the largest is not
+// finite (infinity and NaN have the highest bits, so the integer maximum finds
+// them).
+__device__ __forceinline__ uint32_t mx4_scale(float m, int ceil) {
+  uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
+  a = umax_dpp<kQuadXor1>(a);
+  a = umax_dpp<kQuadXor2>(a);
+  // adding what takes a mantissa over 0.5 past 1 raises the exponent
+  const uint32_t e = (a + (ceil ? 0x3FFFFFu : 0u)) >> 23;
+  const uint32_t b = e > 2u ? e - 2u : 0u;
+  return a >= 0x7F800000u ? 255u : b;
+}
+
+// The 8 codes of w under scale byte b, element e in bits 4 e .. 4 e + 3:
+// nearest, ties to even, saturating at 6; 0 under byte 255.
+__device__ __forceinline__ uint32_t mx4_codes(const float* w, uint32_t b) {
+  const float s = __uint_as_float(b << 23);
+  uint32_t r = 0u;
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[0], w[1], s, 0);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[2], w[3], s, 1);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[4], w[5], s, 2);
+  r = __builtin_amdgcn_cvt_scalef32_pk_fp4_f32(r, w[6], w[7], s, 3);
+  return b == 255u ? 0u : r;
+}
+
+// The 8 magnitudes with signs that codes stand for, before their scale.
+__device__ __forceinline__ void mx4_levels(uint32_t r, float* w) {
+  typedef float f32x2 __attribute__((ext_vector_type(2)));
+  const f32x2 q0 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, 1.0f, 0);
+  const f32x2 q1 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, 1.0f, 1);
+  const f32x2 q2 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, 1.0f, 2);
+  const f32x2 q3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, 1.0f, 3);
+  w[0] = q0[0]; w[1] = q0[1]; w[2] = q1[0]; w[3] = q1[1];
+  w[4] = q2[0]; w[5] = q2[1]; w[6] = q3[0]; w[7] = q3[1];
+}
+
+// 2^(b - 127): a subnormal for b = 0, NaN for 255.
+__device__ __forceinline__ float mx4_power(uint32_t b) {
+  return __uint_as_float(b == 0u ? 0x00400000u : b == 255u ? 0x7FC00000u : b << 23);
+}
+
+}  // namespace hr

@@ -1,8 +1,9 @@
 /*
  * hr.h -- C ABI of libhr.so: randomized Hadamard rotation, fused int4 (and
  * int8) quantization, HARP-style butterfly, int4 dequant, the W4A4 (and
- * W4A8) GEMM, and the 4-bit key/value cache with the attention over it, on AMD
- * Instinct MI355X (gfx950).
+ * W4A8) GEMM, the 4-bit key/value cache with the attention over it, MXFP4
+ * quantization and its GEMM, and the norms between two blocks of a layer, on
+ * AMD Instinct MI355X (gfx950).
  *
  * Conventions shared by every call
  * --------------------------------
@@ -597,6 +598,152 @@ int32_t hr_kv4_attention(const hr_kv4_cache* cache, const void* q, int32_t dtype
  * sizes that the call refuses give 0). */
 int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, int64_t total, int32_t batch,
                                    int32_t q_heads, int32_t max_new, int64_t max_len, int32_t window);
+
+/*
+ * MXFP4, the microscaled 4-bit floating point of the OCP Microscaling Formats
+ * specification, which this GPU's matrix cores multiply directly: blocks of 32
+ * consecutive elements of a row, each an e2m1 code, and one power-of-two scale
+ * a block.
+ *
+ *   codes   [rows][n/2] uint8, two codes a byte, element 2j in the low nibble;
+ *           bit 3 of a code is its sign, bits 0-2 count the magnitudes 0, 0.5,
+ *           1, 1.5, 2, 3, 4, 6.
+ *   scales  [rows][n/32] uint8, byte b stands for 2^(b - 127), 255 for NaN.
+ */
+
+/* How a block's scale follows from its largest magnitude a. */
+typedef enum {
+  HR_MX_FLOOR = 0,  /* 2^(floor(log2 a) - 2), the specification's: what is over
+                       6 of them (up to 8) saturates */
+  HR_MX_CEIL = 1    /* the smallest power of two of which a is at most 6:
+                       nothing saturates */
+} hr_mx_rule;
+
+/*
+ * hr_quant_mxfp4 -- quantize rows to MXFP4.
+ *
+ * Defines: the rotation-free quantizer of "Experiment -- Hadamard rotation for
+ * int4 (W4A4) accuracy" (Method: per-group quantization inside one kernel) in
+ * the MXFP4 format.
+ *
+ * For every block of 32 consecutive values y of a row: a = max |y|, the scale
+ * 2^E by `rule` with E at least -127 (byte E + 127; 0 where a is 0), and the
+ * codes nearest to y / 2^E, ties to the even code, 6 beyond it; a code keeps
+ * its value's sign, -0 included.  Every step but that rounding is exact.  A
+ * block that holds a value that is not finite gets byte 255 and zero codes.
+ *
+ *   x       [rows] rows of n elements of x_dtype (HR_F32, HR_BF16 or HR_F16),
+ *           x_stride elements apart (at least n; a multiple of 16 bytes).
+ *   n       a multiple of 32, at most 2^18; rows * n is at most 2^34.
+ *   codes, scales  as above, 16-byte aligned as x is.
+ */
+int32_t hr_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n, int32_t rule,
+                       uint8_t* codes, uint8_t* scales, void* stream);
+
+/*
+ * hr_rotate_quant_mxfp4 -- hr_quant_mxfp4 of rows rotated on the way by a
+ * blockwise randomized Hadamard transform, y = (I kron H_p)(d * x) / sqrt(p).
+ *
+ * Defines: as hr_rotate_quant_int4 ("Experiment -- ...", Hypothesis and
+ * Method; the sign diagonal of HARP's incoherence processing), block by block.
+ * Both operands of a product rotated alike leave it as it is.
+ *
+ * The transform is computed in fp32 (1/sqrt(p) rounded to it); a value that is
+ * not finite reaches every element of its Hadamard block.
+ *
+ *   order   p in {32, 64, 128, 256}, dividing n.
+ *   signs   [n] int8 +-1, 16-byte aligned, or NULL (all +1).
+ *   other arguments as hr_quant_mxfp4.
+ */
+int32_t hr_rotate_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n,
+                              int32_t order, const int8_t* signs, int32_t rule, uint8_t* codes, uint8_t* scales,
+                              void* stream);
+
+/*
+ * hr_dequant_mxfp4 -- the rows that MXFP4 codes and scales stand for, rotated
+ * back where `order` is not 0: x_hat = q 2^E, or d * (I kron H_p)(q 2^E) /
+ * sqrt(p), rounded once to dtype.
+ *
+ *   order   0 (no rotation) or as hr_rotate_quant_mxfp4, with its signs.
+ *   out     [rows][n] of dtype (HR_F32, HR_BF16 or HR_F16).
+ */
+int32_t hr_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t rows, int32_t n, int32_t order,
+                         const int8_t* signs, int32_t dtype, void* out, void* stream);
+
+/*
+ * hr_mxfp4_gemm -- C = A W^T of two MXFP4 operands.
+ *
+ * Defines: the W4A4 product of "Experiment -- ..." (Hypothesis and Verdict) on
+ * operands whose group scales the matrix cores apply themselves.
+ *
+ * C[m][n] = sum over blocks j of 2^(Ea[m][j] + Ew[n][j]) sum_k qa qw.  The
+ * products are exact and the sums fp32: each sum of a matrix instruction (64
+ * or 128 terms and the running sum) is within 2^-22 of its largest term of the
+ * exact one, and terms below 2^-126 may count as 0.  Rounded once to dtype.  A
+ * scale byte of 255 makes its row (or column) of C NaN.
+ *
+ *   a_codes, a_scales  [M][K/2], [M][K/32];  w_codes, w_scales  [N][K/2],
+ *             [N][K/32], all 16-byte aligned.
+ *   K         a multiple of 32, at most 2^18;  M and N at most 2^24, ceil(M/16)
+ *             ceil(N/16) at most 2^31 - 1.
+ *   c         [M][N] of dtype (HR_F32, HR_BF16 or HR_F16).
+ */
+int32_t hr_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,
+                      const uint8_t* w_scales, int64_t M, int64_t N, int64_t K, int32_t dtype, void* c, void* stream);
+
+/*
+ * What stands between two blocks of a layer, for every row of n elements:
+ *   u = o, or post_weight * o / sqrt(mean(o^2) + eps) with post_norm
+ *   r = x + scale * gate * u       (the new residual stream)
+ *   h = weight * r / sqrt(mean(r^2) + eps)
+ * in fp32; h follows from r as computed, before it is rounded to be stored.
+ * Without block_out, r = x, and h is the plain norm of x.
+ *
+ *   x          [rows] rows of n elements of x_dtype, x_stride apart.
+ *   block_out  the block's output o, [rows] rows of dtype, block_stride
+ *              apart, or NULL.
+ *   gate       [gates][n] of dtype, or NULL (no gate): row i takes gate
+ *              i / (rows / gates); gates divides rows (1: one for all rows).
+ *   post_weight, weight  [n] fp32, or NULL (all 1).
+ *   dtype      of block_out, gate and h: x_dtype, or any where x_dtype is
+ *              HR_F32.
+ *   post_norm  0 or 1; eps >= 0, scale: finite.
+ *   n          1 to 32768; rows at most 2^24.
+ * Strides are in elements, at least n.  x, block_out, gate, residual and h need
+ * no alignment but their elements'.  The struct is host memory, read during the
+ * call.
+ */
+typedef struct {
+  const void* x;
+  const void* block_out;
+  const float* post_weight;
+  const void* gate;
+  const float* weight;
+  int64_t rows, x_stride, block_stride, gates;
+  int32_t n, x_dtype, dtype, post_norm;
+  float scale, eps;
+} hr_norm;
+
+/*
+ * hr_norm_residual -- r and h as above.
+ *
+ *   residual  [rows] rows of x_dtype, residual_stride apart; x itself (with its
+ *             stride) is allowed, any other overlap is undefined.  NULL without
+ *             block_out.
+ *   h         [rows][n] of dtype, or NULL: only r.
+ */
+int32_t hr_norm_residual(const hr_norm* p, void* residual, int64_t residual_stride, void* h, void* stream);
+
+/*
+ * hr_norm_residual_quant_mxfp4 -- the same with h quantized to MXFP4, unrounded
+ * and rotated on the way where `order` is not 0: the next product's operand.
+ *
+ *   order, signs, rule, codes, scales  as hr_rotate_quant_mxfp4 (order 0: as
+ *             hr_quant_mxfp4); n a multiple of 32 and of order.
+ */
+int32_t hr_norm_residual_quant_mxfp4(const hr_norm* p, void* residual, int64_t residual_stride, int32_t order,
+                                     const int8_t* signs, int32_t rule, uint8_t* codes, uint8_t* scales,
+                                     void* stream);
 
 #ifdef __cplusplus
 }

@@ -26,7 +26,11 @@ Modules and the passages they follow:
 * ``harp``         -- HARP's general processor: mixed-radix stages of dense
   blocks Q(theta) G_b (Givens for b = 2, Cayley map for b > 2).  HARP
   technical summary, sections 2.1-2.2.
+* ``kv4``          -- the 4-bit key/value cache and attention over it.
+* ``mxfp4``        -- the microscaled 4-bit format: quantization, reading back,
+  the product.
+* ``norm``         -- the norms between two blocks of a layer.
 
 Readings of points the pages leave open are stated where they are used.
 """
-from . import hadamard, mixed_radix, butterfly, quant, gemm, probe, harp, kv4  # noqa: F401
+from . import hadamard, mixed_radix, butterfly, quant, gemm, probe, harp, kv4, mxfp4, norm  # noqa: F401

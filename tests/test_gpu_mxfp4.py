@@ -1,0 +1,418 @@
+"""MXFP4 on the GPU against the fp64 oracle: quantizing, reading back, the product.
+
+Without a rotation the quantizer's one rounding is decided exactly, so codes and
+scales are equal bit for bit.  With it y is computed in fp32: log2(p) additions
+and the product with fl(1/sqrt p) are each off by half a step of what they hold,
+at most S = sum |x| / sqrt(p) of the Hadamard block, so y is within (log2 p + 3)
+2^-24 S of the oracle's; codes are checked where that does not reach over a
+border, and either neighbour is allowed where it does.
+
+Reading back: rounded once (half a step of the type) on top of the same bound.
+
+Product: a matrix instruction sums 64 or 128 exact products and the running sum,
+each at most 2^-22 of the largest off, so K / 64 instructions and 8 joins of
+waves are within (K / 64 + 8) 2^-22 of the sum of magnitudes, plus half a step
+of the output's type.  Rounding to nearest makes infinity of what is at least the
+type's largest number and half a step (65520 in fp16).
+"""
+import numpy as np
+import pytest
+import torch
+
+import hadamard_rotation_int4_amd as hr
+from oracle import mxfp4
+
+pytestmark = pytest.mark.gpu
+
+DEV = "cuda:0"
+TYPES = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _rng(seed):
+    return np.random.Generator(np.random.PCG64(seed))
+
+
+def _t(x):
+    return torch.from_numpy(np.ascontiguousarray(x)).to(DEV)
+
+
+def _num(t):
+    return t.detach().cpu().double().numpy() if t.is_floating_point() else t.detach().cpu().numpy()
+
+
+def _signs(rng, n):
+    return (rng.integers(0, 2, n) * 2 - 1).astype(np.int8)
+
+
+def _half_step(dtype):
+    return torch.finfo(dtype).eps / 2
+
+
+def _rows(rng, rows, n, dtype, spread=0.3):
+    x = rng.standard_normal((rows, n)) * np.exp(spread * rng.standard_normal((rows, 1)))
+    return _t((x * np.where(rng.random(n) < 0.02, 20, 1)).astype(np.float32)).to(dtype)
+
+
+def check_exact(x, codes, scales, rule):
+    want, b = mxfp4.quantize(_num(x), rule)
+    assert np.array_equal(scales.cpu().numpy(), b)
+    assert np.array_equal(codes.cpu().numpy(), mxfp4.pack(want))
+
+
+def check_near(y, off, codes, scales, rule):
+    """Codes and scales of y, known to `off` (both fp64 [rows][n])."""
+    g, d = (v.reshape(*v.shape[:-1], -1, 32) for v in (y, off))
+    a, da = np.abs(g).max(-1), d.max(-1)
+    b = scales.cpu().numpy()
+    lo, hi = mxfp4.scale_bytes(np.maximum(a - da, 0), rule), mxfp4.scale_bytes(a + da, rule)
+    assert ((b >= lo) & (b <= hi)).all()
+    # the check must not be empty: few are undecided (one or two of a small call may be)
+    assert (lo != hi).sum() <= 2 + 0.01 * lo.size
+    c = mxfp4.unpack(codes.cpu().numpy()).reshape(g.shape)
+    s = np.ldexp(1.0, b.astype(int) - 127)[..., None]
+    levels = np.concatenate([mxfp4.LEVELS, -mxfp4.LEVELS])
+    got = levels[c]
+    below, above = levels[mxfp4.encode((g - d) / s)], levels[mxfp4.encode((g + d) / s)]
+    assert ((got >= below) & (got <= above)).all()
+    assert (below != above).sum() <= 2 + 0.01 * below.size
+
+
+def rotation_error(x, order):
+    """Bound of what fp32 makes of the rotated rows x (fp64)."""
+    s = np.abs(x).reshape(*x.shape[:-1], -1, order).sum(-1) / np.sqrt(order)
+    return np.repeat(s, order, -1) * (np.log2(order) + 3) * 2.0 ** -24
+
+
+# ------------------------------------------------------------------ quantizing
+
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows,n", [(1, 32), (3, 64), (1, 4096), (77, 96), (5, 2080), (130, 5120), (1000, 32)])
+def test_quant(rows, n, dtype, rule):
+    x = _rows(_rng(rows + n), rows, n, TYPES[dtype])
+    check_exact(x, *hr.quant_mxfp4(x, rule), rule)
+
+
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_quant_every_value(dtype, rule):
+    """Every finite 16-bit value under a range of scales: a block holds 31 of them
+    and a largest."""
+    bits = np.arange(65536, dtype=np.uint32).astype(np.uint16)
+    v = _t(bits.view(np.int16)).view(TYPES[dtype])
+    v = v[torch.isfinite(v)]
+    v = v[: v.numel() // 31 * 31].view(-1, 31)
+    for top in (6.0, 4.0, 7.5, 0.75, 1024.0, 2.0 ** -14):
+        near = torch.where(v.float().abs() > top, v.float() * 0, v.float()).to(v.dtype)
+        x = torch.cat([near, torch.full_like(v[:, :1], top)], 1).contiguous()
+        check_exact(x, *hr.quant_mxfp4(x, rule), rule)
+
+
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+def test_quant_borders(rule):
+    """fp32 values at, just below and just above every border between codes and
+    between scales, over the whole range of exponents."""
+    one = np.float32(1)
+    near = [v for i in range(7) for m in [np.float32((mxfp4.LEVELS[i] + mxfp4.LEVELS[i + 1]) / 2)]
+            for v in (m, np.nextafter(m, one * 9), np.nextafter(m, -one))]
+    tops = [v for m in (np.float32(4), np.float32(6), np.float32(8))
+            for v in (m, np.nextafter(m, one * 9), np.nextafter(m, one))]
+    rows = []
+    for t in tops:
+        x = np.zeros(32, dtype=np.float32)
+        x[:len(near)] = near
+        x[len(near):len(near) + 3] = [-0.0, -near[1], 1e-30]
+        x[31] = t
+        rows.append(x)
+    rows = np.stack(rows)
+    with np.errstate(over="ignore", under="ignore"):
+        for e in (-140, -130, -128, -127, -126, -125, -124, -100, -3, 0, 1, 60, 124):
+            x = np.ldexp(rows, e).astype(np.float32)
+            x = _t(np.where(np.isfinite(x), x, np.float32(3e38)))
+            check_exact(x, *hr.quant_mxfp4(x, rule), rule)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("order", [0, 32, 256])
+def test_not_finite_stays_in_its_block(dtype, order):
+    x = _rows(_rng(7), 6, 768, TYPES[dtype])
+    unit = order or 32
+    for row, col, v in ((0, 5, float("nan")), (1, 300, float("inf")), (2, 767, -float("inf"))):
+        clean = hr.rotate_quant_mxfp4(x, order) if order else hr.quant_mxfp4(x)
+        y = x.clone()
+        y[row, col] = v
+        codes, scales = hr.rotate_quant_mxfp4(y, order) if order else hr.quant_mxfp4(y)
+        at = col // unit * unit
+        bad = slice(at // 32, (at + unit) // 32)
+        assert (scales[row, bad] == 255).all() and not codes[row, at // 2:(at + unit) // 2].any()
+        codes[row, at // 2:(at + unit) // 2] = clean[0][row, at // 2:(at + unit) // 2]
+        scales[row, bad] = clean[1][row, bad]
+        assert torch.equal(codes, clean[0]) and torch.equal(scales, clean[1])
+    back = hr.dequant_mxfp4(*(hr.rotate_quant_mxfp4(y, order) if order else hr.quant_mxfp4(y)), order=order)
+    assert torch.isnan(back[2, 768 - unit:]).all() and torch.isfinite(back[2, :768 - unit]).all()
+
+
+@pytest.mark.parametrize("rule", ["floor", "ceil"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("order", [32, 64, 128, 256])
+@pytest.mark.parametrize("rows,blocks,signed", [(1, 1, True), (3, 5, False), (77, 3, True), (33, 16, True), (1, 64, True)])
+def test_rotate_quant(rows, blocks, signed, order, dtype, rule):
+    rng = _rng(order + rows + blocks)
+    n = order * blocks
+    x = _rows(rng, rows, n, TYPES[dtype])
+    signs = _signs(rng, n) if signed else None
+    codes, scales = hr.rotate_quant_mxfp4(x, order, None if signs is None else _t(signs), rule)
+    xs = _num(x)
+    check_near(mxfp4.rotate(xs, order, signs), rotation_error(xs, order), codes, scales, rule)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("order", [0, 64, 128])
+def test_strided_rows_and_given_outputs(dtype, order):
+    rng = _rng(3)
+    wide = _rows(rng, 37, 3 * 384, TYPES[dtype])
+    x = wide[:, 384:768]
+    codes = torch.full((37, 192), 77, dtype=torch.uint8, device=DEV)
+    scales = torch.full((37, 12), 77, dtype=torch.uint8, device=DEV)
+    if order:
+        got = hr.rotate_quant_mxfp4(x, order, codes=codes, scales=scales)
+        want = hr.rotate_quant_mxfp4(x.contiguous(), order)
+    else:
+        got, want = hr.quant_mxfp4(x, codes=codes, scales=scales), hr.quant_mxfp4(x.contiguous())
+    assert got[0] is codes and got[1] is scales
+    assert torch.equal(codes, want[0]) and torch.equal(scales, want[1])
+    with pytest.raises(hr.HRError):
+        hr.quant_mxfp4(wide[:, 1:385])                       # not 16-byte aligned
+    odd = torch.zeros((4, 385), dtype=TYPES[dtype], device=DEV)
+    with pytest.raises(hr.HRError):
+        hr.quant_mxfp4(odd[:, :384])                         # rows not a multiple of 16 bytes apart
+
+
+def test_row_past_4_gib():
+    """Rows whose bytes lie past 32 bits of offset."""
+    step = (1 << 30) + 64
+    big = torch.empty((3 * step,), dtype=torch.bfloat16, device=DEV)
+    x = torch.as_strided(big, (3, 256), (step, 1))
+    x.copy_(_rows(_rng(4), 3, 256, torch.bfloat16))
+    check_exact(x.contiguous(), *hr.quant_mxfp4(x), "floor")
+
+
+def test_no_rows():
+    x = torch.empty((0, 64), dtype=torch.bfloat16, device=DEV)
+    codes, scales = hr.rotate_quant_mxfp4(x, 64)
+    assert codes.shape == (0, 32) and scales.shape == (0, 2)
+    assert hr.dequant_mxfp4(codes, scales).shape == (0, 64)
+
+
+# ------------------------------------------------------------------ reading back
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_dequant_every_code_and_scale(dtype):
+    packed = np.tile((np.arange(16) + 16 * np.arange(16)[::-1]).astype(np.uint8), (256, 1))
+    scales = np.arange(256, dtype=np.uint8).reshape(256, 1)
+    want = torch.from_numpy(mxfp4.values(packed, scales)).float().to(TYPES[dtype])
+    got = hr.dequant_mxfp4(_t(packed), _t(scales), dtype=TYPES[dtype]).cpu()
+    assert torch.equal(torch.isnan(got), torch.isnan(want))
+    assert torch.equal(torch.nan_to_num(got.float(), 0.0), torch.nan_to_num(want.float(), 0.0))
+    assert torch.equal(torch.signbit(got[:255]), torch.signbit(want[:255]))
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("order", [0, 32, 64, 128, 256])
+@pytest.mark.parametrize("rows,blocks", [(1, 1), (5, 3), (129, 8)])
+def test_dequant(rows, blocks, order, dtype):
+    rng = _rng(order + rows)
+    n = (order or 32) * blocks
+    packed = rng.integers(0, 256, (rows, n // 2), dtype=np.uint8)
+    scales = rng.integers(117, 132, (rows, n // 32), dtype=np.uint8)
+    signs = _signs(rng, n) if order else None
+    got = _num(hr.dequant_mxfp4(_t(packed), _t(scales), order or None, None if signs is None else _t(signs), TYPES[dtype]))
+    v = mxfp4.values(packed, scales)
+    want, off = v, 0.0
+    if order:
+        want, off = mxfp4.unrotate(v, order, signs), rotation_error(v, order)
+    tiny = torch.finfo(TYPES[dtype]).tiny * _half_step(TYPES[dtype])     # half a step of subnormals
+    assert (np.abs(got - want) <= off + np.abs(want) * _half_step(TYPES[dtype]) * 1.001 + tiny).all()
+
+
+# ------------------------------------------------------------------ the product
+
+def _operand(rng, rows, k, lo=120, hi=132):
+    return rng.integers(0, 256, (rows, k // 2), dtype=np.uint8), rng.integers(lo, hi, (rows, k // 32), dtype=np.uint8)
+
+
+def check_gemm(got, a, sa, w, sw, dtype):
+    want, size = mxfp4.gemm(a, sa, w, sw)
+    k = 2 * a.shape[1]
+    got, off = _num(got), (k / 64 + 8) * 2.0 ** -22 * size
+    edge = torch.finfo(dtype).max * (1 + _half_step(dtype) / 2)      # the last step is 2 half steps of the largest binade
+    past, inside = np.abs(want) - off >= edge, np.abs(want) + off < edge
+    assert (got[past] == np.copysign(np.inf, want[past])).all() and np.isfinite(got[inside]).all()
+    want, got, off = want[inside], got[inside], off[inside]
+    err = np.abs(got - want)
+    allowed = off + _half_step(dtype) * 1.001 * np.abs(want)
+    assert (err <= allowed).all(), f"{(err / allowed).max():.3g} times what is allowed"
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("k", [32, 64, 96, 128, 160, 480, 512, 1056, 2080])
+@pytest.mark.parametrize("m,n", [(1, 1), (1, 16), (2, 17), (15, 33), (16, 64), (17, 100)])
+def test_gemm_rows(m, n, k, dtype):
+    rng = _rng(m * 1000 + n + k)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=TYPES[dtype])
+    check_gemm(got, *a, *w, TYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16", "f16"])
+@pytest.mark.parametrize("m,n,k", [(33, 70, 256), (64, 128, 512), (65, 256, 288), (100, 333, 1024), (128, 128, 4096),
+                                   (129, 257, 640), (200, 1000, 96), (256, 256, 128), (257, 512, 160), (300, 515, 2048),
+                                   (511, 130, 32), (513, 770, 1120), (1024, 512, 256), (1100, 1300, 352)])
+def test_gemm_tiles(m, n, k, dtype):
+    rng = _rng(m + n + k)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=TYPES[dtype])
+    check_gemm(got, *a, *w, TYPES[dtype])
+
+
+@pytest.mark.parametrize("m", [1, 16, 100, 300])
+def test_gemm_long_rows(m):
+    rng = _rng(m)
+    a, w = _operand(rng, m, 65536), _operand(rng, 72, 65536)
+    check_gemm(hr.mxfp4_gemm(*map(_t, a + w)), *a, *w, torch.float32)
+
+
+@pytest.mark.parametrize("m,n", [(3, 40), (80, 144), (300, 300)])
+def test_gemm_one_code_at_a_time(m, n):
+    """Each operand is one non-zero code a row in a place and block of its own:
+    every place of every fragment and every scale is told apart."""
+    k = 1024
+    rng = _rng(m)
+    for seed in range(3):
+        at = rng.integers(0, k, m)
+        codes = np.zeros((m, k), dtype=np.uint8)
+        codes[np.arange(m), at] = rng.integers(1, 8, m)
+        a = mxfp4.pack(codes), rng.integers(100, 140, (m, k // 32), dtype=np.uint8)
+        w = _operand(rng, n, k, 100, 140)
+        got = _num(hr.mxfp4_gemm(*map(_t, a + w)))
+        want, _ = mxfp4.gemm(*a, *w)
+        assert np.array_equal(got, want)          # one product each: nothing to round
+
+
+@pytest.mark.parametrize("m", [1, 20, 200, 400])
+def test_gemm_nan_scales_stay_in_their_rows(m):
+    rng = _rng(m + 5)
+    n, k = 333, 544
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    clean = hr.mxfp4_gemm(*map(_t, a + w))
+    a[1][m // 2, 3] = 255
+    w[1][n - 1, k // 32 - 1] = 255
+    w[0][n - 1] = 0                                # also over zero codes
+    got = hr.mxfp4_gemm(*map(_t, a + w))
+    assert torch.isnan(got[m // 2]).all() and torch.isnan(got[:, n - 1]).all()
+    keep_m = [i for i in range(m) if i != m // 2]
+    assert torch.equal(got[keep_m][:, :n - 1], clean[keep_m][:, :n - 1])
+
+
+@pytest.mark.parametrize("m", [1, 20, 200, 400])
+def test_gemm_far_scales(m):
+    """Scales at both ends of their range, whose products are not, and zero codes
+    under any of them."""
+    rng = _rng(m + 6)
+    n, k = 50, 256
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    a[1][:], w[1][:] = rng.integers(2, 12, a[1].shape), rng.integers(238, 246, w[1].shape)
+    check_gemm(hr.mxfp4_gemm(*map(_t, a + w)), *a, *w, torch.float32)
+    a[0][:, :16] = 0                               # blocks of zeros
+    a[1][:, 0] = 0
+    check_gemm(hr.mxfp4_gemm(*map(_t, a + w)), *a, *w, torch.float32)
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 512, 1024), (40, 96, 512), (300, 260, 512)])
+def test_gemm_same_every_time_and_outside_untouched(m, n, k):
+    rng = _rng(9)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    args = [_t(v) for v in a + w]
+    guard = torch.full((m + 2, n), 7.0, device=DEV)
+    first = hr.mxfp4_gemm(*args)
+    for _ in range(3):
+        out = hr.mxfp4_gemm(*args, out=guard[1:m + 1]) if n % 4 == 0 else hr.mxfp4_gemm(*args)
+        assert torch.equal(out, first)
+    assert (guard[0] == 7.0).all() and (guard[m + 1] == 7.0).all()
+
+
+def test_gemm_no_rows():
+    rng = _rng(1)
+    a, w = _operand(rng, 4, 64), _operand(rng, 4, 64)
+    a, w = [_t(v) for v in a], [_t(v) for v in w]
+    assert hr.mxfp4_gemm(a[0][:0], a[1][:0], *w).shape == (0, 4)
+    assert hr.mxfp4_gemm(*a, w[0][:0], w[1][:0]).shape == (4, 0)
+
+
+# ------------------------------------------------------------------ together
+
+@pytest.mark.parametrize("m", [1, 16, 300])
+def test_rotation_quantization_and_product_as_a_layer_uses_them(m):
+    """Both operands are rotated alike, so the product of the codes is that of the
+    rows read back and rotated back.  Those are near the rows they stand for: a
+    value in a code's normal range is off by at most 1/5 of itself (1.25 -> 1, 2.5,
+    5), or 1/4 where it saturates (8 -> 6), a smaller one by 1/4 of the scale, and
+    the largest of the block is at least 3 scales (ceil; 4 with floor): 1/12 of
+    it.  Rotated back that is a 2-norm over each Hadamard block."""
+    rng = _rng(m)
+    n, k = 384, 1024
+    x, w = _rows(rng, m, k, torch.bfloat16), _rows(rng, n, k, torch.bfloat16, 0.0)
+    s = _signs(rng, k)
+    xq, wq = hr.rotate_quant_mxfp4(x, 128, _t(s)), hr.rotate_quant_mxfp4(w, 128, _t(s), "ceil")
+    c = _num(hr.mxfp4_gemm(*xq, *wq))
+    xb, wb = (hr.dequant_mxfp4(*q, 128, _t(s)) for q in (xq, wq))
+    for rows, back in ((x, xb), (w, wb)):
+        y = mxfp4.rotate(_num(rows), 128, s).reshape(rows.shape[0], -1, 4, 32)
+        off = np.maximum(np.abs(y) / 4, np.abs(y).max(-1, keepdims=True) / 12)
+        off = np.sqrt((off ** 2).sum((-1, -2)))
+        got = np.sqrt(((_num(back) - _num(rows)).reshape(rows.shape[0], -1, 128) ** 2).sum(-1))
+        assert (got <= off * (1 + 2.0 ** -10)).all()
+    _, size = mxfp4.gemm(*(v.cpu().numpy() for v in xq + wq))
+    xs, ws = _num(xb), _num(wb)
+    # what reading back in fp32 leaves of each operand, times the other's size
+    turn = rotation_error(xs, 128) @ np.abs(ws).T + np.abs(xs) @ rotation_error(ws, 128).T
+    assert (np.abs(c - xs @ ws.T) <= (k / 64 + 8) * 2.0 ** -22 * size + 2 * turn).all()
+
+
+def test_captured_and_replayed():
+    rng = _rng(11)
+    x = _rows(rng, 40, 512, torch.bfloat16)
+    w = hr.quant_mxfp4(_rows(rng, 96, 512, torch.bfloat16))
+    signs = _t(_signs(rng, 512))
+
+    def step():
+        return hr.mxfp4_gemm(*hr.rotate_quant_mxfp4(x, 64, signs), *w, dtype=torch.bfloat16)
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for seed in range(4):
+        x.copy_(_rows(_rng(seed), 40, 512, torch.bfloat16))
+        want = step()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
+def test_two_streams():
+    rng = _rng(12)
+    xs = [_rows(rng, 300, 1024, torch.bfloat16) for _ in range(2)]
+    w = hr.quant_mxfp4(_rows(rng, 512, 1024, torch.bfloat16))
+    want = [hr.mxfp4_gemm(*hr.quant_mxfp4(x), *w) for x in xs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    got = []
+    for _ in range(5):
+        got = []
+        for s, x in zip(streams, xs):
+            with torch.cuda.stream(s):
+                got.append(hr.mxfp4_gemm(*hr.quant_mxfp4(x), *w))
+    torch.cuda.synchronize()
+    assert all(torch.equal(g, v) for g, v in zip(got, want))
