@@ -44,6 +44,7 @@ struct Mx4GemmArgs {
   int K;
   int dtype;             // of c
   void* c;               // [M][N]
+  int stream;            // set by the launcher: nontemporal stores of c
 };
 
 // r = x + scale gate (block or its norm), h = weight r / rms(r), after host

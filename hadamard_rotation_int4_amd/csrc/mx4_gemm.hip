@@ -29,60 +29,385 @@ __device__ __forceinline__ void store_c(const Mx4GemmArgs& p, int64_t at, float 
   else reinterpret_cast<_Float16*>(p.c)[at] = (_Float16)v;
 }
 
-// 16 columns and 16 MT rows of C a workgroup; its waves take the steps of 128
-// along K in turn and their sums are joined in LDS, in the waves' order.
-constexpr int kRowWaves = 8;
+// Eight of them, 16-byte aligned; around the L2s where C is large.
+__device__ __forceinline__ void store_octet_c(const Mx4GemmArgs& p, int64_t at, const float* v) {
+  if (p.stream) {
+    if (p.dtype == kDtF32) store_vec<kDtF32, 8, true>(reinterpret_cast<float*>(p.c) + at, v);
+    else if (p.dtype == kDtBf16) store_vec<kDtBf16, 8, true>(reinterpret_cast<uint16_t*>(p.c) + at, v);
+    else store_vec<kDtF16, 8, true>(reinterpret_cast<uint16_t*>(p.c) + at, v);
+  } else {
+    store_vec_any<8>(p.dtype, p.c, at, v);
+  }
+}
 
-template <int MT>
-__global__ __launch_bounds__(64 * kRowWaves) void mx4_gemm_rows_kernel(Mx4GemmArgs p) {
-  __shared__ v4f part[kRowWaves][MT][64];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+// 16 columns and 16 MT rows of C a workgroup.  K goes in runs of 512 codes (four
+// steps of 128: 256 bytes of a row and 16 of its scales), which the waves take in
+// turn straight from memory into registers, all loads of a run before its products;
+// their sums are joined in LDS, in the waves' order.
+template <int MT, int WAVES>
+__global__ __launch_bounds__(64 * WAVES) void mx4_gemm_rows_kernel(Mx4GemmArgs p) {
+  struct __attribute__((packed, aligned(1))) Scales { uint32_t v[4]; };
+  __shared__ v4f part[WAVES][MT][64];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int r = lane & 15, kb = lane >> 4;
   const int64_t n0 = (int64_t)blockIdx.x * 16, m0 = (int64_t)blockIdx.y * (16 * MT);
-  const int blocks = p.K / kMxBlock, steps = (blocks + 3) / 4;
-  const int64_t wrow = n0 + r < p.N ? n0 + r : p.N - 1;     // rows past the end: the last again, stored nowhere
-  int64_t arow[MT];
+  const int blocks = p.K / kMxBlock, runs = blocks / 16;
+  // rows past the end: the last again, stored nowhere
+  const int64_t wrow = n0 + r < p.N ? n0 + r : p.N - 1;
+  const uint8_t* const w = p.w + wrow * (p.K / 2) + 16 * kb;
+  const uint8_t* const sw = p.sw + wrow * blocks;
+  const uint8_t* a[MT];
+  const uint8_t* sa[MT];
 #pragma unroll
-  for (int t = 0; t < MT; ++t) arow[t] = m0 + 16 * t + r < p.M ? m0 + 16 * t + r : p.M - 1;
+  for (int t = 0; t < MT; ++t) {
+    const int64_t row = m0 + 16 * t + r < p.M ? m0 + 16 * t + r : p.M - 1;
+    a[t] = p.a + row * (p.K / 2) + 16 * kb;
+    sa[t] = p.sa + row * blocks;
+  }
   v4f acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int s = wave; s < steps; s += kRowWaves) {
-    const int j = 4 * s + kb;
-    const bool live = j < blocks;                           // past the end: zero codes and scales
-    const uint4 z = make_uint4(0u, 0u, 0u, 0u);
-    const uint4 wc = live ? *reinterpret_cast<const uint4*>(p.w + wrow * (p.K / 2) + 16 * j) : z;
-    const int ws = live ? p.sw[wrow * blocks + j] : 0;
+  for (int q = wave; q < runs; q += WAVES) {
+    uint4 wc[4], ac[MT][4];
+    Scales as[MT];
+#pragma unroll
+    for (int s = 0; s < 4; ++s) wc[s] = *reinterpret_cast<const uint4*>(w + 256 * q + 64 * s);
+    const Scales ws = *reinterpret_cast<const Scales*>(sw + 16 * q);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
-      const uint4 ac = live ? *reinterpret_cast<const uint4*>(p.a + arow[t] * (p.K / 2) + 16 * j) : z;
-      const int as = live ? p.sa[arow[t] * blocks + j] : 0;
-      acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wc), fp4_operand(ac), acc[t], kFp4, kFp4, 0, ws,
-                                                                0, as);
+#pragma unroll
+      for (int s = 0; s < 4; ++s) ac[t][s] = *reinterpret_cast<const uint4*>(a[t] + 256 * q + 64 * s);
+      as[t] = *reinterpret_cast<const Scales*>(sa[t] + 16 * q);
+    }
+#pragma unroll
+    for (int s = 0; s < 4; ++s)
+#pragma unroll
+      for (int t = 0; t < MT; ++t)
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wc[s]), fp4_operand(ac[t][s]), acc[t], kFp4,
+                                                                  kFp4, 0, (int)(ws.v[s] >> (8 * kb)), 0,
+                                                                  (int)(as[t].v[s] >> (8 * kb)));
+  }
+  // what is left of K: fewer than four steps, past its end zero codes and scales
+  if (wave == runs % WAVES) {
+    for (int j = 16 * runs + kb; j < blocks + kb; j += 4) {
+      const bool live = j < blocks;
+      const uint4 z = make_uint4(0u, 0u, 0u, 0u);
+      const uint4 wc = live ? *reinterpret_cast<const uint4*>(w + 16 * (j - kb)) : z;
+      const int ws = live ? sw[j] : 0;
+#pragma unroll
+      for (int t = 0; t < MT; ++t) {
+        const uint4 ac = live ? *reinterpret_cast<const uint4*>(a[t] + 16 * (j - kb)) : z;
+        const int as = live ? sa[t][j] : 0;
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wc), fp4_operand(ac), acc[t], kFp4, kFp4, 0, ws,
+                                                                  0, as);
+      }
     }
   }
 #pragma unroll
   for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
   __syncthreads();
-  for (int i = threadIdx.x; i < MT * 64; i += 64 * kRowWaves) {
+  const bool quads = p.N % 4 == 0;
+  for (int i = threadIdx.x; i < MT * 64; i += 64 * WAVES) {
     const int t = i >> 6, l = i & 63;
     v4f c = part[0][t][l];
 #pragma unroll
-    for (int w = 1; w < kRowWaves; ++w) c += part[w][t][l];
+    for (int v = 1; v < WAVES; ++v) c += part[v][t][l];
     const int64_t m = m0 + 16 * t + (l & 15), n = n0 + 4 * (l >> 4);
     if (m >= p.M) continue;
+    const float x[4] = {c[0], c[1], c[2], c[3]};
+    if (quads) {
+      if (n < p.N) store_vec_any<4>(p.dtype, p.c, m * p.N + n, x);
+    } else {
 #pragma unroll
-    for (int v = 0; v < 4; ++v)
-      if (n + v < p.N) store_c(p, m * p.N + n + v, c[v]);
+      for (int v = 0; v < 4; ++v)
+        if (n + v < p.N) store_c(p, m * p.N + n + v, x[v]);
+    }
   }
 }
 
-hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t s) {
-  const unsigned cols = (unsigned)((a.N + 15) / 16);
-  if (a.M <= 16)
-    hipLaunchKernelGGL((mx4_gemm_rows_kernel<1>), dim3(cols, (unsigned)((a.M + 15) / 16)), dim3(64 * kRowWaves), 0, s, a);
-  else
-    hipLaunchKernelGGL((mx4_gemm_rows_kernel<4>), dim3(cols, (unsigned)((a.M + 63) / 64)), dim3(64 * kRowWaves), 0, s, a);
+// ---------------------------------------------------------------- tiles
+
+template <int V>
+struct MxC { static constexpr int value = V; };
+
+// Workgroup barrier that leaves the caller's own waits as they are (the compiler
+// drains every outstanding memory operation before the barriers that it emits).
+__device__ __forceinline__ void mx_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
+constexpr int kNowhere = 0x40000000;     // past the end of every panel of an operand
+constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
+
+// (32 WM TM) x (32 WN TN) outputs a workgroup of WM WN waves, TM x TN tiles of
+// v_mfma_scale_f32_32x32x64_f8f6f4 a wave.
+//
+// A stage is 256 codes of K: 128 bytes of each row, copied from memory into LDS
+// (8 rows an instruction), two stages in LDS.  A lane of the instruction holds
+// row l % 32 of its operand and 32 codes; half h = l / 32 takes blocks 4 h + s at
+// step s < 4 of a stage, so that one 4-byte word holds a lane's scales of the
+// stage and the step picks its byte.  In LDS the 16-byte chunk c of row r sits
+// at chunk c ^ (r % 8): 8 consecutive rows of one chunk, which a read serves at
+// once, lie in 8 different places.  The copy writes LDS in lane order, so it is
+// the source chunk of a lane that is permuted, within the row's 128 bytes.
+//
+// SL: scales come through LDS too, 16 bytes of each row every second stage (for K
+// a multiple of 128: whole words); else each lane loads its own words.
+template <int WM, int WN, int TM, int TN, bool SL, int OCC>
+__global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
+  constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
+  constexpr int ROWB = 128;                        // bytes of a row and stage
+  constexpr int QA = BM / 8, QW = BN / 8;          // copies of 1 KB of a stage
+  constexpr int DPW = (QA + QW) / WAVES;
+  constexpr int SCB = SL ? (BM + BN) * 16 : 16;    // scales of two stages
+  constexpr int QS = (BM + BN) / 64, SPW = (QS + WAVES - 1) / WAVES;
+  static_assert((QA + QW) % WAVES == 0, "equal copies a wave");
+  static_assert(!SL || (BM % 64 == 0 && BN % 64 == 0), "a copy of scales stays in one operand");
+  __shared__ __attribute__((aligned(16))) char sbuf0[(BM + BN) * ROWB];
+  __shared__ __attribute__((aligned(16))) char sbuf1[(BM + BN) * ROWB];
+  __shared__ __attribute__((aligned(16))) char sscale[2 * SCB];
+  const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN * (32 * TM), wn = wave % WN * (32 * TN);
+
+  // Workgroups go round the 8 dies in turn: each die takes a run of consecutive
+  // tiles, which go down 8 rows of tiles before the next column, so that the
+  // dies' L2s share panels of both operands.
+  const int total = tiles_m * tiles_n, die = blockIdx.x & 7;
+  const int tile = die * (total >> 3) + min(die, total & 7) + (int)(blockIdx.x >> 3);
+  const int width = 8 * tiles_n, group = tile / width, in = tile - group * width;
+  const int high = min(8, tiles_m - 8 * group);
+  const int64_t m0 = (int64_t)(8 * group + in % high) * BM, n0 = (int64_t)(in / high) * BN;
+
+  const int blocks = p.K / kMxBlock, stages = (blocks + 7) / 8, stride = p.K / 2;
+  const int rows_a = (int)(p.M - m0 < BM ? p.M - m0 : BM), rows_w = (int)(p.N - n0 < BN ? p.N - n0 : BN);
+  // rows past the end lie past the buffer's end: nothing is read there, and what
+  // LDS holds for them (codes are finite whatever they are) goes into outputs
+  // that are not stored
+  const __amdgpu_buffer_rsrc_t ra =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + m0 * stride), 0, rows_a * stride, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rw =
+      __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + n0 * stride), 0, rows_w * stride, 0x00020000);
+  const int chunk = (lane & 7) ^ (lane >> 3);
+  const int src = (lane >> 3) * stride + 16 * chunk;
+  // the last stage: chunks past the end take the row's last one (under zero scales)
+  const int last = 8 * (stages - 1);
+  const int src_last = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
+  auto buf = [&](auto b) -> char* {
+    if constexpr (decltype(b)::value == 0) return sbuf0;
+    else return sbuf1;
+  };
+  // stage s into buffer b; behind the last stage nothing is read (the loop has no
+  // branch: the compiler would move products over it)
+  auto copy = [&](int s, auto b) {
+    char* dst = buf(b);
+    const int v = s < stages - 1 ? src : s < stages ? src_last : kNowhere;
+#pragma unroll
+    for (int j = 0; j < DPW; ++j) {
+      const int q = wave * DPW + j;
+      const bool a = q < QA;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? ra : rw,
+                                               (__attribute__((address_space(3))) void*)(dst + 1024 * q), 16, v,
+                                               8 * (a ? q : q - QA) * stride + s * ROWB, 0, 0);
+    }
+  };
+
+  // Scales: the 4-byte word of blocks 8 s + 4 h .. + 3 of each of this lane's rows.
+  // Past the end of a row words are zero.  A zero byte is 2^-127, and in both
+  // operands its products are below 2^-240 and count as 0 whatever the codes are.
+  const uint8_t* const sa = p.sa + m0 * blocks;
+  const uint8_t* const sw = p.sw + n0 * blocks;
+  uint32_t sc[T], sn[T], srow[T];
+  const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc((void*)sa, 0, rows_a * blocks, 0x00020000);
+  const __amdgpu_buffer_rsrc_t rsw = __builtin_amdgcn_make_buffer_rsrc((void*)sw, 0, rows_w * blocks, 0x00020000);
+#pragma unroll
+  for (int i = 0; i < T; ++i) {
+    const int r = i < TM ? wm + 32 * i + l32 : wn + 32 * (i - TM) + l32;
+    if (SL) srow[i] = (uint32_t)(i < TM ? r : BM + r) * 16 + 4 * h;
+    else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
+  }
+  auto copy_scales = [&](int t) {                   // of stages 2 t and 2 t + 1
+    const int v = 2 * t < stages ? lane * blocks : kNowhere;
+#pragma unroll
+    for (int j = 0; j < SPW; ++j) {
+      const int q = wave * SPW + j;
+      const bool a = q < BM / 64;
+      if (QS % WAVES == 0 || q < QS)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? rsa : rsw,
+                                                 (__attribute__((address_space(3))) void*)(sscale + (t & 1) * SCB + 1024 * q),
+                                                 16, v, 64 * (a ? q : q - BM / 64) * blocks + 16 * t, 0, 0);
+    }
+  };
+  auto load_scales = [&](int s, uint32_t* v) {
+    if constexpr (SL) {
+#pragma unroll
+      for (int i = 0; i < T; ++i)
+        v[i] = *reinterpret_cast<const uint32_t*>(sscale + ((s >> 1) & 1) * SCB + (s & 1) * 8 + srow[i]);
+    } else {
+      // past the end of a row its last word, shifted by use_scales
+      struct __attribute__((packed, aligned(1))) U { uint32_t v; };
+      const uint32_t from = min(8 * s + 4 * h, blocks - 4);
+#pragma unroll
+      for (int i = 0; i < T; ++i) v[i] = reinterpret_cast<const U*>((i < TM ? sa : sw) + (srow[i] + from))->v;
+    }
+  };
+  auto use_scales = [&](int s, const uint32_t* v) {
+    if constexpr (SL) {
+      const bool past = 8 * s + 4 * h >= blocks;
+#pragma unroll
+      for (int i = 0; i < T; ++i) sc[i] = past ? 0u : v[i];
+    } else {
+      const int half = 4 * min(max(8 * s + 4 * h - (blocks - 4), 0), 4);      // in two shifts: they may be 32 together
+#pragma unroll
+      for (int i = 0; i < T; ++i) sc[i] = v[i] >> half >> half;
+    }
+  };
+
+  typedef float v16f __attribute__((ext_vector_type(16)));
+  v16f acc[TN][TM];
+#pragma unroll
+  for (int j = 0; j < TN; ++j)
+#pragma unroll
+    for (int i = 0; i < TM; ++i) acc[j][i] = (v16f){};
+
+  int at[4];                       // of chunk 4 h + s of this lane's row in a tile
+#pragma unroll
+  for (int s = 0; s < 4; ++s) at[s] = l32 * ROWB + 16 * ((4 * h + s) ^ (l32 & 7));
+  auto read = [&](auto b, int s, uint4 (&f)[T]) {
+    const char* base = buf(b);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) f[i] = *reinterpret_cast<const uint4*>(base + at[s] + (wm + 32 * i) * ROWB);
+#pragma unroll
+    for (int j = 0; j < TN; ++j) f[TM + j] = *reinterpret_cast<const uint4*>(base + at[s] + (BM + wn + 32 * j) * ROWB);
+  };
+  auto multiply = [&](auto sc_, const uint4 (&f)[T]) {
+    constexpr int S = decltype(sc_)::value;
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TN; ++j)
+        acc[j][i] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(fp4_operand(f[TM + j]), fp4_operand(f[i]), acc[j][i],
+                                                                    kFp4, kFp4, S, (int)sc[TM + j], S, (int)sc[i]);
+  };
+  auto interleave = [&]() {
+#pragma unroll
+    for (int i = 0; i < T; ++i) {
+      __builtin_amdgcn_sched_group_barrier(kSchedDsRead, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(kSchedMfma, TM * TN / T > 0 ? TM * TN / T : 1, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+
+  uint4 f0[T], f1[T];
+  // stage s from buffer B: the fragments of its first step are in f0
+  auto stage = [&](int s, auto b) {
+    constexpr int B = decltype(b)::value;
+    if (!SL) load_scales(s + 1, sn);
+    read(b, 1, f1);
+    multiply(MxC<0>{}, f0);
+    interleave();
+    read(b, 2, f0);
+    multiply(MxC<1>{}, f1);
+    interleave();
+    read(b, 3, f1);
+    multiply(MxC<2>{}, f0);
+    interleave();
+    // every read of this buffer is done and the next stage has landed, in every wave
+    __builtin_amdgcn_s_waitcnt(0x0070);            // vmcnt(0) lgkmcnt(0)
+    mx_barrier();
+    if (SL) load_scales(s + 1, sn);
+    read(MxC<1 - B>{}, 0, f0);                     // behind the last stage: nothing uses it
+    copy(s + 2, b);
+    if (SL && B == 0) copy_scales((s + 2) >> 1);
+    multiply(MxC<3>{}, f1);
+    interleave();
+    use_scales(s + 1, sn);
+  };
+
+  copy(0, MxC<0>{});
+  if (SL) copy_scales(0);
+  else load_scales(0, sn);
+  copy(1, MxC<1>{});
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  mx_barrier();
+  if (SL) load_scales(0, sn);
+  use_scales(0, sn);
+  read(MxC<0>{}, 0, f0);
+  int s = 0;
+  for (; s + 2 <= stages; s += 2) {
+    stage(s, MxC<0>{});
+    stage(s + 1, MxC<1>{});
+  }
+  if (s < stages) stage(s, MxC<0>{});
+  // no copy is left when LDS is written again or goes to another workgroup
+  __builtin_amdgcn_s_waitcnt(0x0070);
+  mx_barrier();
+
+  // A lane holds row l32 of a tile and columns 8 (v / 4) + 4 h + v % 4.  A wave turns
+  // 32 rows of its columns at a time in its own part of LDS, so that rows are stored
+  // whole; 16-byte unit u of row r at u ^ (r % 8).
+  constexpr int CW = 32 * TN, PITCH = CW * 4;
+  static_assert(32 * PITCH * WAVES <= 2 * (BM + BN) * ROWB, "fits where the stages were");
+  constexpr int HALF = (BM + BN) * ROWB / (32 * PITCH);    // waves whose part fits in the first buffer
+  char* const part = wave < HALF ? sbuf0 + wave * (32 * PITCH) : sbuf1 + (wave - HALF) * (32 * PITCH);
+  const bool octets = p.N % 8 == 0;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        *reinterpret_cast<v4f*>(part + l32 * PITCH + 16 * ((8 * j + 2 * q + h) ^ (l32 & 7))) =
+            (v4f){acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    __builtin_amdgcn_wave_barrier();
+    if (octets) {
+      constexpr int LPR = CW / 8;                  // lanes of a row
+#pragma unroll
+      for (int r = 0; r < 32; r += 64 / LPR) {
+        const int rr = r + lane / LPR, n = 8 * (lane % LPR), m = wm + 32 * i + rr;
+        const v4f x = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4) ^ (rr & 7)));
+        const v4f y = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4 + 1) ^ (rr & 7)));
+        const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+        if (m < rows_a && wn + n < rows_w) store_octet_c(p, (m0 + m) * p.N + n0 + wn + n, v);
+      }
+    } else {
+      for (int r = 0; r < 32; ++r)
+#pragma unroll
+        for (int n = 0; n < CW; n += 64) {
+          const int m = wm + 32 * i + r, c = n + lane;
+          if ((CW % 64 == 0 || c < CW) && m < rows_a && wn + c < rows_w)
+            store_c(p, (m0 + m) * p.N + n0 + wn + c, *reinterpret_cast<const float*>(part + r * PITCH + 16 * ((c / 4) ^ (r & 7)) + 4 * (c % 4)));
+        }
+    }
+    __builtin_amdgcn_wave_barrier();
+  }
+}
+
+template <int WM, int WN, int TM, int TN, bool SL, int OCC>
+static void launch_tile(const Mx4GemmArgs& a, hipStream_t s) {
+  constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
+  const int tm = (int)((a.M + BM - 1) / BM), tn = (int)((a.N + BN - 1) / BN);
+  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, SL, OCC>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, s, a, tm,
+                     tn);
+}
+
+template <int MT, int WAVES>
+static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
+  hipLaunchKernelGGL((mx4_gemm_rows_kernel<MT, WAVES>), dim3((unsigned)((a.N + 15) / 16), (unsigned)((a.M + 16 * MT - 1) / (16 * MT))),
+                     dim3(64 * WAVES), 0, s, a);
+}
+
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
+  Mx4GemmArgs a = args;
+  a.stream = a.M * a.N * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
+  if (a.M <= 16) launch_rows<1, 8>(a, s);
+  else if (a.M <= 64 || a.K < 128) launch_rows<4, 8>(a, s);
+  else if (a.K % 128) {
+    if (a.M <= 512) launch_tile<2, 2, 1, 2, false, 2>(a, s);
+    else launch_tile<4, 2, 2, 4, false, 1>(a, s);
+  } else {
+    if (a.M <= 512) launch_tile<2, 2, 1, 2, true, 2>(a, s);
+    else launch_tile<4, 2, 2, 4, true, 1>(a, s);
+  }
   return hipGetLastError();
 }
 
