@@ -22,6 +22,7 @@ struct Mx4QuantArgs {
   int ceil;              // scale rule: 1: the largest element never saturates
   uint8_t* codes;        // [rows][n / 2]
   uint8_t* scales;       // [rows][n / 32]
+  int stream;            // set by the launcher: nontemporal loads of x
 };
 
 struct Mx4DequantArgs {
@@ -33,6 +34,7 @@ struct Mx4DequantArgs {
   const int8_t* signs;
   int dtype;             // of y
   void* y;               // [rows][n]
+  int stream;            // set by the launcher: nontemporal stores of y
 };
 
 struct Mx4GemmArgs {
@@ -72,6 +74,9 @@ struct NormArgs {
 
 hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t s);
 hipError_t launch_mx4_dequant(const Mx4DequantArgs& a, hipStream_t s);
+// Their parts where 16-bit rows are rotated.
+void launch_mx4_rotate_quant(const Mx4QuantArgs& a, hipStream_t s);
+void launch_mx4_rotate_back(const Mx4DequantArgs& a, hipStream_t s);
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
 

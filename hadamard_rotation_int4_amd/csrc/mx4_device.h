@@ -54,20 +54,24 @@ __device__ __forceinline__ float mx4_absmax(const float* w) {
   return __builtin_elementwise_maximum(m, fabsf(w[7]));
 }
 
-// Scale byte of the block of this quad, from the lane's own largest magnitude
-// m.  The exponent of the largest less that of 4 (the largest binade of e2m1),
-// so that it scales to [4, 8) and what is over 6 saturates; with `ceil` one
-// more where it is over 6.  Not below 2^-127; 255 when the largest is not
-// finite (infinity and NaN have the highest bits, so the integer maximum finds
-// them).
-__device__ __forceinline__ uint32_t mx4_scale(float m, int ceil) {
-  uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
-  a = umax_dpp<kQuadXor1>(a);
-  a = umax_dpp<kQuadXor2>(a);
+// Scale byte of a block from the bits of its largest magnitude.  The exponent of
+// the largest less that of 4 (the largest binade of e2m1), so that it scales to
+// [4, 8) and what is over 6 saturates; with `ceil` one more where it is over 6.  Not
+// below 2^-127; 255 when the largest is not finite (infinity and NaN have the
+// highest bits, so an integer maximum finds them).
+__device__ __forceinline__ uint32_t mx4_scale_byte(uint32_t a, int ceil) {
   // adding what takes a mantissa over 0.5 past 1 raises the exponent
   const uint32_t e = (a + (ceil ? 0x3FFFFFu : 0u)) >> 23;
   const uint32_t b = e > 2u ? e - 2u : 0u;
   return a >= 0x7F800000u ? 255u : b;
+}
+
+// The same for the block of this quad, from the lane's own largest magnitude m.
+__device__ __forceinline__ uint32_t mx4_scale(float m, int ceil) {
+  uint32_t a = __float_as_uint(m) & 0x7FFFFFFFu;
+  a = umax_dpp<kQuadXor1>(a);
+  a = umax_dpp<kQuadXor2>(a);
+  return mx4_scale_byte(a, ceil);
 }
 
 // The 8 codes of w under scale byte b, element e in bits 4 e .. 4 e + 3:
@@ -91,6 +95,22 @@ __device__ __forceinline__ void mx4_levels(uint32_t r, float* w) {
   const f32x2 q3 = __builtin_amdgcn_cvt_scalef32_pk_f32_fp4(r, 1.0f, 3);
   w[0] = q0[0]; w[1] = q0[1]; w[2] = q1[0]; w[3] = q1[1];
   w[4] = q2[0]; w[5] = q2[1]; w[6] = q3[0]; w[7] = q3[1];
+}
+
+// The same in 16 bits, two to a word (every level is exact in either type).
+template <int DT>
+__device__ __forceinline__ void mx4_levels16(uint32_t r, u32x4& x) {
+  if constexpr (DT == kDtBf16) {
+    x[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, 1.0f, 0));
+    x[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, 1.0f, 1));
+    x[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, 1.0f, 2));
+    x[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(r, 1.0f, 3));
+  } else {
+    x[0] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(r, 1.0f, 0));
+    x[1] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(r, 1.0f, 1));
+    x[2] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(r, 1.0f, 2));
+    x[3] = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_f16_fp4(r, 1.0f, 3));
+  }
 }
 
 // 2^(b - 127): a subnormal for b = 0, NaN for 255.

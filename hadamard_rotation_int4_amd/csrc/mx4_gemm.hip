@@ -152,21 +152,26 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 //
 // SL: scales come through LDS too, 16 bytes of each row every second stage (for K
 // a multiple of 128: whole words); else each lane loads its own words.
-template <int WM, int WN, int TM, int TN, bool SL, int OCC>
-__global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
+//
+// KG: teams of WM WN waves that take pairs of stages in turn, each with buffers of
+// its own; their sums are joined in LDS, in the teams' order.  A stage of a small
+// tile takes as long as its loads do, and KG teams have KG times as many under way.
+template <int WM, int WN, int TM, int TN, int KG, bool SL, int OCC>
+__global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
   constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
   constexpr int ROWB = 128;                        // bytes of a row and stage
   constexpr int QA = BM / 8, QW = BN / 8;          // copies of 1 KB of a stage
   constexpr int DPW = (QA + QW) / WAVES;
-  constexpr int SCB = SL ? (BM + BN) * 16 : 16;    // scales of two stages
-  constexpr int QS = (BM + BN) / 64, SPW = (QS + WAVES - 1) / WAVES;
+  constexpr int SA = (BM + 63) / 64, QS = SA + (BN + 63) / 64;   // copies of 64 rows' scales of two stages
+  constexpr int SCB = SL ? QS * 1024 : 16, SPW = (QS + WAVES - 1) / WAVES;
+  constexpr int BUF = (BM + BN) * ROWB;
   static_assert((QA + QW) % WAVES == 0, "equal copies a wave");
-  static_assert(!SL || (BM % 64 == 0 && BN % 64 == 0), "a copy of scales stays in one operand");
-  __shared__ __attribute__((aligned(16))) char sbuf0[(BM + BN) * ROWB];
-  __shared__ __attribute__((aligned(16))) char sbuf1[(BM + BN) * ROWB];
-  __shared__ __attribute__((aligned(16))) char sscale[2 * SCB];
+  __shared__ __attribute__((aligned(16))) char sbuf0[KG * BUF];
+  __shared__ __attribute__((aligned(16))) char sbuf1[KG * BUF];
+  __shared__ __attribute__((aligned(16))) char sscale[KG * 2 * SCB];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int team = KG == 1 ? 0 : wave_all / WAVES, wave = wave_all - team * WAVES;
   const int wm = wave / WN * (32 * TM), wn = wave % WN * (32 * TN);
 
   // Workgroups go round the 8 dies in turn: each die takes a run of consecutive
@@ -193,9 +198,11 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4Gem
   const int last = 8 * (stages - 1);
   const int src_last = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
   auto buf = [&](auto b) -> char* {
-    if constexpr (decltype(b)::value == 0) return sbuf0;
-    else return sbuf1;
+    if constexpr (decltype(b)::value == 0) return sbuf0 + team * BUF;
+    else return sbuf1 + team * BUF;
   };
+  // the team's stage i as a stage of K
+  auto place = [&](int i) { return KG == 1 ? i : 2 * (KG * (i >> 1) + team) + (i & 1); };
   // stage s into buffer b; behind the last stage nothing is read (the loop has no
   // branch: the compiler would move products over it)
   auto copy = [&](int s, auto b) {
@@ -222,41 +229,42 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4Gem
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const int r = i < TM ? wm + 32 * i + l32 : wn + 32 * (i - TM) + l32;
-    if (SL) srow[i] = (uint32_t)(i < TM ? r : BM + r) * 16 + 4 * h;
+    if (SL) srow[i] = (uint32_t)(i < TM ? r : 64 * SA + r) * 16 + 4 * h + team * 2 * SCB;
     else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
   }
-  auto copy_scales = [&](int t) {                   // of stages 2 t and 2 t + 1
+  auto copy_scales = [&](int i) {                   // of the team's stages 2 i and 2 i + 1
+    const int t = KG * i + team;
     const int v = 2 * t < stages ? lane * blocks : kNowhere;
 #pragma unroll
     for (int j = 0; j < SPW; ++j) {
       const int q = wave * SPW + j;
-      const bool a = q < BM / 64;
+      const bool a = q < SA;
       if (QS % WAVES == 0 || q < QS)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? rsa : rsw,
-                                                 (__attribute__((address_space(3))) void*)(sscale + (t & 1) * SCB + 1024 * q),
-                                                 16, v, 64 * (a ? q : q - BM / 64) * blocks + 16 * t, 0, 0);
+                                                 (__attribute__((address_space(3))) void*)(sscale + (2 * team + (i & 1)) * SCB + 1024 * q),
+                                                 16, v, 64 * (a ? q : q - SA) * blocks + 16 * t, 0, 0);
     }
   };
-  auto load_scales = [&](int s, uint32_t* v) {
+  auto load_scales = [&](int k, uint32_t* v) {      // of the team's stage k
     if constexpr (SL) {
 #pragma unroll
       for (int i = 0; i < T; ++i)
-        v[i] = *reinterpret_cast<const uint32_t*>(sscale + ((s >> 1) & 1) * SCB + (s & 1) * 8 + srow[i]);
+        v[i] = *reinterpret_cast<const uint32_t*>(sscale + ((k >> 1) & 1) * SCB + (k & 1) * 8 + srow[i]);
     } else {
       // past the end of a row its last word, shifted by use_scales
       struct __attribute__((packed, aligned(1))) U { uint32_t v; };
-      const uint32_t from = min(8 * s + 4 * h, blocks - 4);
+      const uint32_t from = min(8 * place(k) + 4 * h, blocks - 4);
 #pragma unroll
       for (int i = 0; i < T; ++i) v[i] = reinterpret_cast<const U*>((i < TM ? sa : sw) + (srow[i] + from))->v;
     }
   };
-  auto use_scales = [&](int s, const uint32_t* v) {
+  auto use_scales = [&](int k, const uint32_t* v) {
     if constexpr (SL) {
-      const bool past = 8 * s + 4 * h >= blocks;
+      const bool past = 8 * place(k) + 4 * h >= blocks;
 #pragma unroll
       for (int i = 0; i < T; ++i) sc[i] = past ? 0u : v[i];
     } else {
-      const int half = 4 * min(max(8 * s + 4 * h - (blocks - 4), 0), 4);      // in two shifts: they may be 32 together
+      const int half = 4 * min(max(8 * place(k) + 4 * h - (blocks - 4), 0), 4);      // in two shifts: they may be 32 together
 #pragma unroll
       for (int i = 0; i < T; ++i) sc[i] = v[i] >> half >> half;
     }
@@ -298,10 +306,10 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4Gem
   };
 
   uint4 f0[T], f1[T];
-  // stage s from buffer B: the fragments of its first step are in f0
-  auto stage = [&](int s, auto b) {
+  // the team's stage k from buffer B: the fragments of its first step are in f0
+  auto stage = [&](int k, auto b) {
     constexpr int B = decltype(b)::value;
-    if (!SL) load_scales(s + 1, sn);
+    if (!SL) load_scales(k + 1, sn);
     read(b, 1, f1);
     multiply(MxC<0>{}, f0);
     interleave();
@@ -314,41 +322,79 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4Gem
     // every read of this buffer is done and the next stage has landed, in every wave
     __builtin_amdgcn_s_waitcnt(0x0070);            // vmcnt(0) lgkmcnt(0)
     mx_barrier();
-    if (SL) load_scales(s + 1, sn);
+    if (SL) load_scales(k + 1, sn);
     read(MxC<1 - B>{}, 0, f0);                     // behind the last stage: nothing uses it
-    copy(s + 2, b);
-    if (SL && B == 0) copy_scales((s + 2) >> 1);
+    copy(place(k + 2), b);
+    if (SL && B == 0) copy_scales((k + 2) >> 1);
     multiply(MxC<3>{}, f1);
     interleave();
-    use_scales(s + 1, sn);
+    use_scales(k + 1, sn);
   };
 
-  copy(0, MxC<0>{});
+  copy(place(0), MxC<0>{});
   if (SL) copy_scales(0);
   else load_scales(0, sn);
-  copy(1, MxC<1>{});
+  copy(place(1), MxC<1>{});
   __builtin_amdgcn_s_waitcnt(0x0070);
   mx_barrier();
   if (SL) load_scales(0, sn);
   use_scales(0, sn);
   read(MxC<0>{}, 0, f0);
-  int s = 0;
-  for (; s + 2 <= stages; s += 2) {
-    stage(s, MxC<0>{});
-    stage(s + 1, MxC<1>{});
+  // every team runs the same number: behind the end of K under zero scales
+  const int turns = KG == 1 ? stages : (stages + 2 * KG - 1) / (2 * KG) * 2;
+  int k = 0;
+  for (; k + 2 <= turns; k += 2) {
+    stage(k, MxC<0>{});
+    stage(k + 1, MxC<1>{});
   }
-  if (s < stages) stage(s, MxC<0>{});
+  if (k < turns) stage(k, MxC<0>{});
   // no copy is left when LDS is written again or goes to another workgroup
   __builtin_amdgcn_s_waitcnt(0x0070);
   mx_barrier();
+
+  constexpr int PER = WAVES * TM * TN * 4096, FIT = KG * BUF / PER;      // bytes of a team's sums; teams in a buffer
+  if constexpr (KG > 1) {
+    // the sums of the teams but the first, [wave][tile][quad][lane]
+    static_assert(KG - 1 <= 2 * FIT, "fits where the stages were");
+    auto part = [&](int g, int i, int j, int q) {
+      char* base = g <= FIT ? sbuf0 + (g - 1) * PER : sbuf1 + (g - 1 - FIT) * PER;
+      return reinterpret_cast<v4f*>(base + ((((wave * TM + i) * TN + j) * 4 + q) * 64 + lane) * 16);
+    };
+    if (team > 0) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            *part(team, i, j, q) =
+                (v4f){acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
+    }
+    __syncthreads();
+    if (team > 0) return;
+#pragma unroll
+    for (int g = 1; g < KG; ++g)
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const v4f x = *part(g, i, j, q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[j][i][4 * q + e] += x[e];
+          }
+  }
 
   // A lane holds row l32 of a tile and columns 8 (v / 4) + 4 h + v % 4.  A wave turns
   // 32 rows of its columns at a time in its own part of LDS, so that rows are stored
   // whole; 16-byte unit u of row r at u ^ (r % 8).
   constexpr int CW = 32 * TN, PITCH = CW * 4;
-  static_assert(32 * PITCH * WAVES <= 2 * (BM + BN) * ROWB, "fits where the stages were");
-  constexpr int HALF = (BM + BN) * ROWB / (32 * PITCH);    // waves whose part fits in the first buffer
-  char* const part = wave < HALF ? sbuf0 + wave * (32 * PITCH) : sbuf1 + (wave - HALF) * (32 * PITCH);
+  // with teams behind what they left, which other waves may still be reading
+  constexpr int LEFT0 = (KG - 1 < FIT ? KG - 1 : FIT) * PER, SKIP1 = KG - 1 > FIT ? (KG - 1 - FIT) * PER : 0;
+  constexpr int HALF = SKIP1 ? 0 : (KG * BUF - LEFT0) / (32 * PITCH);      // waves whose part fits in the first buffer
+  static_assert(HALF >= WAVES || SKIP1 + (WAVES - HALF) * 32 * PITCH <= KG * BUF, "fits where the stages were");
+  char* const part = wave < HALF ? sbuf0 + LEFT0 + wave * (32 * PITCH) : sbuf1 + SKIP1 + (wave - HALF) * (32 * PITCH);
   const bool octets = p.N % 8 == 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
@@ -382,12 +428,12 @@ __global__ __launch_bounds__(64 * WM * WN, OCC) void mx4_gemm_tile_kernel(Mx4Gem
   }
 }
 
-template <int WM, int WN, int TM, int TN, bool SL, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, bool SL, int OCC>
 static void launch_tile(const Mx4GemmArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   const int tm = (int)((a.M + BM - 1) / BM), tn = (int)((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, SL, OCC>), dim3((unsigned)(tm * tn)), dim3(64 * WM * WN), 0, s, a, tm,
-                     tn);
+  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, SL, OCC>), dim3((unsigned)(tm * tn)),
+                     dim3(64 * WM * WN * KG), 0, s, a, tm, tn);
 }
 
 template <int MT, int WAVES>
@@ -396,18 +442,40 @@ static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
                      dim3(64 * WAVES), 0, s, a);
 }
 
+// Which tile, by how many of them there are for the 256 compute units: the largest
+// of which there is about one for each (kEnough), a few stragglers costing less than
+// smaller tiles' traffic; fewer of the small ones get teams.  bf16, us, chosen |
+// next smaller | next larger:
+//   256 x 256  1024 x 14336 x 4096 (224 tiles) 34 | 42 | -;   3000 x 5120 x 5120 (240) 43 | 52 | -
+//   128 x 128  512 x 14336 x 4096 (448) 24 | 32 | 30;         1536 x 4096 x 4096 (384) 21 | 27 | 28
+//   64 x 64    512 x 4096 x 4096 (512) 12.2 | 12.4 in teams of 2 | 15.7
+//   in teams   256 x 4096 x 4096 (256) 9.6 | 13.3 | 10.9 alone, 15.4 (128 x 128)
+//   32 x 64    128 x 4096 x 14336 (256), teams of 4, 18 | - | 26
+//   32 x 32    64 x 4096 x 14336 (256), teams of 4, 13 | - | 17
+constexpr int kEnough = 180;
+
+template <bool SL>
+static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
+  auto count = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if (count(256, 256) >= kEnough) launch_tile<4, 2, 2, 4, 1, SL, 1>(a, s);
+  else if (count(128, 128) >= kEnough) launch_tile<2, 2, 2, 2, 1, SL, 2>(a, s);
+  else if (count(64, 64) >= 2 * kEnough) launch_tile<2, 2, 1, 1, 1, SL, 4>(a, s);
+  else if (count(64, 64) >= kEnough) launch_tile<2, 2, 1, 1, 2, SL, 2>(a, s);
+  else if (count(32, 64) >= kEnough) launch_tile<1, 2, 1, 1, 4, SL, 1>(a, s);
+  else launch_tile<1, 1, 1, 1, 4, SL, 1>(a, s);
+}
+
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
   Mx4GemmArgs a = args;
   a.stream = a.M * a.N * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
-  if (a.M <= 16) launch_rows<1, 8>(a, s);
-  else if (a.M <= 64 || a.K < 128) launch_rows<4, 8>(a, s);
-  else if (a.K % 128) {
-    if (a.M <= 512) launch_tile<2, 2, 1, 2, false, 2>(a, s);
-    else launch_tile<4, 2, 2, 4, false, 1>(a, s);
-  } else {
-    if (a.M <= 512) launch_tile<2, 2, 1, 2, true, 2>(a, s);
-    else launch_tile<4, 2, 2, 4, true, 1>(a, s);
-  }
+  // A few rows are bound by the weights' bytes, which go straight to registers: 16 x
+  // 4096 x 14336 9.6 us (32 x 32 tiles 14).  With many columns a 32 x 64 tile reads
+  // the rows of A less often: 16 x 14336 x 4096 8.9 us against 11.5.  Tiles need four
+  // blocks of K.
+  if (a.K < 128) launch_rows<4, 8>(a, s);
+  else if (a.M <= 16 && a.N <= 8192) launch_rows<1, 8>(a, s);
+  else if (a.K % 128 == 0) launch_tiles<true>(a, s);
+  else launch_tiles<false>(a, s);
   return hipGetLastError();
 }
 

@@ -11,7 +11,8 @@
 //
 // A lane takes an octet of a row (8 elements) and everything stays in
 // registers: a Hadamard block is in-lane butterflies and DPP exchanges over
-// order / 8 lanes, a scale a maximum over the 4 lanes of a quad.
+// order / 8 lanes, a scale a maximum over the 4 lanes of a quad.  16-bit rows that
+// are rotated go through the matrix cores instead (mx4_rotate.hip).
 #include "mx4_device.h"
 
 namespace hr {
@@ -136,30 +137,37 @@ static void launch_d(const Mx4DequantArgs& a, int64_t octets, hipStream_t s) {
                      octets, mx4_magic(a.n / 8));
 }
 
-#define HR_MX4_DISPATCH(launch, a, octets, s)                          \
-  do {                                                                 \
-    if (a.dtype == kDtBf16) HR_MX4_ORDER(launch, kDtBf16, a, octets, s) \
-    else if (a.dtype == kDtF16) HR_MX4_ORDER(launch, kDtF16, a, octets, s) \
-    else HR_MX4_ORDER(launch, kDtF32, a, octets, s)                    \
+#define HR_MX4_TYPE(launch, a, octets, s)                  \
+  do {                                                     \
+    if (a.dtype == kDtBf16) launch<kDtBf16, 0>(a, octets, s);  \
+    else if (a.dtype == kDtF16) launch<kDtF16, 0>(a, octets, s); \
+    else launch<kDtF32, 0>(a, octets, s);                  \
   } while (0)
 #define HR_MX4_ORDER(launch, DT, a, octets, s)          \
   switch (a.order) {                                    \
     case 32: launch<DT, 4>(a, octets, s); break;        \
     case 64: launch<DT, 8>(a, octets, s); break;        \
     case 128: launch<DT, 16>(a, octets, s); break;      \
-    case 256: launch<DT, 32>(a, octets, s); break;      \
-    default: launch<DT, 0>(a, octets, s); break;        \
+    default: launch<DT, 32>(a, octets, s); break;       \
   }
 
-hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t s) {
+hipError_t launch_mx4_quant(const Mx4QuantArgs& args, hipStream_t s) {
+  Mx4QuantArgs a = args;
+  a.stream = a.rows * a.n * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
   const int64_t octets = a.rows * (a.n / 8);
-  HR_MX4_DISPATCH(launch_q, a, octets, s);
+  if (a.order && a.dtype != kDtF32) launch_mx4_rotate_quant(a, s);
+  else if (a.order) HR_MX4_ORDER(launch_q, kDtF32, a, octets, s)
+  else HR_MX4_TYPE(launch_q, a, octets, s);
   return hipGetLastError();
 }
 
-hipError_t launch_mx4_dequant(const Mx4DequantArgs& a, hipStream_t s) {
+hipError_t launch_mx4_dequant(const Mx4DequantArgs& args, hipStream_t s) {
+  Mx4DequantArgs a = args;
+  a.stream = a.rows * a.n * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
   const int64_t octets = a.rows * (a.n / 8);
-  HR_MX4_DISPATCH(launch_d, a, octets, s);
+  if (a.order && a.dtype != kDtF32) launch_mx4_rotate_back(a, s);
+  else if (a.order) HR_MX4_ORDER(launch_d, kDtF32, a, octets, s)
+  else HR_MX4_TYPE(launch_d, a, octets, s);
   return hipGetLastError();
 }
 

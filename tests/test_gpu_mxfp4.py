@@ -166,6 +166,43 @@ def test_rotate_quant(rows, blocks, signed, order, dtype, rule):
     check_near(mxfp4.rotate(xs, order, signs), rotation_error(xs, order), codes, scales, rule)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("order", [32, 64, 128, 256])
+@pytest.mark.parametrize("rows,n", [(16390, 1024), (5462, 3 * 1024 + 1024), (3400, 5120), (70000, 256)])
+def test_rotate_quant_many_rows(rows, n, order, dtype):
+    """Calls of many tiles, whose waves take several rows: every row as alone."""
+    rng = _rng(rows)
+    x, signs = _rows(rng, rows, n, TYPES[dtype]), _t(_signs(rng, n))
+    codes, scales = hr.rotate_quant_mxfp4(x, order, signs)
+    back = hr.dequant_mxfp4(codes, scales, order, signs, TYPES[dtype])
+    at = torch.from_numpy(np.unique(np.concatenate([[0, 1, 2, 3, rows - 4, rows - 3, rows - 2, rows - 1],
+                                                    rng.integers(0, rows, 40)]))).to(DEV)
+    some = x[at].contiguous()
+    c, s = hr.rotate_quant_mxfp4(some, order, signs)
+    assert torch.equal(codes[at], c) and torch.equal(scales[at], s)
+    assert torch.equal(back[at], hr.dequant_mxfp4(c, s, order, signs, TYPES[dtype]))
+    xs = _num(some)
+    check_near(mxfp4.rotate(xs, order, signs.cpu().numpy()), rotation_error(xs, order), c, s, "floor")
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("order", [32, 64, 128, 256])
+def test_rotate_quant_tiny_and_large(order, dtype):
+    """Values near both ends of the type, subnormal ones among them."""
+    rng = _rng(order)
+    info = torch.finfo(TYPES[dtype])
+    x = rng.standard_normal((4, 512))
+    # fp32 values small enough that the bound itself is not below fp32's last step
+    small = info.tiny * (4.0 if dtype == "f16" else 2.0 ** 26)
+    x[0] *= small
+    x[1] *= small * 2.0 ** 4
+    x[2] *= info.max / order / 8
+    x = _t(x).to(TYPES[dtype])
+    xs = _num(x)
+    codes, scales = hr.rotate_quant_mxfp4(x, order)
+    check_near(mxfp4.rotate(xs, order), rotation_error(xs, order), codes, scales, "floor")
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 @pytest.mark.parametrize("order", [0, 64, 128])
 def test_strided_rows_and_given_outputs(dtype, order):
@@ -273,6 +310,21 @@ def test_gemm_tiles(m, n, k, dtype):
     a, w = _operand(rng, m, k), _operand(rng, n, k)
     got = hr.mxfp4_gemm(*map(_t, a + w), dtype=TYPES[dtype])
     check_gemm(got, *a, *w, TYPES[dtype])
+
+
+@pytest.mark.parametrize("m,n,k", [(3400, 3601, 256), (3333, 3600, 288), (1700, 1801, 512), (1793, 1700, 544),
+                                   (1400, 1150, 384), (1300, 1201, 416), (832, 1024, 640), (833, 1023, 672),
+                                   (12, 8200, 512), (16, 9001, 160)])
+def test_gemm_every_tile(m, n, k):
+    """Sizes that reach each tile, with whole and with ragged edges and both ways
+    of the scales; rows and columns of all parts of the product."""
+    rng = _rng(m + n + k)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=torch.bfloat16)
+    at = np.unique(np.concatenate([np.arange(min(m, 70)), np.arange(max(0, m - 70), m), rng.integers(0, m, 300)]))
+    check_gemm(got[torch.from_numpy(at).to(DEV)], a[0][at], a[1][at], *w, torch.bfloat16)
+    at = np.unique(np.concatenate([np.arange(70), np.arange(n - 70, n), rng.integers(0, n, 300)]))
+    check_gemm(got[:, torch.from_numpy(at).to(DEV)], *a, w[0][at], w[1][at], torch.bfloat16)
 
 
 @pytest.mark.parametrize("m", [1, 16, 100, 300])
