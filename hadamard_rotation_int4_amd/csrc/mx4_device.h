@@ -12,6 +12,10 @@
 
 namespace hr {
 
+// Workgroup barrier that leaves the caller's own waits as they are (the compiler
+// drains every outstanding memory operation before the barriers that it emits).
+__device__ __forceinline__ void mx_barrier() { asm volatile("s_barrier" ::: "memory"); }
+
 // 1 / sqrt(8 L)
 template <int L>
 __device__ __forceinline__ constexpr float mx4_norm() {
@@ -24,26 +28,48 @@ __device__ __forceinline__ int mx4_lane(int lane) {
   return L >= 8 ? (lane & ~(L - 1)) | kv4_logical<L>(lane) : lane;
 }
 
-// Factor that makes w after mx4_fwht the rotated values: 1 / sqrt(order) and
-// the lane's sign.
+// Whether mx4_fwht leaves this lane's values negated; a: its octet in its block.
 template <int L>
-__device__ __forceinline__ float mx4_factor(int a) {
-  return (__popc(a & (L >= 16 ? 15 : L - 1)) & 1) ? -mx4_norm<L>() : mx4_norm<L>();
-}
+__device__ __forceinline__ bool mx4_negated(int a) { return __popc(a & (L >= 16 ? 15 : L - 1)) & 1; }
 
-// w[0..7] := +-H_{8 L} w over L lanes, a the lane's octet in its block.
+// w[i] += dpp(w[i]) * sigma for 8 registers, as HR_FMAC_DPP16.
+#define HR_FMAC_DPP8(w, sigma, CTRL) \
+  asm volatile("s_nop 1\n\t" \
+"v_fmac_f32_dpp %0, %0, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %1, %1, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %2, %2, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %3, %3, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %4, %4, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %5, %5, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %6, %6, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+"v_fmac_f32_dpp %7, %7, %8 " CTRL " row_mask:0xf bank_mask:0xf\n\t" \
+  : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4]), "+v"(w[5]), "+v"(w[6]), "+v"(w[7]) \
+  : "v"(sigma))
+
+// w[0..7] := H_{8 L} w over L lanes, negated where mx4_negated; a: the lane's octet in
+// its block.
 template <int L>
 __device__ __forceinline__ void mx4_fwht(float* w, int a) {
-  if (L >= 8) {
-    fwht_lanes<8, L>(w, a);
-    return;
-  }
   fwht_regs<8>(w);
   const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;
+  HR_FMAC_DPP8(w, b0, "quad_perm:[1,0,3,2]");
+  HR_FMAC_DPP8(w, b1, "quad_perm:[2,3,0,1]");
+  if (L >= 8) {
+    const float b2 = (a & 4) ? -1.0f : 1.0f;
+    HR_FMAC_DPP8(w, b2, "row_half_mirror");
+  }
+  if (L >= 16) {
+    const float b3 = (a & 8) ? -1.0f : 1.0f;
+    HR_FMAC_DPP8(w, b3, "row_ror:8");
+  }
+  if (L >= 32) {
+    const float b4 = (a & 16) ? -1.0f : 1.0f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = fmaf(dpp<kQuadXor1>(w[e]), b0, w[e]);
-#pragma unroll
-  for (int e = 0; e < 8; ++e) w[e] = fmaf(dpp<kQuadXor2>(w[e]), b1, w[e]);
+    for (int e = 0; e < 8; ++e) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
+      w[e] = fmaf(__uint_as_float(s[1]), b4, __uint_as_float(s[0]));
+    }
+  }
 }
 
 // Largest magnitude of 8 elements; NaN if one is.

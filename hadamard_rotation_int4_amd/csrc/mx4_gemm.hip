@@ -131,10 +131,6 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_gemm_rows_kernel(Mx4GemmArgs p
 template <int V>
 struct MxC { static constexpr int value = V; };
 
-// Workgroup barrier that leaves the caller's own waits as they are (the compiler
-// drains every outstanding memory operation before the barriers that it emits).
-__device__ __forceinline__ void mx_barrier() { asm volatile("s_barrier" ::: "memory"); }
-
 constexpr int kNowhere = 0x40000000;     // past the end of every panel of an operand
 constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 

@@ -68,7 +68,7 @@ __global__ __launch_bounds__(kMx4Threads) void mx4_quant_kernel(Mx4QuantArgs p, 
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[u][e] = flip(w[u][e], sg[e]);
       mx4_fwht<L>(w[u], a);
-      const float f = mx4_factor<L>(a);
+      const float f = mx4_negated<L>(a) ? -mx4_norm<L>() : mx4_norm<L>();
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[u][e] *= f;
     }
@@ -110,7 +110,7 @@ __global__ __launch_bounds__(kMx4Threads) void mx4_dequant_kernel(Mx4DequantArgs
     const int64_t o = first + 64 * u + a;
     if (L) {
       mx4_fwht<L>(w, a);
-      const float g = mx4_factor<L>(a);
+      const float g = mx4_negated<L>(a) ? -mx4_norm<L>() : mx4_norm<L>();
       uint32_t sg[8];
       int64_t row;
       uint32_t col;
