@@ -70,6 +70,7 @@ struct NormArgs {
   int ceil;
   uint8_t* codes;
   uint8_t* scales;
+  float turn;            // set by the launcher: 1 / sqrt(order), 1 without a rotation
 };
 
 hipError_t launch_mx4_quant(const Mx4QuantArgs& a, hipStream_t s);

@@ -72,6 +72,31 @@ __device__ __forceinline__ void mx4_fwht(float* w, int a) {
   }
 }
 
+// The same for an order (32 to 256) known at run time; one of 0 leaves w as it is.
+__device__ __forceinline__ void mx4_fwht_any(float* w, int a, int order) {
+  if (order == 0) return;
+  fwht_regs<8>(w);
+  const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;
+  HR_FMAC_DPP8(w, b0, "quad_perm:[1,0,3,2]");
+  HR_FMAC_DPP8(w, b1, "quad_perm:[2,3,0,1]");
+  if (order >= 64) {
+    const float b2 = (a & 4) ? -1.0f : 1.0f;
+    HR_FMAC_DPP8(w, b2, "row_half_mirror");
+  }
+  if (order >= 128) {
+    const float b3 = (a & 8) ? -1.0f : 1.0f;
+    HR_FMAC_DPP8(w, b3, "row_ror:8");
+  }
+  if (order >= 256) {
+    const float b4 = (a & 16) ? -1.0f : 1.0f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
+      w[e] = fmaf(__uint_as_float(s[1]), b4, __uint_as_float(s[0]));
+    }
+  }
+}
+
 // Largest magnitude of 8 elements; NaN if one is.
 __device__ __forceinline__ float mx4_absmax(const float* w) {
   float m = __builtin_elementwise_maximum(__builtin_elementwise_maximum(fabsf(w[0]), fabsf(w[1])), fabsf(w[2]));

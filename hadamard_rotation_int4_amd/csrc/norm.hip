@@ -17,17 +17,25 @@
 
 namespace hr {
 
+// 16 bytes at any address.
+typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+
 // 8 elements of type DT as they lie in memory.
 template <int DT>
 struct Octet { uint32_t v[DT == kDtF32 ? 8 : 4]; };
 
 // From element `at` of base, which need not be aligned; zeros from the n-th of the
 // row on.
-template <int DT>
+template <int DT, bool NT = false>
 __device__ __forceinline__ void load_octet(const void* base, int64_t at, int col, int n, Octet<DT>& o) {
   if (col + 8 <= n) {
-    struct __attribute__((packed, aligned(DT == kDtF32 ? 4 : 2))) U { Octet<DT> o; };
-    o = reinterpret_cast<const U*>(reinterpret_cast<const char*>(base) + at * (DT == kDtF32 ? 4 : 2))->o;
+    const u32x4_any* q = reinterpret_cast<const u32x4_any*>(reinterpret_cast<const char*>(base) + at * (DT == kDtF32 ? 4 : 2));
+#pragma unroll
+    for (int i = 0; i < (DT == kDtF32 ? 2 : 1); ++i) {
+      const u32x4_any x = NT ? __builtin_nontemporal_load(q + i) : q[i];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o.v[4 * i + e] = x[e];
+    }
     return;
   }
   if (DT == kDtF32) {
@@ -61,29 +69,21 @@ __device__ __forceinline__ void widen(const Octet<DT>& o, float* w) {
   }
 }
 
-template <int DT>
+template <int DT, bool NT>
 __device__ __forceinline__ void store_octet(void* base, int64_t at, int col, int n, const float* w) {
   if (col + 8 <= n) {
-    if (DT == kDtF32) {
-      struct __attribute__((packed, aligned(4))) U { float v[8]; };
-      U u;
+    u32x4_any* q = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(base) + at * (DT == kDtF32 ? 4 : 2));
 #pragma unroll
-      for (int e = 0; e < 8; ++e) u.v[e] = w[e];
-      *reinterpret_cast<U*>(reinterpret_cast<float*>(base) + at) = u;
-    } else {
-      struct __attribute__((packed, aligned(2))) U { uint32_t v[4]; };
-      U u;
+    for (int i = 0; i < (DT == kDtF32 ? 2 : 1); ++i) {
+      u32x4_any x;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (DT == kDtBf16) {
-          const bf16x2 b = {(__bf16)w[2 * i], (__bf16)w[2 * i + 1]};
-          u.v[i] = __builtin_bit_cast(uint32_t, b);
-        } else {
-          const half2v h = {(_Float16)w[2 * i], (_Float16)w[2 * i + 1]};
-          u.v[i] = __builtin_bit_cast(uint32_t, h);
-        }
+      for (int e = 0; e < 4; ++e) {
+        if (DT == kDtF32) x[e] = __float_as_uint(w[4 * i + e]);
+        else if (DT == kDtBf16) x[e] = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)w[2 * e], (__bf16)w[2 * e + 1]});
+        else x[e] = __builtin_bit_cast(uint32_t, (half2v){(_Float16)w[2 * e], (_Float16)w[2 * e + 1]});
       }
-      *reinterpret_cast<U*>(reinterpret_cast<uint16_t*>(base) + at) = u;
+      if (NT) __builtin_nontemporal_store(x, q + i);
+      else q[i] = x;
     }
     return;
   }
@@ -113,9 +113,9 @@ __device__ __forceinline__ float block_sum(float v, float (*red)[WAVES], int slo
   return t;
 }
 
-// XT, DT: types of the stream and of the block and the norm; CH octets a lane;
-// L = 0: no rotation, QUANT: h goes to MXFP4.
-template <int XT, int DT, int WAVES, int CH, bool QUANT, int L>
+// XT, DT: types of the stream and of the block and the norm; CH octets a lane; NT:
+// rows are read and written around the L2s; QUANT: h goes to MXFP4.
+template <int XT, int DT, int WAVES, int CH, bool NT, bool QUANT>
 __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs p) {
   __shared__ float red[4][WAVES];
   // the same labels with and without a rotation, so that sums have one order and
@@ -127,11 +127,11 @@ __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs p) {
 
   // What rows share: the factors of the norm, with the rotation's signs and scale, and
   // of the block's output; kept where there are registers for them.
-  constexpr bool KEEP = CH <= 2;
+  constexpr bool KEEP = WAVES * CH <= 16;
   const bool one_gate = p.gate && p.gate_rows >= p.rows, row_gate = p.gate && !one_gate;
   auto norm_factors = [&](int i, float* w) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) w[e] = L ? mx4_norm<L ? L : 4>() : 1.0f;
+    for (int e = 0; e < 8; ++e) w[e] = QUANT ? p.turn : 1.0f;
     if (p.weight) {
       Octet<kDtF32> o;
       load_octet<kDtF32>(p.weight, col[i], col[i], p.n, o);
@@ -140,7 +140,7 @@ __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs p) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) w[e] *= v[e];
     }
-    if (L) {
+    if (QUANT && p.signs) {
       uint32_t sg[8];
       load_signs<8>(p.signs, col[i] < p.n ? col[i] : 0, sg);
 #pragma unroll
@@ -172,15 +172,15 @@ __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs p) {
       if (p.block) block_factors(i, pw[i]);
     }
   }
-  const uint32_t flips = L && mx4_negated<L ? L : 4>(a) ? 0x88888888u : 0u;
+  const uint32_t flips = QUANT && p.order && (__popc(a & (min(p.order, 128) / 8 - 1)) & 1) ? 0x88888888u : 0u;
 
   Octet<XT> xo[CH];
   Octet<DT> bo[CH], go[CH];
   auto load_row = [&](int64_t row) {
 #pragma unroll
     for (int i = 0; i < CH; ++i) {
-      load_octet<XT>(p.x, row * p.x_stride + col[i], col[i], p.n, xo[i]);
-      if (p.block) load_octet<DT>(p.block, row * p.block_stride + col[i], col[i], p.n, bo[i]);
+      load_octet<XT, NT>(p.x, row * p.x_stride + col[i], col[i], p.n, xo[i]);
+      if (p.block) load_octet<DT, NT>(p.block, row * p.block_stride + col[i], col[i], p.n, bo[i]);
       if (row_gate) load_octet<DT>(p.gate, (int64_t)((uint32_t)row / (uint32_t)p.gate_rows) * p.n + col[i], col[i], p.n, go[i]);
     }
   };
@@ -224,7 +224,7 @@ __global__ __launch_bounds__(64 * WAVES) void norm_kernel(NormArgs p) {
       for (int i = 0; i < CH; ++i) {
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[i][e] = fmaf(u[i][e], f, r[i][e]);
-        store_octet<XT>(p.residual, row * p.residual_stride + col[i], col[i], p.n, r[i]);
+        store_octet<XT, NT>(p.residual, row * p.residual_stride + col[i], col[i], p.n, r[i]);
       }
     }
     if (QUANT || p.h) {
@@ -241,10 +241,10 @@ float* const w = wt[KEEP ? i : 0];
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[i][e] *= f * w[e];
         if (!QUANT) {
-          store_octet<DT>(p.h, row * p.n + col[i], col[i], p.n, r[i]);
+          store_octet<DT, NT>(p.h, row * p.n + col[i], col[i], p.n, r[i]);
           continue;
         }
-        if (L) mx4_fwht<L ? L : 4>(r[i], a);
+        mx4_fwht_any(r[i], a, p.order);
         const uint32_t b = mx4_scale(mx4_absmax(r[i]), p.ceil);
         const uint32_t code = mx4_codes(r[i], b) ^ (b == 255u ? 0u : flips);
         if (col[i] < p.n) {
@@ -258,34 +258,43 @@ float* const w = wt[KEEP ? i : 0];
 }
 
 template <int XT, int DT, int WAVES, int CH>
-static void launch_n4(const NormArgs& a, hipStream_t s) {
+static void launch_rows(const NormArgs& a, hipStream_t s) {
   // 16 waves a compute unit, unless that leaves them uneven numbers of few rows
   const int64_t most = 256 * 16 / WAVES;
   const dim3 grid((unsigned)(a.rows < 4 * most ? a.rows : most)), threads(64 * WAVES);
-  if (!a.codes) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, false, 0>), grid, threads, 0, s, a);
-  else if (a.order == 0) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, 0>), grid, threads, 0, s, a);
-  else if (a.order == 32) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, 4>), grid, threads, 0, s, a);
-  else if (a.order == 64) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, 8>), grid, threads, 0, s, a);
-  else if (a.order == 128) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, 16>), grid, threads, 0, s, a);
-  else hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, 32>), grid, threads, 0, s, a);
+  // large streams: 16384 x 4096 bf16 95 us against 102 without the hint, to MXFP4 78
+  // against 88
+  const bool nt = a.rows * a.n * (XT == kDtF32 ? 4 : 2) >= kStreamBytes;
+  if (a.codes) {
+    if (nt) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, true>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, false, true>), grid, threads, 0, s, a);
+  } else {
+    if (nt) hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, true, false>), grid, threads, 0, s, a);
+    else hipLaunchKernelGGL((norm_kernel<XT, DT, WAVES, CH, false, false>), grid, threads, 0, s, a);
+  }
 }
 
+// The lanes that a row needs, by its length alone: a row's bits do not depend on how
+// many there are.
 template <int XT, int DT>
-static void launch_n2(const NormArgs& a, hipStream_t s) {
-  if (a.n <= 512) launch_n4<XT, DT, 1, 1>(a, s);
-  else if (a.n <= 2048) launch_n4<XT, DT, 4, 1>(a, s);
-  else if (a.n <= 4096) launch_n4<XT, DT, 8, 1>(a, s);
-  else if (a.n <= 8192) launch_n4<XT, DT, 8, 2>(a, s);
-  else if (a.n <= 16384) launch_n4<XT, DT, 16, 2>(a, s);
-  else launch_n4<XT, DT, 16, 4>(a, s);
+static void launch_length(const NormArgs& a, hipStream_t s) {
+  if (a.n <= 512) launch_rows<XT, DT, 1, 1>(a, s);
+  else if (a.n <= 2048) launch_rows<XT, DT, 4, 1>(a, s);
+  else if (a.n <= 4096) launch_rows<XT, DT, 4, 2>(a, s);
+  else if (a.n <= 8192) launch_rows<XT, DT, 8, 2>(a, s);
+  else if (a.n <= 16384) launch_rows<XT, DT, 16, 2>(a, s);
+  else launch_rows<XT, DT, 16, 4>(a, s);
 }
 
-hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
-  if (a.x_dtype == kDtBf16) launch_n2<kDtBf16, kDtBf16>(a, s);
-  else if (a.x_dtype == kDtF16) launch_n2<kDtF16, kDtF16>(a, s);
-  else if (a.dtype == kDtBf16) launch_n2<kDtF32, kDtBf16>(a, s);
-  else if (a.dtype == kDtF16) launch_n2<kDtF32, kDtF16>(a, s);
-  else launch_n2<kDtF32, kDtF32>(a, s);
+hipError_t launch_norm(const NormArgs& args, hipStream_t s) {
+  NormArgs a = args;
+  constexpr float turns[4] = {0.17677669529663687f, 0.125f, 0.08838834764831845f, 0.0625f};
+  a.turn = a.order == 0 ? 1.0f : turns[a.order == 32 ? 0 : a.order == 64 ? 1 : a.order == 128 ? 2 : 3];
+  if (a.x_dtype == kDtBf16) launch_length<kDtBf16, kDtBf16>(a, s);
+  else if (a.x_dtype == kDtF16) launch_length<kDtF16, kDtF16>(a, s);
+  else if (a.dtype == kDtBf16) launch_length<kDtF32, kDtBf16>(a, s);
+  else if (a.dtype == kDtF16) launch_length<kDtF32, kDtF16>(a, s);
+  else launch_length<kDtF32, kDtF32>(a, s);
   return hipGetLastError();
 }
 
