@@ -9,8 +9,7 @@
 // neighbouring lanes (columns), one v_fmac_f32_dpp an element; its signs, as in
 // kv4_device.h, are one for all of a lane's elements.
 //
-// Lane (column c, half h) supplies elements 16 h .. 16 h + 15 of its block: 32
-// contiguous bytes.  The rows of H_32 are given to the instruction in the order in
+// Lane (column c, half h) supplies elements 16 h .. 16 h + 15 of its block.  The rows of H_32 are given to the instruction in the order in
 // which its results come out (v = 0 .. 15 of half h), so that a lane gets back
 // elements 16 h + v: 8 bytes of codes.
 //
@@ -88,56 +87,76 @@ __device__ __forceinline__ void sign_words(const int8_t* signs, int first, uint3
   }
 }
 
-// Where the tiles of a wave lie.  ROWS: rows are whole numbers of tiles, and a wave
-// takes the same columns of R consecutive rows, one set of signs for all; else
-// tiles follow one another over the ends of rows.
+// Where the tiles of a wave lie, in halves of 16 blocks: half g of tile u, of which
+// this lane sees block j = c % 16.  ROWS: rows are whole numbers of tiles, and a wave
+// takes the same columns of R consecutive rows, one set of signs for all; else tiles
+// follow one another over the ends of rows.
 template <int R, bool ROWS>
 struct MxTiles {
-  int64_t block[R];      // flat block of this lane, -1: past the end
-  int64_t row[R];
-  uint32_t col[R];       // first element of the block in its row
-  __device__ __forceinline__ MxTiles(int64_t wave, int c, int64_t rows, uint32_t per, uint32_t magic) {
+  int64_t rows;
+  uint32_t per, magic, group, ct, first, row0, col0, j;
+  __device__ __forceinline__ MxTiles(int64_t wave, int j_, int64_t rows_, uint32_t per_, uint32_t magic_)
+      : rows(rows_), per(per_), magic(magic_), j(j_) {
+    const uint32_t tiles = per / 32;
+    group = ROWS ? (uint32_t)wave / tiles : 0;
+    ct = (uint32_t)wave - group * tiles;
+    first = (uint32_t)wave * 32 * R;
+    row0 = ROWS ? 0 : first / per;
+    col0 = first - row0 * per;
+  }
+  // row, first element in it and flat block; past the end the first row again and
+  // block -1, stored nowhere
+  __device__ __forceinline__ void at(int u, int g, int64_t* row, uint32_t* col, int64_t* block) const {
     if (ROWS) {
-      const uint32_t tiles = per / 32, group = (uint32_t)wave / tiles, ct = (uint32_t)wave - group * tiles;
-#pragma unroll
-      for (int u = 0; u < R; ++u) {
-        row[u] = (int64_t)group * R + u;
-        col[u] = 32 * (32 * ct + c);
-        block[u] = row[u] < rows ? row[u] * per + 32 * ct + c : -1;
-        if (row[u] >= rows) row[u] = 0;
-      }
+      *row = (int64_t)group * R + u;
+      *col = 32 * (32 * ct + 16 * g + j);
+      *block = *row * per + 32 * ct + 16 * g + j;
     } else {
-      const uint32_t first = (uint32_t)wave * 32 * R, row0 = first / per, col0 = first - row0 * per;
-#pragma unroll
-      for (int u = 0; u < R; ++u) {
-        const uint32_t x = col0 + 32 * u + c, q = per == 1 ? x : __umulhi(x, magic);
-        row[u] = (int64_t)row0 + q;
-        col[u] = 32 * (x - q * per);
-        block[u] = row[u] < rows ? (int64_t)first + 32 * u + c : -1;
-        if (row[u] >= rows) {
-          row[u] = 0;
-          col[u] = 0;
-        }
-      }
+      const uint32_t x = col0 + 32 * u + 16 * g + j, q = per == 1 ? x : __umulhi(x, magic);
+      *row = (int64_t)row0 + q;
+      *col = 32 * (x - q * per);
+      *block = (int64_t)first + 32 * u + 16 * g + j;
+    }
+    if (*row >= rows) {
+      *row = 0;
+      *block = -1;
+      if (!ROWS) *col = 0;
     }
   }
 };
 
+// Memory's order and the product's.  Lane (c, h) needs both 16-byte quarters 2 h and
+// 2 h + 1 of its block, but an instruction that takes quarter 2 h of every block
+// would touch half of each line.  Instead instruction g takes the 16 blocks of half
+// g whole, rows of lanes with c < 16 their quarters 2 h, the others 2 h + 1, and an
+// exchange between rows makes the one of the other (its own inverse).
+__device__ __forceinline__ void swap_quarters(u32x4 (&x)[2]) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) {
+    const auto s = __builtin_amdgcn_permlane16_swap(x[0][e], x[1][e], false, false);
+    x[0][e] = s[0];
+    x[1][e] = s[1];
+  }
+}
+
 template <int DT, int S, int R, bool ROWS>
 __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_quant_kernel(Mx4QuantArgs p, int64_t waves, uint32_t magic) {
-  const int lane = threadIdx.x & 63, c = kv4_logical<32>(lane), h = lane >> 5;
+  const int lane = threadIdx.x & 63, c = kv4_logical<32>(lane), h = lane >> 5, g = c >> 4;
   const int64_t wave = (int64_t)blockIdx.x * (kMxRotThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= waves) return;
-  const MxTiles<R, ROWS> at(wave, c, p.rows, p.n / 32, magic);
+  const MxTiles<R, ROWS> tiles(wave, c & 15, p.rows, p.n / 32, magic);
   u32x4 x[R][2];
 #pragma unroll
-  for (int u = 0; u < R; ++u) {
-    // past the end: the first row again, stored nowhere
-    const u32x4* src = reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p.x) + at.row[u] * p.x_stride +
-                                                      at.col[u] + 16 * h);
+  for (int u = 0; u < R; ++u)
 #pragma unroll
-    for (int k = 0; k < 2; ++k) x[u][k] = p.stream ? __builtin_nontemporal_load(src + k) : src[k];
-  }
+    for (int k = 0; k < 2; ++k) {
+      int64_t row, block;
+      uint32_t col;
+      tiles.at(u, k, &row, &col, &block);
+      const u32x4* src =
+          reinterpret_cast<const u32x4*>(reinterpret_cast<const uint16_t*>(p.x) + row * p.x_stride + col + 8 * (2 * h + g));
+      x[u][k] = p.stream ? __builtin_nontemporal_load(src) : *src;
+    }
   u32x4 hf[2];
   hadamard_operand<DT>(lane, hf);
   constexpr float NORM = mx4_norm<4 << S>();
@@ -146,7 +165,13 @@ __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_quant_kernel(Mx4Q
   f32x16 d[R];
 #pragma unroll
   for (int u = 0; u < R; ++u) {
-    if (u == 0 || !ROWS) sign_words(p.signs, at.col[u] + 16 * h, 0u, m);
+    if (u == 0 || !ROWS) {
+      int64_t row, block;
+      uint32_t col;
+      tiles.at(u, g, &row, &col, &block);
+      sign_words(p.signs, col + 16 * h, 0u, m);
+    }
+    swap_quarters(x[u]);
 #pragma unroll
     for (int k = 0; k < 2; ++k)
 #pragma unroll
@@ -163,25 +188,31 @@ __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_quant_kernel(Mx4Q
     const auto sw = __builtin_amdgcn_permlane32_swap(__float_as_uint(a), __float_as_uint(a), false, false);
     const uint32_t b = mx4_scale_byte(sw[0] > sw[1] ? sw[0] : sw[1], p.ceil);
     const uint2 code = make_uint2(mx4_codes(w, b), mx4_codes(w + 8, b));
-    if (at.block[u] >= 0) {
+    int64_t row, block;
+    uint32_t col;
+    tiles.at(u, g, &row, &col, &block);
+    if (block >= 0) {
       const uint32_t f = b == 255u ? 0u : flips;
-      *reinterpret_cast<uint2*>(p.codes + at.block[u] * 16 + 8 * h) = make_uint2(code.x ^ f, code.y ^ f);
-      if (h == 0) p.scales[at.block[u]] = (uint8_t)b;
+      *reinterpret_cast<uint2*>(p.codes + block * 16 + 8 * h) = make_uint2(code.x ^ f, code.y ^ f);
+      if (h == 0) p.scales[block] = (uint8_t)b;
     }
   }
 }
 
 template <int DT, int S, int R, bool ROWS>
 __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_back_kernel(Mx4DequantArgs p, int64_t waves, uint32_t magic) {
-  const int lane = threadIdx.x & 63, c = kv4_logical<32>(lane), h = lane >> 5;
+  const int lane = threadIdx.x & 63, c = kv4_logical<32>(lane), h = lane >> 5, g = c >> 4;
   const int64_t wave = (int64_t)blockIdx.x * (kMxRotThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   if (wave >= waves) return;
-  const MxTiles<R, ROWS> at(wave, c, p.rows, p.n / 32, magic);
+  const MxTiles<R, ROWS> tiles(wave, c & 15, p.rows, p.n / 32, magic);
   uint2 code[R];
   uint32_t b[R];
 #pragma unroll
   for (int u = 0; u < R; ++u) {
-    const int64_t f = at.block[u] < 0 ? 0 : at.block[u];
+    int64_t row, block;
+    uint32_t col;
+    tiles.at(u, g, &row, &col, &block);
+    const int64_t f = block < 0 ? 0 : block;
     code[u] = *reinterpret_cast<const uint2*>(p.codes + f * 16 + 8 * h);
     b[u] = p.scales[f];
   }
@@ -205,7 +236,12 @@ __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_back_kernel(Mx4De
 #pragma unroll
     for (int v = 0; v < 16; ++v) w[v] = d[u][v] * f;
     across<S>(w, c);
-    if (u == 0 || !ROWS) sign_words(p.signs, at.col[u] + 16 * h, flips, m);
+    if (u == 0 || !ROWS) {
+      int64_t row, block;
+      uint32_t col;
+      tiles.at(u, g, &row, &col, &block);
+      sign_words(p.signs, col + 16 * h, flips, m);
+    }
     u32x4 y[2];
 #pragma unroll
     for (int k = 0; k < 2; ++k)
@@ -216,13 +252,16 @@ __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_back_kernel(Mx4De
         else y[k][e] = __builtin_bit_cast(uint32_t, (half2v){(_Float16)lo, (_Float16)hi});
         y[k][e] ^= m[4 * k + e];
       }
-    if (at.block[u] >= 0) {
-      u32x4* dst = reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + at.block[u] * 32 + 16 * h);
+    swap_quarters(y);
 #pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (p.stream) __builtin_nontemporal_store(y[k], dst + k);
-        else dst[k] = y[k];
-      }
+    for (int k = 0; k < 2; ++k) {
+      int64_t row, block;
+      uint32_t col;
+      tiles.at(u, k, &row, &col, &block);
+      if (block < 0) continue;
+      u32x4* dst = reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(p.y) + block * 32 + 8 * (2 * h + g));
+      if (p.stream) __builtin_nontemporal_store(y[k], dst);
+      else *dst = y[k];
     }
   }
 }

@@ -96,13 +96,24 @@ __device__ __forceinline__ void store_octet(void* base, int64_t at, int col, int
     }
 }
 
+// Sum over the wave, the same in every lane: partners add the same two numbers.
+__device__ __forceinline__ float wave_sum(float v) {
+  v += dpp<kQuadXor1>(v);
+  v += dpp<kQuadXor2>(v);
+  v += dpp<kRowHalfMirror>(v);
+  v += dpp<kRowMirror>(v);
+  const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+  const auto t = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(t[0]) + __uint_as_float(t[1]);
+}
+
 // Sum over the workgroup, the same in every thread.  Its own barrier waits for LDS
 // alone and leaves loads in flight; no two sums that no other lies between may share
 // a slot.
 template <int WAVES>
 __device__ __forceinline__ float block_sum(float v, float (*red)[WAVES], int slot) {
-#pragma unroll
-  for (int o = 32; o >= 1; o >>= 1) v += __shfl_xor(v, o, 64);
+  v = wave_sum(v);
   if (WAVES == 1) return v;
   if ((threadIdx.x & 63) == 0) red[slot][threadIdx.x >> 6] = v;
   __builtin_amdgcn_s_waitcnt(0xC07F);              // lgkmcnt(0)
