@@ -266,35 +266,43 @@ __global__ __launch_bounds__(kMxRotThreads, 2) void mx4_rotate_back_kernel(Mx4De
   }
 }
 
-// Tiles of a wave: several when that still leaves waves for every compute unit.
-constexpr int kMxManyTiles = 4 * 4096;
+// Tiles of a wave on the way back: two when there are waves enough for every compute
+// unit (65536 x 2048, order 128: 60 us, with one 66, with four 65).  On the way there one
+// is best (57, 60, 62).
+constexpr int64_t kMxManyTiles = 4 * 4096;
 
-template <template <int, int, int, bool> class K, int DT, int S, typename Args>
+template <template <int, int, int, bool> class K, int DT, int S, int MANY, typename Args>
 static void launch_rotate(const Args& a, hipStream_t s) {
   const uint32_t per = a.n / 32;
   const int64_t tiles = (a.rows * per + 31) / 32;
   const uint32_t magic = (uint32_t)(((uint64_t)1 << 32) / per + 1);
-  const bool rows = per % 32 == 0;
   auto go = [&](auto kernel, int64_t waves) {
     hipLaunchKernelGGL(kernel, dim3((unsigned)((waves + kMxRotThreads / 64 - 1) / (kMxRotThreads / 64))), dim3(kMxRotThreads),
                        0, s, a, waves, magic);
   };
-  if (rows && tiles >= kMxManyTiles) go(K<DT, S, 4, true>::kernel, (a.rows + 3) / 4 * (per / 32));
-  else go(K<DT, S, 1, false>::kernel, tiles);
+  if (per % 32) go(K<DT, S, 1, false>::kernel, tiles);
+  else if (MANY == 1 || tiles < kMxManyTiles) go(K<DT, S, 1, true>::kernel, tiles);
+  else go(K<DT, S, MANY, true>::kernel, (a.rows + MANY - 1) / MANY * (per / 32));
 }
 
 template <int DT, int S, int R, bool ROWS>
-struct MxTo { static constexpr auto kernel = mx4_rotate_quant_kernel<DT, S, R, ROWS>; };
+struct MxTo {
+  static constexpr int many = 1;
+  static constexpr auto kernel = mx4_rotate_quant_kernel<DT, S, R, ROWS>;
+};
 template <int DT, int S, int R, bool ROWS>
-struct MxBack { static constexpr auto kernel = mx4_rotate_back_kernel<DT, S, R, ROWS>; };
+struct MxBack {
+  static constexpr int many = 2;
+  static constexpr auto kernel = mx4_rotate_back_kernel<DT, S, R, ROWS>;
+};
 
 template <template <int, int, int, bool> class K, int DT, typename Args>
 static void launch_order(const Args& a, hipStream_t s) {
   switch (a.order) {
-    case 32: launch_rotate<K, DT, 0>(a, s); break;
-    case 64: launch_rotate<K, DT, 1>(a, s); break;
-    case 128: launch_rotate<K, DT, 2>(a, s); break;
-    default: launch_rotate<K, DT, 3>(a, s); break;
+    case 32: launch_rotate<K, DT, 0, K<DT, 0, 1, true>::many>(a, s); break;
+    case 64: launch_rotate<K, DT, 1, K<DT, 0, 1, true>::many>(a, s); break;
+    case 128: launch_rotate<K, DT, 2, K<DT, 0, 1, true>::many>(a, s); break;
+    default: launch_rotate<K, DT, 3, K<DT, 0, 1, true>::many>(a, s); break;
   }
 }
 
