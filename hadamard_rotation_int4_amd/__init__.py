@@ -892,18 +892,26 @@ def kv4_attention(cache: KV4Cache, q: torch.Tensor, table: torch.Tensor, lens: t
 
 _MX_RULES = {"floor": 0, "ceil": 1}
 _MX_ORDERS = (32, 64, 128, 256)
+_U8, _F32 = torch.uint8, torch.float32
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
 
 
-def _call(index: int, fn: str, *args) -> None:
+def _launch(index: int, fn, *args) -> None:
     """A C call on the current stream of device `index`, made while that is the current device."""
-    if _get_device is not None and _get_device() == index:
-        st = getattr(lib, fn)(*args, _raw_stream(index) if _raw_stream is not None else _stream(index))
+    if _raw_stream is not None and _get_device is not None and _get_device() == index:
+        st = fn(*args, _raw_stream(index))
     else:
         with torch.cuda.device(index):
-            st = getattr(lib, fn)(*args, _stream(index))
+            st = fn(*args, _stream(index))
     if st:
-        raise HRError(st, fn)
+        raise HRError(st, fn.__name__)
+
+
+def _device_of(t, name: str) -> int:
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"{name}: tensor must live on the GPU")
+    return index
 
 
 def _ptr(index: int, t, name: str) -> int:
@@ -926,22 +934,26 @@ def _strided(t, name: str, dtypes):
     if len(shape) != 2:
         raise ValueError(f"{name}: expected a 2-D [rows][n] tensor, got shape {tuple(shape)}")
     rows, n = shape
+    if t.is_contiguous():
+        return rows, n, n, dtype
     step, last = t.stride()
-    if (last != 1 and n > 1 and rows) or (rows > 1 and step < n):
+    if (last != 1 and n > 1) or (rows > 1 and step < n):
         raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
     return rows, n, step if rows > 1 else n, dtype
 
 
-def _mx_sizes(n: int, order: int, signs) -> None:
+def _mx_order(order, n: int, signs) -> int:
     if n <= 0 or n % 32:
         raise ValueError(f"rows of {n} elements are not whole blocks of 32")
-    if order:
-        if order not in _MX_ORDERS or n % order:
-            raise ValueError(f"order={order} not in {_MX_ORDERS} or not dividing the row length {n}")
+    if not order:
         if signs is not None:
-            _kv4_index(signs, "signs", torch.int8, (n,))
-    elif signs is not None:
-        raise ValueError("signs go with an order")
+            raise ValueError("signs go with an order")
+        return 0
+    if order not in _MX_ORDERS or n % order:
+        raise ValueError(f"order={order} not in {_MX_ORDERS} or not dividing the row length {n}")
+    if signs is not None:
+        _kv4_index(signs, "signs", torch.int8, (n,))
+    return order
 
 
 def _mx_rule(rule) -> int:
@@ -950,31 +962,49 @@ def _mx_rule(rule) -> int:
     return _MX_RULES[rule]
 
 
-def _mx_outputs(rows: int, n: int, codes, scales, device):
+def _mx_pair(codes, scales, name: str = ""):
+    """Check codes uint8 [rows][n/2] and their scales uint8 [rows][n/32]; returns
+    (rows, n/2).  One comparison where all is well: a step of few tokens costs what
+    these calls cost the host."""
+    try:
+        rows, half = codes.shape
+        fine = (codes.dtype is _U8 and scales.dtype is _U8 and half > 0 and not half & 15
+                and scales.shape == (rows, half >> 4) and codes.is_contiguous() and scales.is_contiguous())
+    except (AttributeError, ValueError):
+        fine = False
+    if not fine:
+        _kv4_index(codes, name + "codes", _U8, _ANY_2D)
+        rows, half = codes.shape
+        if half == 0 or half % 16:
+            raise ValueError(f"{name}codes: rows of {2 * half} codes are not whole blocks of 32")
+        _kv4_index(scales, name + "scales", _U8, (rows, half // 16))
+    return rows, half
+
+
+def _mx_outputs(x, rows: int, n: int, codes, scales):
     if codes is None:
-        codes = torch.empty((rows, n // 2), dtype=torch.uint8, device=device)
+        codes = x.new_empty((rows, n >> 1), dtype=_U8)
     else:
-        _kv4_index(codes, "codes", torch.uint8, (rows, n // 2))
+        _kv4_index(codes, "codes", _U8, (rows, n // 2))
     if scales is None:
-        scales = torch.empty((rows, n // 32), dtype=torch.uint8, device=device)
+        scales = x.new_empty((rows, n >> 5), dtype=_U8)
     else:
-        _kv4_index(scales, "scales", torch.uint8, (rows, n // 32))
+        _kv4_index(scales, "scales", _U8, (rows, n // 32))
     return codes, scales
 
 
-def _mx_quant(fn, x, order, signs, rule, codes, scales):
+def _mx_quant(x, order, signs, rule, codes, scales):
     rows, n, step, dtype = _strided(x, "x", _KV4_TYPES)
-    _mx_sizes(n, order, signs)
+    order = _mx_order(order, n, signs)
     rule = _mx_rule(rule)
-    index = x.get_device()
-    px = _ptr(index, x, "x") if index >= 0 else _ptr(0, x, "x")
-    codes, scales = _mx_outputs(rows, n, codes, scales, x.device)
-    pc, ps = _ptr(index, codes, "codes"), _ptr(index, scales, "scales")
+    index = _device_of(x, "x")
+    codes, scales = _mx_outputs(x, rows, n, codes, scales)
+    out = _ptr(index, codes, "codes"), _ptr(index, scales, "scales")
     if order:
-        _call(index, fn, px, _KV4_TYPES[dtype], step, rows, n, order, None if signs is None else _ptr(index, signs, "signs"),
-              rule, pc, ps)
+        _launch(index, lib.hr_rotate_quant_mxfp4, x.data_ptr(), _KV4_TYPES[dtype], step, rows, n, order,
+                None if signs is None else _ptr(index, signs, "signs"), rule, *out)
     else:
-        _call(index, fn, px, _KV4_TYPES[dtype], step, rows, n, rule, pc, ps)
+        _launch(index, lib.hr_quant_mxfp4, x.data_ptr(), _KV4_TYPES[dtype], step, rows, n, rule, *out)
     return codes, scales
 
 
@@ -984,7 +1014,7 @@ def quant_mxfp4(x: torch.Tensor, rule: str = "floor", codes: torch.Tensor | None
     fp32, n a multiple of 32, rows may be strided (a multiple of 16 bytes);
     rule: "floor" (the format's, saturating) or "ceil" (nothing saturates).
     Returns (codes uint8 [rows][n/2], scales uint8 [rows][n/32])."""
-    return _mx_quant("hr_quant_mxfp4", x, 0, None, rule, codes, scales)
+    return _mx_quant(x, 0, None, rule, codes, scales)
 
 
 def rotate_quant_mxfp4(x: torch.Tensor, order: int = 128, signs: torch.Tensor | None = None, rule: str = "floor",
@@ -994,7 +1024,7 @@ def rotate_quant_mxfp4(x: torch.Tensor, order: int = 128, signs: torch.Tensor | 
     signs: int8 [n] of +-1, or None."""
     if order not in _MX_ORDERS:
         raise ValueError(f"order={order} not in {_MX_ORDERS}")
-    return _mx_quant("hr_rotate_quant_mxfp4", x, order, signs, rule, codes, scales)
+    return _mx_quant(x, order, signs, rule, codes, scales)
 
 
 def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, order: int | None = None,
@@ -1003,22 +1033,18 @@ def dequant_mxfp4(codes: torch.Tensor, scales: torch.Tensor, order: int | None =
     """The rows that MXFP4 codes uint8 [rows][n/2] and scales uint8 [rows][n/32]
     stand for, rotated back if an order (and its signs) is given
     (hr_dequant_mxfp4): [rows][n] of dtype."""
-    _kv4_index(codes, "codes", torch.uint8, _ANY_2D)
-    rows, half = codes.shape
-    n, order = 2 * half, order or 0
-    _mx_sizes(n, order, signs)
-    _kv4_index(scales, "scales", torch.uint8, (rows, n // 32))
+    rows, half = _mx_pair(codes, scales)
+    n = 2 * half
+    order = _mx_order(order, n, signs)
     if dtype not in _KV4_TYPES:
         raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
-    index = codes.get_device()
-    pc = _ptr(max(index, 0), codes, "codes")
-    ps = _ptr(index, scales, "scales")
+    index = _device_of(codes, "codes")
     if out is None:
-        out = torch.empty((rows, n), dtype=dtype, device=codes.device)
+        out = codes.new_empty((rows, n), dtype=dtype)
     else:
         _kv4_index(out, "out", dtype, (rows, n))
-    _call(index, "hr_dequant_mxfp4", pc, ps, rows, n, order, None if signs is None else _ptr(index, signs, "signs"),
-          _KV4_TYPES[dtype], _ptr(index, out, "out"))
+    _launch(index, lib.hr_dequant_mxfp4, codes.data_ptr(), _ptr(index, scales, "scales"), rows, n, order,
+            None if signs is None else _ptr(index, signs, "signs"), _KV4_TYPES[dtype], _ptr(index, out, "out"))
     return out
 
 
@@ -1027,33 +1053,27 @@ def mxfp4_gemm(a_codes: torch.Tensor, a_scales: torch.Tensor, w_codes: torch.Ten
     """C = A W^T of MXFP4 operands (hr_mxfp4_gemm): a_codes uint8 [M][K/2],
     a_scales uint8 [M][K/32], w_codes [N][K/2], w_scales [N][K/32]; any M and N,
     K a multiple of 32.  fp32 sums, C [M][N] of dtype (bf16, fp16 or fp32)."""
-    _kv4_index(a_codes, "a_codes", torch.uint8, _ANY_2D)
-    _kv4_index(w_codes, "w_codes", torch.uint8, _ANY_2D)
-    M, half = a_codes.shape
-    N = w_codes.shape[0]
-    if half == 0 or half % 16:
-        raise ValueError(f"a_codes: rows of {2 * half} codes are not whole blocks of 32")
-    if w_codes.shape[1] != half:
-        raise ValueError(f"w_codes: rows of {2 * w_codes.shape[1]} codes, but a_codes has {2 * half}")
-    _kv4_index(a_scales, "a_scales", torch.uint8, (M, half // 16))
-    _kv4_index(w_scales, "w_scales", torch.uint8, (N, half // 16))
+    M, half = _mx_pair(a_codes, a_scales, "a_")
+    N, w_half = _mx_pair(w_codes, w_scales, "w_")
+    if w_half != half:
+        raise ValueError(f"w_codes: rows of {2 * w_half} codes, but a_codes has {2 * half}")
     if dtype not in _KV4_TYPES:
         raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
-    index = a_codes.get_device()
-    pa = _ptr(max(index, 0), a_codes, "a_codes")
-    pw, psa, psw = _ptr(index, w_codes, "w_codes"), _ptr(index, a_scales, "a_scales"), _ptr(index, w_scales, "w_scales")
+    index = _device_of(a_codes, "a_codes")
     if out is None:
-        out = torch.empty((M, N), dtype=dtype, device=a_codes.device)
+        out = a_codes.new_empty((M, N), dtype=dtype)
     else:
         _kv4_index(out, "out", dtype, (M, N))
-    _call(index, "hr_mxfp4_gemm", pa, psa, pw, psw, M, N, 2 * half, _KV4_TYPES[dtype], _ptr(index, out, "out"))
+    _launch(index, lib.hr_mxfp4_gemm, a_codes.data_ptr(), _ptr(index, a_scales, "a_scales"),
+            _ptr(index, w_codes, "w_codes"), _ptr(index, w_scales, "w_scales"), M, N, 2 * half, _KV4_TYPES[dtype],
+            _ptr(index, out, "out"))
     return out
 
 
 def _norm_weight(t, name: str, n: int, index: int):
     if t is None:
         return None
-    _kv4_index(t, name, torch.float32, (n,))
+    _kv4_index(t, name, _F32, (n,))
     return _ptr(index, t, name)
 
 
@@ -1067,10 +1087,8 @@ def _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, dtype,
         dtype = xt if block_out is None else getattr(block_out, "dtype", None)
     if dtype not in _KV4_TYPES:
         raise TypeError(f"dtype {dtype} not in {[_DT_NAME[d] for d in _KV4_TYPES]}")
-    if xt is not torch.float32 and dtype is not xt:
+    if xt is not _F32 and dtype is not xt:
         raise TypeError(f"dtype {dtype}: must be x's ({xt}) unless that is float32")
-    index = x.get_device()
-    px = _ptr(max(index, 0), x, "x")
     po = pg = pr = None
     bstep = rstep = n
     gates = 1
@@ -1078,7 +1096,6 @@ def _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, dtype,
         brows, bn, bstep, _ = _strided(block_out, "block_out", (dtype,))
         if brows != rows or bn != n:
             raise ValueError(f"block_out: shape {tuple(block_out.shape)}, expected {(rows, n)}")
-        po = _ptr(index, block_out, "block_out")
         if post_weight is not None and not post_norm:
             raise ValueError("post_weight goes with post_norm")
         if gate is not None:
@@ -1086,19 +1103,26 @@ def _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, dtype,
             gates = gate.shape[0]
             if gates < 1 or rows % gates:
                 raise ValueError(f"gate: {gates} rows do not divide the {rows} of x")
+        index = _device_of(x, "x")
+        po = _ptr(index, block_out, "block_out")
+        if gate is not None:
             pg = _ptr(index, gate, "gate")
         if residual is None:
-            residual = torch.empty((rows, n), dtype=xt, device=x.device)
-        else:
+            residual = torch.empty_like(x) if step == n else x.new_empty((rows, n))
+        elif residual is not x:
             rrows, rn, rstep, _ = _strided(residual, "residual", (xt,))
             if rrows != rows or rn != n:
                 raise ValueError(f"residual: shape {tuple(residual.shape)}, expected {(rows, n)}")
+        else:
+            rstep = step
         pr = _ptr(index, residual, "residual")
     elif post_norm or post_weight is not None or gate is not None or residual is not None:
         raise ValueError("post_norm, post_weight, gate and residual go with block_out")
     elif alone:
         raise ValueError("neither block_out nor h: nothing to compute")
-    p = _NormStruct(px, po, _norm_weight(post_weight, "post_weight", n, index), pg,
+    else:
+        index = _device_of(x, "x")
+    p = _NormStruct(x.data_ptr(), po, _norm_weight(post_weight, "post_weight", n, index), pg,
                     _norm_weight(weight, "weight", n, index), rows, step, bstep, gates, n, _KV4_TYPES[xt],
                     _KV4_TYPES[dtype], 1 if post_norm else 0, scale, eps)
     return p, index, x if block_out is None else residual, pr, rstep, rows, n, dtype
@@ -1122,13 +1146,13 @@ def norm_residual(x: torch.Tensor, block_out: torch.Tensor | None = None, weight
     if not want_h:
         if out is not None:
             raise ValueError("out goes with want_h")
-        _call(index, "hr_norm_residual", ctypes.addressof(p), pr, rstep, None)
+        _launch(index, lib.hr_norm_residual, ctypes.addressof(p), pr, rstep, None)
         return res, None
     if out is None:
-        out = torch.empty((rows, n), dtype=dtype, device=x.device)
+        out = x.new_empty((rows, n), dtype=dtype)
     else:
         _kv4_index(out, "out", dtype, (rows, n))
-    _call(index, "hr_norm_residual", ctypes.addressof(p), pr, rstep, _ptr(index, out, "out"))
+    _launch(index, lib.hr_norm_residual, ctypes.addressof(p), pr, rstep, _ptr(index, out, "out"))
     return res, out
 
 
@@ -1144,11 +1168,10 @@ def norm_residual_quant_mxfp4(x: torch.Tensor, block_out: torch.Tensor | None = 
     Returns (r, codes uint8 [rows][n/2], scales uint8 [rows][n/32])."""
     p, index, res, pr, rstep, rows, n, _ = _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, None,
                                                  residual, False)
-    order = order or 0
-    _mx_sizes(n, order, signs)
+    order = _mx_order(order, n, signs)
     rule = _mx_rule(rule)
-    codes, scales = _mx_outputs(rows, n, codes, scales, x.device)
-    _call(index, "hr_norm_residual_quant_mxfp4", ctypes.addressof(p), pr, rstep, order,
-          None if signs is None else _ptr(index, signs, "signs"), rule, _ptr(index, codes, "codes"),
-          _ptr(index, scales, "scales"))
+    codes, scales = _mx_outputs(x, rows, n, codes, scales)
+    _launch(index, lib.hr_norm_residual_quant_mxfp4, ctypes.addressof(p), pr, rstep, order,
+            None if signs is None else _ptr(index, signs, "signs"), rule, _ptr(index, codes, "codes"),
+            _ptr(index, scales, "scales"))
     return res, codes, scales
