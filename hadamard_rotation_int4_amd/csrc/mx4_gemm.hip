@@ -15,6 +15,7 @@ namespace hr {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
 
 constexpr int kFp4 = 4;      // format code of the instruction's operands
 
@@ -146,20 +147,27 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // once, lie in 8 different places.  The copy writes LDS in lane order, so it is
 // the source chunk of a lane that is permuted, within the row's 128 bytes.
 //
-// SL: scales come through LDS too, 16 bytes of each row every second stage (for K
-// a multiple of 128: whole words); else each lane loads its own words.
+// SM, how a lane gets its scales.  kCopied: copied into LDS, 16 bytes of each row
+// every second stage, for K a multiple of 128 (whole words).  kBrought: the same
+// through registers, at any alignment, for K of at least 512.  kOwn: each lane loads
+// its own words.
 //
 // KG: teams of WM WN waves that take pairs of stages in turn, each with buffers of
 // its own; their sums are joined in LDS, in the teams' order.  A stage of a small
 // tile takes as long as its loads do, and KG teams have KG times as many under way.
-template <int WM, int WN, int TM, int TN, int KG, bool SL, int OCC>
+enum { kOwn, kCopied, kBrought };
+
+template <int WM, int WN, int TM, int TN, int KG, int SM, int OCC>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
   constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
   constexpr int ROWB = 128;                        // bytes of a row and stage
   constexpr int QA = BM / 8, QW = BN / 8;          // copies of 1 KB of a stage
   constexpr int DPW = (QA + QW) / WAVES;
-  constexpr int SA = (BM + 63) / 64, QS = SA + (BN + 63) / 64;   // copies of 64 rows' scales of two stages
-  constexpr int SCB = SL ? QS * 1024 : 16, SPW = (QS + WAVES - 1) / WAVES;
+  constexpr bool SL = SM != kOwn;                  // through LDS
+  constexpr int SA = (BM + 63) / 64, QS = SA + (BN + 63) / 64;     // copies of 64 rows' scales of two stages
+  constexpr int SCB = SM == kCopied ? QS * 1024 : SL ? (BM + BN) * 16 : 16;      // bytes of them
+  constexpr int SPW = (QS + WAVES - 1) / WAVES;    // copies of a wave
+  constexpr int SPT = (BM + BN + 64 * WAVES - 1) / (64 * WAVES);   // rows of scales of a thread
   constexpr int BUF = (BM + BN) * ROWB;
   static_assert((QA + QW) % WAVES == 0, "equal copies a wave");
   __shared__ __attribute__((aligned(16))) char sbuf0[KG * BUF];
@@ -217,28 +225,72 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   // Scales: the 4-byte word of blocks 8 s + 4 h .. + 3 of each of this lane's rows.
   // Past the end of a row words are zero.  A zero byte is 2^-127, and in both
   // operands its products are below 2^-240 and count as 0 whatever the codes are.
+  struct __attribute__((packed, aligned(1))) Word { uint32_t v; };
+  struct __attribute__((packed, aligned(1))) Run { uint32_t v[4]; };
   const uint8_t* const sa = p.sa + m0 * blocks;
   const uint8_t* const sw = p.sw + n0 * blocks;
   uint32_t sc[T], sn[T], srow[T];
-  const __amdgpu_buffer_rsrc_t rsa = __builtin_amdgcn_make_buffer_rsrc((void*)sa, 0, rows_a * blocks, 0x00020000);
-  const __amdgpu_buffer_rsrc_t rsw = __builtin_amdgcn_make_buffer_rsrc((void*)sw, 0, rows_w * blocks, 0x00020000);
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const int r = i < TM ? wm + 32 * i + l32 : wn + 32 * (i - TM) + l32;
-    if (SL) srow[i] = (uint32_t)(i < TM ? r : 64 * SA + r) * 16 + 4 * h + team * 2 * SCB;
+    if (SL) srow[i] = (uint32_t)(i < TM ? r : (SM == kCopied ? 64 * SA : BM) + r) * 16 + 4 * h + team * 2 * SCB;
     else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
   }
-  auto copy_scales = [&](int i) {                   // of the team's stages 2 i and 2 i + 1
-    const int t = KG * i + team;
-    const int v = 2 * t < stages ? lane * blocks : kNowhere;
+  // kCopied: of the team's stages 2 i and 2 i + 1; nothing is read behind the end of the
+  // operand, what is read of the next row behind the end of a row is not used
+  auto copy_scales = [&](int i) {
+    const int q = KG * i + team;
+    const int v = 2 * q < stages ? lane * blocks : kNowhere;
 #pragma unroll
     for (int j = 0; j < SPW; ++j) {
-      const int q = wave * SPW + j;
-      const bool a = q < SA;
-      if (QS % WAVES == 0 || q < QS)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? rsa : rsw,
-                                                 (__attribute__((address_space(3))) void*)(sscale + (2 * team + (i & 1)) * SCB + 1024 * q),
-                                                 16, v, 64 * (a ? q : q - SA) * blocks + 16 * t, 0, 0);
+      const int c = wave * SPW + j;
+      const bool a = c < SA;
+      const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(a ? sa : sw), 0, (a ? rows_a : rows_w) * blocks, 0x00020000);
+      if (QS % WAVES == 0 || c < QS)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs,
+                                                 (__attribute__((address_space(3))) void*)(sscale + (2 * team + (i & 1)) * SCB + 1024 * c),
+                                                 16, v, 64 * (a ? c : c - SA) * blocks + 16 * q, 0, 0);
+    }
+  };
+  // kBrought: a thread brings 16 bytes of its rows, of the team's stages 2 i and 2 i +
+  // 1; the last ones, which may be fewer, are made once.
+  const uint8_t* run_row[SPT];
+  uint32_t run_at[SPT];
+  v4u run[SPT], run_last[SPT];
+  const int runs = (blocks + 15) / 16;
+  if constexpr (SM == kBrought) {
+#pragma unroll
+    for (int t = 0; t < SPT; ++t) {
+      const int r = min((int)threadIdx.x - team * 64 * WAVES + t * 64 * WAVES, BM + BN - 1);     // the last again
+      run_row[t] = r < BM ? sa + (int64_t)min(r, rows_a - 1) * blocks : sw + (int64_t)min(r - BM, rows_w - 1) * blocks;
+      run_at[t] = (uint32_t)r * 16 + team * 2 * SCB;
+      // the last 16 of the row, shifted down to where the last run begins
+      const int down = 16 * runs - blocks;
+      const Run x = *reinterpret_cast<const Run*>(run_row[t] + blocks - 16);
+      const uint64_t lo = x.v[0] | (uint64_t)x.v[1] << 32, hi = x.v[2] | (uint64_t)x.v[3] << 32;
+      const int b = 8 * (down & 7);
+      const uint64_t s0 = b ? lo >> b | hi << (64 - b) : lo, s1 = hi >> b;
+      const uint64_t y0 = down >= 8 ? s1 : s0, y1 = down >= 8 ? 0 : s1;
+      run_last[t] = (v4u){(uint32_t)y0, (uint32_t)(y0 >> 32), (uint32_t)y1, (uint32_t)(y1 >> 32)};
+    }
+  }
+  auto bring_scales = [&](int i) {
+    const int q = KG * i + team;
+#pragma unroll
+    for (int t = 0; t < SPT; ++t) {
+      const Run x = *reinterpret_cast<const Run*>(run_row[t] + 16 * min(q, blocks / 16 - 1));
+      run[t] = (v4u){x.v[0], x.v[1], x.v[2], x.v[3]};
+    }
+  };
+  auto put_scales = [&](int i) {
+    const int q = KG * i + team;
+#pragma unroll
+    for (int t = 0; t < SPT; ++t) {
+      v4u x;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[e] = q < runs - 1 ? run[t][e] : q < runs ? run_last[t][e] : 0u;
+      *reinterpret_cast<v4u*>(sscale + (i & 1) * SCB + run_at[t]) = x;
     }
   };
   auto load_scales = [&](int k, uint32_t* v) {      // of the team's stage k
@@ -248,15 +300,14 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
         v[i] = *reinterpret_cast<const uint32_t*>(sscale + ((k >> 1) & 1) * SCB + (k & 1) * 8 + srow[i]);
     } else {
       // past the end of a row its last word, shifted by use_scales
-      struct __attribute__((packed, aligned(1))) U { uint32_t v; };
       const uint32_t from = min(8 * place(k) + 4 * h, blocks - 4);
 #pragma unroll
-      for (int i = 0; i < T; ++i) v[i] = reinterpret_cast<const U*>((i < TM ? sa : sw) + (srow[i] + from))->v;
+      for (int i = 0; i < T; ++i) v[i] = reinterpret_cast<const Word*>((i < TM ? sa : sw) + (srow[i] + from))->v;
     }
   };
   auto use_scales = [&](int k, const uint32_t* v) {
     if constexpr (SL) {
-      const bool past = 8 * place(k) + 4 * h >= blocks;
+      const bool past = SM == kCopied && 8 * place(k) + 4 * h >= blocks;
 #pragma unroll
       for (int i = 0; i < T; ++i) sc[i] = past ? 0u : v[i];
     } else {
@@ -320,16 +371,28 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     mx_barrier();
     if (SL) load_scales(k + 1, sn);
     read(MxC<1 - B>{}, 0, f0);                     // behind the last stage: nothing uses it
+    if (SM == kBrought && B == 0) {
+      // where the scales lay that were last read behind the barrier of stage k - 2
+      put_scales((k >> 1) + 1);
+      bring_scales((k >> 1) + 2);
+    }
     copy(place(k + 2), b);
-    if (SL && B == 0) copy_scales((k + 2) >> 1);
+    if (SM == kCopied && B == 0) copy_scales((k >> 1) + 1);
     multiply(MxC<3>{}, f1);
     interleave();
     use_scales(k + 1, sn);
   };
 
   copy(place(0), MxC<0>{});
-  if (SL) copy_scales(0);
-  else load_scales(0, sn);
+  if constexpr (SM == kCopied) {
+    copy_scales(0);
+  } else if constexpr (SM == kBrought) {
+    bring_scales(0);
+    put_scales(0);
+    bring_scales(1);
+  } else {
+    load_scales(0, sn);
+  }
   copy(place(1), MxC<1>{});
   __builtin_amdgcn_s_waitcnt(0x0070);
   mx_barrier();
@@ -424,11 +487,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   }
 }
 
-template <int WM, int WN, int TM, int TN, int KG, bool SL, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int SM, int OCC>
 static void launch_tile(const Mx4GemmArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   const int tm = (int)((a.M + BM - 1) / BM), tn = (int)((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, SL, OCC>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, SM, OCC>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN * KG), 0, s, a, tm, tn);
 }
 
@@ -450,15 +513,24 @@ static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
 //   32 x 32    64 x 4096 x 14336 (256), teams of 4, 13 | - | 17
 constexpr int kEnough = 180;
 
-template <bool SL>
+// Scales of rows that are not whole words: through LDS where stages are many and
+// tiles large (4096 x 4096 x 4128 52 us against 65), each lane its own where not (64 x
+// 4096 x 4128 7.6 against 8.7).
+template <int WM, int WN, int TM, int TN, int KG, int OCC>
+static void launch_scales(const Mx4GemmArgs& a, hipStream_t s) {
+  if (a.K % 128 == 0) launch_tile<WM, WN, TM, TN, KG, kCopied, OCC>(a, s);
+  else if (KG <= 2 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, KG <= 2 ? kBrought : kOwn, OCC>(a, s);
+  else launch_tile<WM, WN, TM, TN, KG, kOwn, OCC>(a, s);
+}
+
 static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
   auto count = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (count(256, 256) >= kEnough) launch_tile<4, 2, 2, 4, 1, SL, 1>(a, s);
-  else if (count(128, 128) >= kEnough) launch_tile<2, 2, 2, 2, 1, SL, 2>(a, s);
-  else if (count(64, 64) >= 2 * kEnough) launch_tile<2, 2, 1, 1, 1, SL, 4>(a, s);
-  else if (count(64, 64) >= kEnough) launch_tile<2, 2, 1, 1, 2, SL, 2>(a, s);
-  else if (count(32, 64) >= kEnough) launch_tile<1, 2, 1, 1, 4, SL, 1>(a, s);
-  else launch_tile<1, 1, 1, 1, 4, SL, 1>(a, s);
+  if (count(256, 256) >= kEnough) launch_scales<4, 2, 2, 4, 1, 1>(a, s);
+  else if (count(128, 128) >= kEnough) launch_scales<2, 2, 2, 2, 1, 2>(a, s);
+  else if (count(64, 64) >= 2 * kEnough) launch_scales<2, 2, 1, 1, 1, 4>(a, s);
+  else if (count(64, 64) >= kEnough) launch_scales<2, 2, 1, 1, 2, 2>(a, s);
+  else if (count(32, 64) >= kEnough) launch_scales<1, 2, 1, 1, 4, 1>(a, s);
+  else launch_scales<1, 1, 1, 1, 4, 1>(a, s);
 }
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
@@ -470,8 +542,7 @@ hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
   // blocks of K.
   if (a.K < 128) launch_rows<4, 8>(a, s);
   else if (a.M <= 16 && a.N <= 8192) launch_rows<1, 8>(a, s);
-  else if (a.K % 128 == 0) launch_tiles<true>(a, s);
-  else launch_tiles<false>(a, s);
+  else launch_tiles(a, s);
   return hipGetLastError();
 }
 
