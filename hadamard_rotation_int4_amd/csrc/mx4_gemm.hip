@@ -69,25 +69,51 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_gemm_rows_kernel(Mx4GemmArgs p
   v4f acc[MT];
 #pragma unroll
   for (int t = 0; t < MT; ++t) acc[t] = (v4f){0.0f, 0.0f, 0.0f, 0.0f};
-  for (int q = wave; q < runs; q += WAVES) {
+  struct Run {
     uint4 wc[4], ac[MT][4];
-    Scales as[MT];
+    Scales ws, as[MT];
+  };
+  auto load = [&](int q, Run& x) {
 #pragma unroll
-    for (int s = 0; s < 4; ++s) wc[s] = *reinterpret_cast<const uint4*>(w + 256 * q + 64 * s);
-    const Scales ws = *reinterpret_cast<const Scales*>(sw + 16 * q);
+    for (int s = 0; s < 4; ++s) x.wc[s] = *reinterpret_cast<const uint4*>(w + 256 * q + 64 * s);
+    x.ws = *reinterpret_cast<const Scales*>(sw + 16 * q);
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
 #pragma unroll
-      for (int s = 0; s < 4; ++s) ac[t][s] = *reinterpret_cast<const uint4*>(a[t] + 256 * q + 64 * s);
-      as[t] = *reinterpret_cast<const Scales*>(sa[t] + 16 * q);
+      for (int s = 0; s < 4; ++s) x.ac[t][s] = *reinterpret_cast<const uint4*>(a[t] + 256 * q + 64 * s);
+      x.as[t] = *reinterpret_cast<const Scales*>(sa[t] + 16 * q);
     }
+  };
+  auto multiply = [&](const Run& x) {
 #pragma unroll
     for (int s = 0; s < 4; ++s)
 #pragma unroll
       for (int t = 0; t < MT; ++t)
-        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(wc[s]), fp4_operand(ac[t][s]), acc[t], kFp4,
-                                                                  kFp4, 0, (int)(ws.v[s] >> (8 * kb)), 0,
-                                                                  (int)(as[t].v[s] >> (8 * kb)));
+        acc[t] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fp4_operand(x.wc[s]), fp4_operand(x.ac[t][s]), acc[t], kFp4,
+                                                                  kFp4, 0, (int)(x.ws.v[s] >> (8 * kb)), 0,
+                                                                  (int)(x.as[t].v[s] >> (8 * kb)));
+  };
+  if (MT == 1) {
+    // the next run is under way while one is multiplied (one token, 4096 x 4096: 4.1 ->
+    // 3.7 us)
+    Run x, y;
+    int q = wave;
+    if (q < runs) load(q, x);
+    for (; q + WAVES < runs; q += 2 * WAVES) {
+      load(q + WAVES, y);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(x);
+      if (q + 2 * WAVES < runs) load(q + 2 * WAVES, x);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(y);
+    }
+    if (q < runs) multiply(x);
+  } else {
+    for (int q = wave; q < runs; q += WAVES) {
+      Run x;
+      load(q, x);
+      multiply(x);
+    }
   }
   // what is left of K: fewer than four steps, past its end zero codes and scales
   if (wave == runs % WAVES) {
@@ -536,12 +562,12 @@ static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
   Mx4GemmArgs a = args;
   a.stream = a.M * a.N * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
-  // A few rows are bound by the weights' bytes, which go straight to registers: 16 x
-  // 4096 x 14336 9.6 us (32 x 32 tiles 14).  With many columns a 32 x 64 tile reads
-  // the rows of A less often: 16 x 14336 x 4096 8.9 us against 11.5.  Tiles need four
-  // blocks of K.
+  // A few rows are bound by the weights' bytes, which go straight to registers while
+  // there is a workgroup for each compute unit: 16 x 4096 x 14336 9.5 us (32 x 64 tiles
+  // 15), one row 7.3.  With more columns tiles read the rows of A less often: 16 x 8192 x
+  // 8192 9.6 us in 32 x 32 tiles, 13.7 in rows.  Tiles need four blocks of K.
   if (a.K < 128) launch_rows<4, 8>(a, s);
-  else if (a.M <= 16 && a.N <= 8192) launch_rows<1, 8>(a, s);
+  else if (a.M <= 16 && a.N <= 4096) launch_rows<1, 8>(a, s);
   else launch_tiles(a, s);
   return hipGetLastError();
 }

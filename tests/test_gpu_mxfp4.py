@@ -314,7 +314,11 @@ def test_gemm_tiles(m, n, k, dtype):
 
 @pytest.mark.parametrize("m,n,k", [(3400, 3601, 256), (3333, 3600, 288), (1700, 1801, 512), (1793, 1700, 544),
                                    (1400, 1150, 384), (1300, 1201, 416), (832, 1024, 640), (833, 1023, 672),
-                                   (12, 8200, 512), (16, 9001, 160)])
+                                   (12, 8200, 512), (16, 9001, 160), (12, 12000, 1152),
+                                   # odd numbers of blocks past the first run of each kind
+                                   (3400, 3601, 1056), (3333, 3600, 2080), (1700, 1801, 1120), (1793, 1700, 1088),
+                                   (1400, 1150, 1184), (1300, 1201, 1504), (832, 1024, 1248), (833, 1023, 1376),
+                                   (1210, 1190, 1440), (850, 1000, 1312), (849, 1001, 1216), (1700, 1801, 1152)])
 def test_gemm_every_tile(m, n, k):
     """Sizes that reach each tile, with whole and with ragged edges and both ways
     of the scales; rows and columns of all parts of the product."""
