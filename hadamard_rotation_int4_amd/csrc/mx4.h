@@ -80,5 +80,10 @@ void launch_mx4_rotate_quant(const Mx4QuantArgs& a, hipStream_t s);
 void launch_mx4_rotate_back(const Mx4DequantArgs& a, hipStream_t s);
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t s);
 hipError_t launch_norm(const NormArgs& a, hipStream_t s);
+// Its parts by the types of the stream and of the block.
+void launch_norm_f16(const NormArgs& a, hipStream_t s);
+void launch_norm_f32_bf16(const NormArgs& a, hipStream_t s);
+void launch_norm_f32_f16(const NormArgs& a, hipStream_t s);
+void launch_norm_f32(const NormArgs& a, hipStream_t s);
 
 }  // namespace hr

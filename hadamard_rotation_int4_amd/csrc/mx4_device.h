@@ -22,15 +22,13 @@ __device__ __forceinline__ constexpr float mx4_norm() {
   return L == 4 ? 0.17677669529663687f : L == 8 ? 0.125f : L == 16 ? 0.08838834764831845f : 0.0625f;
 }
 
-// This lane's octet among the lanes of its wave (L = 0: no rotation).
-template <int L>
-__device__ __forceinline__ int mx4_lane(int lane) {
-  return L >= 8 ? (lane & ~(L - 1)) | kv4_logical<L>(lane) : lane;
-}
+// This lane's octet among the lanes of its wave.
+__device__ __forceinline__ int mx4_lane(int lane) { return (lane & ~31) | kv4_logical<32>(lane); }
 
-// Whether mx4_fwht leaves this lane's values negated; a: its octet in its block.
-template <int L>
-__device__ __forceinline__ bool mx4_negated(int a) { return __popc(a & (L >= 16 ? 15 : L - 1)) & 1; }
+// Whether mx4_fwht of this order leaves this lane's values negated (an exchange with a
+// multiplier of -1 makes own - partner of partner - own; the last one, of order 256,
+// is no such exchange); a: its octet in its block.
+__device__ __forceinline__ bool mx4_negated(int a, int order) { return __popc(a & (min(order, 128) / 8 - 1)) & 1; }
 
 // w[i] += dpp(w[i]) * sigma for 8 registers, as HR_FMAC_DPP16.
 #define HR_FMAC_DPP8(w, sigma, CTRL) \
@@ -46,34 +44,9 @@ __device__ __forceinline__ bool mx4_negated(int a) { return __popc(a & (L >= 16 
   : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3]), "+v"(w[4]), "+v"(w[5]), "+v"(w[6]), "+v"(w[7]) \
   : "v"(sigma))
 
-// w[0..7] := H_{8 L} w over L lanes, negated where mx4_negated; a: the lane's octet in
-// its block.
-template <int L>
-__device__ __forceinline__ void mx4_fwht(float* w, int a) {
-  fwht_regs<8>(w);
-  const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;
-  HR_FMAC_DPP8(w, b0, "quad_perm:[1,0,3,2]");
-  HR_FMAC_DPP8(w, b1, "quad_perm:[2,3,0,1]");
-  if (L >= 8) {
-    const float b2 = (a & 4) ? -1.0f : 1.0f;
-    HR_FMAC_DPP8(w, b2, "row_half_mirror");
-  }
-  if (L >= 16) {
-    const float b3 = (a & 8) ? -1.0f : 1.0f;
-    HR_FMAC_DPP8(w, b3, "row_ror:8");
-  }
-  if (L >= 32) {
-    const float b4 = (a & 16) ? -1.0f : 1.0f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const auto s = __builtin_amdgcn_permlane16_swap(__float_as_uint(w[e]), __float_as_uint(w[e]), false, false);
-      w[e] = fmaf(__uint_as_float(s[1]), b4, __uint_as_float(s[0]));
-    }
-  }
-}
-
-// The same for an order (32 to 256) known at run time; one of 0 leaves w as it is.
-__device__ __forceinline__ void mx4_fwht_any(float* w, int a, int order) {
+// w[0..7] := H_order w over order / 8 lanes, negated where mx4_negated; a: the lane's
+// octet in its block.  Order 0 leaves w as it is.
+__device__ __forceinline__ void mx4_fwht(float* w, int a, int order) {
   if (order == 0) return;
   fwht_regs<8>(w);
   const float b0 = (a & 1) ? -1.0f : 1.0f, b1 = (a & 2) ? -1.0f : 1.0f;

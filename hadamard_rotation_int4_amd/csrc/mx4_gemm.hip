@@ -174,7 +174,7 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // the source chunk of a lane that is permuted, within the row's 128 bytes.
 //
 // SM, how a lane gets its scales.  kCopied: copied into LDS, 16 bytes of each row
-// every second stage, for K a multiple of 128 (whole words).  kBrought: the same
+// every second stage, where each row's are whole words.  kBrought: the same
 // through registers, at any alignment, for K of at least 512.  kOwn: each lane loads
 // its own words.
 //
@@ -544,18 +544,22 @@ constexpr int kEnough = 180;
 // 4096 x 4128 7.6 against 8.7).
 template <int WM, int WN, int TM, int TN, int KG, int OCC>
 static void launch_scales(const Mx4GemmArgs& a, hipStream_t s) {
-  if (a.K % 128 == 0) launch_tile<WM, WN, TM, TN, KG, kCopied, OCC>(a, s);
+  const bool words = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.sa) | reinterpret_cast<uintptr_t>(a.sw)) & 3u) == 0;
+  if (words) launch_tile<WM, WN, TM, TN, KG, kCopied, OCC>(a, s);
   else if (KG <= 2 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, KG <= 2 ? kBrought : kOwn, OCC>(a, s);
   else launch_tile<WM, WN, TM, TN, KG, kOwn, OCC>(a, s);
 }
 
 static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
-  auto count = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
-  if (count(256, 256) >= kEnough) launch_scales<4, 2, 2, 4, 1, 1>(a, s);
-  else if (count(128, 128) >= kEnough) launch_scales<2, 2, 2, 2, 1, 2>(a, s);
-  else if (count(64, 64) >= 2 * kEnough) launch_scales<2, 2, 1, 1, 1, 4>(a, s);
-  else if (count(64, 64) >= kEnough) launch_scales<2, 2, 1, 1, 2, 2>(a, s);
-  else if (count(32, 64) >= kEnough) launch_scales<1, 2, 1, 1, 4, 1>(a, s);
+  // enough of them, and more than half of one filled either way
+  auto fit = [&](int bm, int bn, int enough) {
+    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= enough && 2 * a.M > bm && 2 * a.N > bn;
+  };
+  if (fit(256, 256, kEnough)) launch_scales<4, 2, 2, 4, 1, 1>(a, s);
+  else if (fit(128, 128, kEnough)) launch_scales<2, 2, 2, 2, 1, 2>(a, s);
+  else if (fit(64, 64, 2 * kEnough)) launch_scales<2, 2, 1, 1, 1, 4>(a, s);
+  else if (fit(64, 64, kEnough)) launch_scales<2, 2, 1, 1, 2, 2>(a, s);
+  else if (fit(32, 64, kEnough)) launch_scales<1, 2, 1, 1, 4, 1>(a, s);
   else launch_scales<1, 1, 1, 1, 4, 1>(a, s);
 }
 

@@ -152,7 +152,7 @@ template <int L>
 __global__ __launch_bounds__(kMx4Threads) void mx4_quant_kernel(Mx4QuantArgs p, int64_t octets, uint32_t magic) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int a = mx4_lane<L>(lane);
+  const int a = mx4_lane(lane);
   const int64_t first = ((int64_t)blockIdx.x * (kMx4Threads / 64) + wave) * 64;
   if (first >= octets) return;
   const int64_t o = first + a;
@@ -167,8 +167,8 @@ __global__ __launch_bounds__(kMx4Threads) void mx4_quant_kernel(Mx4QuantArgs p, 
   load_signs<8>(p.signs, 8 * col, sg);
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] = flip(w[e], sg[e]);
-  mx4_fwht<L>(w, a);
-  const float f = mx4_negated<L>(a) ? -mx4_norm<L>() : mx4_norm<L>();
+  mx4_fwht(w, a, 8 * L);
+  const float f = mx4_negated(a, 8 * L) ? -mx4_norm<L>() : mx4_norm<L>();
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] *= f;
   const uint32_t b = mx4_scale(mx4_absmax(w), p.ceil);
@@ -183,7 +183,7 @@ template <int L>
 __global__ __launch_bounds__(kMx4Threads) void mx4_back_kernel(Mx4DequantArgs p, int64_t octets, uint32_t magic) {
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int a = mx4_lane<L>(lane);
+  const int a = mx4_lane(lane);
   const int64_t first = ((int64_t)blockIdx.x * (kMx4Threads / 64) + wave) * 64;
   if (first >= octets) return;
   const int64_t o = first + a;
@@ -199,8 +199,8 @@ __global__ __launch_bounds__(kMx4Threads) void mx4_back_kernel(Mx4DequantArgs p,
   const float f = mx4_power(b);
 #pragma unroll
   for (int e = 0; e < 8; ++e) w[e] *= f;
-  mx4_fwht<L>(w, a);
-  const float g = mx4_negated<L>(a) ? -mx4_norm<L>() : mx4_norm<L>();
+  mx4_fwht(w, a, 8 * L);
+  const float g = mx4_negated(a, 8 * L) ? -mx4_norm<L>() : mx4_norm<L>();
   uint32_t sg[8];
   load_signs<8>(p.signs, 8 * col, sg);
 #pragma unroll

@@ -609,6 +609,8 @@ int64_t hr_kv4_attention_workspace(int32_t heads, int32_t dim, int32_t dtype, in
  *           bit 3 of a code is its sign, bits 0-2 count the magnitudes 0, 0.5,
  *           1, 1.5, 2, 3, 4, 6.
  *   scales  [rows][n/32] uint8, byte b stands for 2^(b - 127), 255 for NaN.
+ * Codes are 16-byte aligned; scales need no alignment (those of some rows of an
+ * operand are its scales from there on).
  */
 
 /* How a block's scale follows from its largest magnitude a. */
@@ -635,7 +637,7 @@ typedef enum {
  *   x       [rows] rows of n elements of x_dtype (HR_F32, HR_BF16 or HR_F16),
  *           x_stride elements apart (at least n; a multiple of 16 bytes).
  *   n       a multiple of 32, at most 2^18; rows * n is at most 2^34.
- *   codes, scales  as above, 16-byte aligned as x is.
+ *   x is 16-byte aligned; codes, scales  as above.
  */
 int32_t hr_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t rows, int32_t n, int32_t rule,
                        uint8_t* codes, uint8_t* scales, void* stream);
@@ -683,7 +685,7 @@ int32_t hr_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t ro
  * scale byte of 255 makes its row (or column) of C NaN.
  *
  *   a_codes, a_scales  [M][K/2], [M][K/32];  w_codes, w_scales  [N][K/2],
- *             [N][K/32], all 16-byte aligned.
+ *             [N][K/32].
  *   K         a multiple of 32, at most 2^18;  M and N at most 2^21, M * N at
  *             most 2^36 (2^30 with K below 128).
  *   c         [M][N] of dtype (HR_F32, HR_BF16 or HR_F16).
@@ -730,7 +732,7 @@ typedef struct {
  *   residual  [rows] rows of x_dtype, residual_stride apart; x itself (with its
  *             stride) is allowed, any other overlap is undefined.  NULL without
  *             block_out.
- *   h         [rows][n] of dtype, or NULL: only r.
+ *   h         [rows][n] of dtype, or NULL: only r; overlaps nothing.
  */
 int32_t hr_norm_residual(const hr_norm* p, void* residual, int64_t residual_stride, void* h, void* stream);
 

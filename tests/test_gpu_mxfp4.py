@@ -370,6 +370,50 @@ def test_gemm_nan_scales_stay_in_their_rows(m):
     assert torch.equal(got[keep_m][:, :n - 1], clean[keep_m][:, :n - 1])
 
 
+@pytest.mark.parametrize("m,n,k", [(5, 40, 544), (40, 200, 640), (300, 260, 1056), (700, 1300, 1024), (900, 1800, 1184)])
+def test_gemm_some_rows_of_operands(m, n, k):
+    """Rows from the middle of larger operands: scales at any address."""
+    rng = _rng(m + n)
+    a, w = _operand(rng, m + 8, k), _operand(rng, n + 5, k)
+    ta, tw = [_t(v) for v in a], [_t(v) for v in w]
+    got = hr.mxfp4_gemm(ta[0][3:3 + m], ta[1][3:3 + m], tw[0][1:1 + n], tw[1][1:1 + n], dtype=torch.bfloat16)
+    check_gemm(got, a[0][3:3 + m], a[1][3:3 + m], w[0][1:1 + n], w[1][1:1 + n], torch.bfloat16)
+    one = hr.dequant_mxfp4(ta[0][3:3 + m], ta[1][3:3 + m])
+    assert np.array_equal(_num(one), mxfp4.values(a[0][3:3 + m], a[1][3:3 + m]))
+    x = _rows(rng, m, k, torch.bfloat16)
+    codes, scales = torch.zeros_like(ta[0]), torch.zeros_like(ta[1])
+    hr.quant_mxfp4(x, codes=codes[3:3 + m], scales=scales[3:3 + m])
+    check_exact(x, codes[3:3 + m], scales[3:3 + m], "floor")
+    assert not scales[:3].any() and not scales[3 + m:].any() and not codes[:3].any() and not codes[3 + m:].any()
+
+
+@pytest.mark.parametrize("m,n,k", [(60000, 8, 512), (9000, 3, 1056), (47000, 40, 256), (30, 20000, 288), (2000, 1, 64)])
+def test_gemm_narrow(m, n, k):
+    rng = _rng(m + n)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=torch.bfloat16)
+    at = np.unique(np.concatenate([np.arange(min(m, 40)), np.arange(max(0, m - 300), m), rng.integers(0, m, 300)]))
+    check_gemm(got[torch.from_numpy(at).to(DEV)], a[0][at], a[1][at], *w, torch.bfloat16)
+
+
+def test_gemm_output_past_4_gib():
+    rng = _rng(8)
+    m, n, k = 40000, 60001, 128
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=torch.bfloat16)
+    at = np.concatenate([np.arange(4), rng.integers(0, m, 20), np.arange(m - 4, m)])
+    check_gemm(got[torch.from_numpy(at).to(DEV)], a[0][at], a[1][at], *w, torch.bfloat16)
+
+
+@pytest.mark.parametrize("m", [1, 20, 200, 400])
+def test_gemm_farthest_scales(m):
+    """2^-127 on one side and up to 2^127 on the other."""
+    rng = _rng(m + 7)
+    n, k = 50, 256
+    a, w = _operand(rng, m, k, 0, 2), _operand(rng, n, k, 250, 255)
+    check_gemm(hr.mxfp4_gemm(*map(_t, a + w)), *a, *w, torch.float32)
+
+
 @pytest.mark.parametrize("m", [1, 20, 200, 400])
 def test_gemm_far_scales(m):
     """Scales at both ends of their range, whose products are not, and zero codes

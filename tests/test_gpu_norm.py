@@ -63,7 +63,7 @@ def check(a, got, dtype):
     assert (np.abs(_num(out) - h) <= dh + np.abs(h) * _half_step(dtype) + tiny).all()
 
 
-SIZES = [(1, 1), (3, 7), (2, 8), (5, 63), (4, 64), (7, 500), (3, 512), (3, 520), (2, 1000), (3, 2047), (2, 2048),
+SIZES = [(1, 1), (9, 33), (33, 64), (70, 65), (17, 128), (18, 129), (9, 256), (5, 257), (3, 7), (2, 8), (5, 63), (4, 64), (7, 500), (3, 512), (3, 520), (2, 1000), (3, 2047), (2, 2048),
          (3, 2049), (2, 4096), (3, 5000), (2, 8192), (2, 8200), (3, 14336), (2, 16384), (2, 16385), (1, 32768)]
 
 
@@ -87,8 +87,8 @@ def test_parts(n, block, post, weights, gates, stream, dtype):
         assert r is a["x"]
 
 
-@pytest.mark.parametrize("rows", [1, 2, 255, 300, 5000])
-@pytest.mark.parametrize("n", [64, 100, 2048, 4096])
+@pytest.mark.parametrize("rows,n", [(rows, n) for rows in (1, 2, 255, 300, 5000, 33333)
+                                    for n in (24, 64, 100, 200, 384, 2048, 4096) if rows * n < 1.3e7])
 def test_many_rows(rows, n):
     gates = rows // 5 if rows % 5 == 0 else rows
     a = _case(_rng(rows), rows, n, "bf16", "bf16", gates=gates)
@@ -147,7 +147,7 @@ def test_no_rows():
 
 @pytest.mark.parametrize("stream,dtype", PAIRS)
 @pytest.mark.parametrize("order", [0, 32, 64, 128, 256])
-@pytest.mark.parametrize("rows,blocks", [(1, 1), (3, 3), (2, 8), (3, 17), (2, 24)])
+@pytest.mark.parametrize("rows,blocks", [(1, 1), (37, 1), (19, 2), (3, 3), (2, 8), (3, 17), (2, 24)])
 @pytest.mark.parametrize("rule", ["floor", "ceil"])
 def test_quantized(rows, blocks, order, stream, dtype, rule):
     rng = _rng(order + rows + blocks)

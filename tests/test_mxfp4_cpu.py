@@ -32,7 +32,6 @@ def _quant(fn="hr_rotate_quant_mxfp4", **kw):
     (dict(scales=None), hr.HR_EINVAL),
     (dict(x=P + 8), hr.HR_EINVAL),
     (dict(codes=P + 4), hr.HR_EINVAL),
-    (dict(scales=P + 1), hr.HR_EINVAL),
     (dict(dt=3), hr.HR_EINVAL),
     (dict(rule=2), hr.HR_EINVAL),
     (dict(rule=-1), hr.HR_EINVAL),
@@ -98,7 +97,7 @@ def _gemm(**kw):
     (dict(sw=None), hr.HR_EINVAL),
     (dict(c=None), hr.HR_EINVAL),
     (dict(a=P + 8), hr.HR_EINVAL),
-    (dict(sw=P + 2), hr.HR_EINVAL),
+    (dict(w=P + 2), hr.HR_EINVAL),
     (dict(c=P + 4), hr.HR_EINVAL),
     (dict(M=-1), hr.HR_EINVAL),
     (dict(dt=3), hr.HR_EINVAL),
