@@ -7,8 +7,19 @@
 //
 // v_mfma_scale_f32_16x16x128_f8f6f4: lane l holds row l % 16 of its operand and
 // the 32 codes (16 bytes) of block l / 16 of the step's four, with that block's
-// scale byte.  The weights are the first operand, so that a lane's four results
-// are four consecutive columns of one row of C.
+// scale byte; the 32x32x64 form likewise with rows l % 32 and two blocks.  The
+// weights are the first operand, so that a lane's results are four consecutive
+// columns of one row of C at a time.
+//
+// Rates on random codes: the 32x32x64 instruction alone, nothing loaded, reaches 6.4
+// PFLOP/s on the whole card (9.0 on zeros: the clock falls with the power drawn, from
+// 2.5 to 1.5 GHz), the 16x16x128 one 5.7.  The 256 x 256 tile reaches 4.1 at 4096 x 4096
+// x 14336 and 3.9 at 8192 x 14336 x 4096 (242 us), where the matrix cores are busy 48% of
+// the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute unit) 3.6 PFLOP/s, 38 us,
+// 7 of them stores at the end and 3 the first loads.  What was tried on it made no
+// difference: other orders of its LDS reads, copies and products, waves' priorities,
+// copies spread over the steps, 4 waves of 128 x 128 (116 against 118 us), bank
+// conflicts taken out (270 against 272 us), dies starting at other stages of K.
 #include "mx4_device.h"
 
 namespace hr {
@@ -169,9 +180,10 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // row l % 32 of its operand and 32 codes; half h = l / 32 takes blocks 4 h + s at
 // step s < 4 of a stage, so that one 4-byte word holds a lane's scales of the
 // stage and the step picks its byte.  In LDS the 16-byte chunk c of row r sits
-// at chunk c ^ (r % 8): 8 consecutive rows of one chunk, which a read serves at
-// once, lie in 8 different places.  The copy writes LDS in lane order, so it is
-// the source chunk of a lane that is permuted, within the row's 128 bytes.
+// at chunk c ^ (r / 2 % 8): 16 consecutive rows of one chunk, which a read serves at
+// once, lie in the 16 places of 256 bytes (with r % 8 two and two met, 4 cycles a
+// read).  The copy writes LDS in lane order, so it is the source chunk of a lane that
+// is permuted, within the row's 128 bytes.
 //
 // SM, how a lane gets its scales.  kCopied: copied into LDS, 16 bytes of each row
 // every second stage, where each row's are whole words.  kBrought: the same
@@ -195,7 +207,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   constexpr int SPW = (QS + WAVES - 1) / WAVES;    // copies of a wave
   constexpr int SPT = (BM + BN + 64 * WAVES - 1) / (64 * WAVES);   // rows of scales of a thread
   constexpr int BUF = (BM + BN) * ROWB;
-  static_assert((QA + QW) % WAVES == 0, "equal copies a wave");
+  static_assert((QA + QW) % WAVES == 0 && DPW % 2 == 0 && QA % 2 == 0, "equal copies a wave, even and odd ones known");
   __shared__ __attribute__((aligned(16))) char sbuf0[KG * BUF];
   __shared__ __attribute__((aligned(16))) char sbuf1[KG * BUF];
   __shared__ __attribute__((aligned(16))) char sscale[KG * 2 * SCB];
@@ -222,11 +234,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + m0 * stride), 0, rows_a * stride, 0x00020000);
   const __amdgpu_buffer_rsrc_t rw =
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + n0 * stride), 0, rows_w * stride, 0x00020000);
-  const int chunk = (lane & 7) ^ (lane >> 3);
-  const int src = (lane >> 3) * stride + 16 * chunk;
-  // the last stage: chunks past the end take the row's last one (under zero scales)
+  // of even and odd copies; in the last stage chunks past the end take the row's last
+  // one (under zero scales)
   const int last = 8 * (stages - 1);
-  const int src_last = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
+  int src[2], src_last[2];
+#pragma unroll
+  for (int o = 0; o < 2; ++o) {
+    const int chunk = (lane & 7) ^ ((lane >> 4) + 4 * o);
+    src[o] = (lane >> 3) * stride + 16 * chunk;
+    src_last[o] = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
+  }
   auto buf = [&](auto b) -> char* {
     if constexpr (decltype(b)::value == 0) return sbuf0 + team * BUF;
     else return sbuf1 + team * BUF;
@@ -237,13 +254,15 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   // branch: the compiler would move products over it)
   auto copy = [&](int s, auto b) {
     char* dst = buf(b);
-    const int v = s < stages - 1 ? src : s < stages ? src_last : kNowhere;
+    int v[2];
+#pragma unroll
+    for (int o = 0; o < 2; ++o) v[o] = s < stages - 1 ? src[o] : s < stages ? src_last[o] : kNowhere;
 #pragma unroll
     for (int j = 0; j < DPW; ++j) {
       const int q = wave * DPW + j;
       const bool a = q < QA;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? ra : rw,
-                                               (__attribute__((address_space(3))) void*)(dst + 1024 * q), 16, v,
+                                               (__attribute__((address_space(3))) void*)(dst + 1024 * q), 16, v[j & 1],
                                                8 * (a ? q : q - QA) * stride + s * ROWB, 0, 0);
     }
   };
@@ -255,11 +274,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   struct __attribute__((packed, aligned(1))) Run { uint32_t v[4]; };
   const uint8_t* const sa = p.sa + m0 * blocks;
   const uint8_t* const sw = p.sw + n0 * blocks;
-  uint32_t sc[T], sn[T], srow[T];
+  uint32_t sc[T], sn[SL ? 2 * T : T], srow[T];     // of this stage, of the next (SL: of two)
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const int r = i < TM ? wm + 32 * i + l32 : wn + 32 * (i - TM) + l32;
-    if (SL) srow[i] = (uint32_t)(i < TM ? r : (SM == kCopied ? 64 * SA : BM) + r) * 16 + 4 * h + team * 2 * SCB;
+    if (SL) srow[i] = (uint32_t)(i < TM ? r : (SM == kCopied ? 64 * SA : BM) + r) * 16 + team * 2 * SCB;
     else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
   }
   // kCopied: of the team's stages 2 i and 2 i + 1; nothing is read behind the end of the
@@ -319,11 +338,16 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       *reinterpret_cast<v4u*>(sscale + (i & 1) * SCB + run_at[t]) = x;
     }
   };
-  auto load_scales = [&](int k, uint32_t* v) {      // of the team's stage k
+  // of the team's stage k; SL: of k, which is even, and k + 1, 16 bytes of a row at once
+  auto load_scales = [&](int k, uint32_t* v) {
     if constexpr (SL) {
 #pragma unroll
-      for (int i = 0; i < T; ++i)
-        v[i] = *reinterpret_cast<const uint32_t*>(sscale + ((k >> 1) & 1) * SCB + (k & 1) * 8 + srow[i]);
+      for (int i = 0; i < T; ++i) {
+        const v4u x = *reinterpret_cast<const v4u*>(sscale + ((k >> 1) & 1) * SCB + srow[i]);
+        const uint32_t x0 = h ? x[1] : x[0], x1 = h ? x[3] : x[2];
+        v[2 * i] = SM == kCopied && 8 * place(k) + 4 * h >= blocks ? 0u : x0;
+        v[2 * i + 1] = SM == kCopied && 8 * place(k + 1) + 4 * h >= blocks ? 0u : x1;
+      }
     } else {
       // past the end of a row its last word, shifted by use_scales
       const uint32_t from = min(8 * place(k) + 4 * h, blocks - 4);
@@ -331,11 +355,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       for (int i = 0; i < T; ++i) v[i] = reinterpret_cast<const Word*>((i < TM ? sa : sw) + (srow[i] + from))->v;
     }
   };
-  auto use_scales = [&](int k, const uint32_t* v) {
+  auto use_scales = [&](int k, auto odd, const uint32_t* v) {
     if constexpr (SL) {
-      const bool past = SM == kCopied && 8 * place(k) + 4 * h >= blocks;
 #pragma unroll
-      for (int i = 0; i < T; ++i) sc[i] = past ? 0u : v[i];
+      for (int i = 0; i < T; ++i) sc[i] = v[2 * i + decltype(odd)::value];
     } else {
       const int half = 4 * min(max(8 * place(k) + 4 * h - (blocks - 4), 0), 4);      // in two shifts: they may be 32 together
 #pragma unroll
@@ -352,7 +375,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
 
   int at[4];                       // of chunk 4 h + s of this lane's row in a tile
 #pragma unroll
-  for (int s = 0; s < 4; ++s) at[s] = l32 * ROWB + 16 * ((4 * h + s) ^ (l32 & 7));
+  for (int s = 0; s < 4; ++s) at[s] = l32 * ROWB + 16 * ((4 * h + s) ^ ((l32 >> 1) & 7));
   auto read = [&](auto b, int s, uint4 (&f)[T]) {
     const char* base = buf(b);
 #pragma unroll
@@ -395,10 +418,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     // every read of this buffer is done and the next stage has landed, in every wave
     __builtin_amdgcn_s_waitcnt(0x0070);            // vmcnt(0) lgkmcnt(0)
     mx_barrier();
-    if (SL) load_scales(k + 1, sn);
+    if (SL && B == 1) load_scales(k + 1, sn);
     read(MxC<1 - B>{}, 0, f0);                     // behind the last stage: nothing uses it
     if (SM == kBrought && B == 0) {
-      // where the scales lay that were last read behind the barrier of stage k - 2
+      // where the scales lay that were read behind the barrier of stage k - 3
       put_scales((k >> 1) + 1);
       bring_scales((k >> 1) + 2);
     }
@@ -406,7 +429,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     if (SM == kCopied && B == 0) copy_scales((k >> 1) + 1);
     multiply(MxC<3>{}, f1);
     interleave();
-    use_scales(k + 1, sn);
+    use_scales(k + 1, MxC<1 - B>{}, sn);
   };
 
   copy(place(0), MxC<0>{});
@@ -423,7 +446,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   __builtin_amdgcn_s_waitcnt(0x0070);
   mx_barrier();
   if (SL) load_scales(0, sn);
-  use_scales(0, sn);
+  use_scales(0, MxC<0>{}, sn);
   read(MxC<0>{}, 0, f0);
   // every team runs the same number: behind the end of K under zero scales
   const int turns = KG == 1 ? stages : (stages + 2 * KG - 1) / (2 * KG) * 2;

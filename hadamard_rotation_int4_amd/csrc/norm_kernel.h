@@ -321,6 +321,7 @@ static void launch_length(const NormArgs& a, hipStream_t s) {
   else if (a.n <= 128) launch_rows<XT, DT, 16, 1>(a, s);
   else if (a.n <= 256) launch_rows<XT, DT, 32, 1>(a, s);
   else if (a.n <= 512) launch_rows<XT, DT, 64, 1>(a, s);
+  else if (a.n <= 1024) launch_rows<XT, DT, 64, 2>(a, s);
   else if (a.n <= 2048) launch_rows<XT, DT, 256, 1>(a, s);
   else if (a.n <= 4096) launch_rows<XT, DT, 256, 2>(a, s);
   else if (a.n <= 8192) launch_rows<XT, DT, 512, 2>(a, s);
