@@ -1140,7 +1140,7 @@ def norm_residual(x: torch.Tensor, block_out: torch.Tensor | None = None, weight
     rows / gates rows; weight, post_weight: fp32 [n], or None (all 1).  x,
     block_out and residual may be strided.  dtype (block_out's or x's by
     default) is that of h: x's, or any for an fp32 x.  residual may be x (in
-    place).  Returns (r, h); h is None with want_h=False."""
+    place); outputs overlap nothing else.  Returns (r, h); h is None with want_h=False."""
     p, index, res, pr, rstep, rows, n, dtype = _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps,
                                                      dtype, residual, not want_h)
     if not want_h:

@@ -9,12 +9,14 @@
 // neighbouring lanes (columns), one v_fmac_f32_dpp an element; its signs, as in
 // kv4_device.h, are one for all of a lane's elements.
 //
-// Lane (column c, half h) supplies elements 16 h .. 16 h + 15 of its block.  The rows of H_32 are given to the instruction in the order in
-// which its results come out (v = 0 .. 15 of half h), so that a lane gets back
-// elements 16 h + v: 8 bytes of codes.
+// Lane (column c, half h) supplies elements 16 h .. 16 h + 15 of its block.  The rows
+// of H_32 are given to the instruction in the order in which its results come out
+// (v = 0 .. 15 of half h), so that a lane gets back elements 16 h + v: 8 bytes of codes.
 //
-// Against butterflies on the vector units (bf16 65536 x 2048, order 128: some 17
-// instructions an element) this needs 6.
+// Bound by memory: bf16 65536 x 2048, order 128, takes 57 us to the format and 60 back
+// (339 MB each, 5.9 and 5.7 TB/s, where a large copy reaches 5.3 and one operand negated
+// 6.1).  With butterflies on the vector units, 17 instructions an element, it was
+// their issue (there and back 190 us); this takes 6 an element.
 #include "mx4_device.h"
 
 namespace hr {

@@ -274,7 +274,7 @@ __global__ __launch_bounds__(LANES <= 64 ? 256 : LANES) void norm_kernel(NormArg
       const float f = 1.0f / sqrtf(row_sum(sum, slot + 1) / (float)p.n + p.eps);
 #pragma unroll
       for (int i = 0; i < CH; ++i) {
-float* const w = wt[KEEP ? i : 0];
+        float* const w = wt[KEEP ? i : 0];
         if (!KEEP) norm_factors(i, w);
 #pragma unroll
         for (int e = 0; e < 8; ++e) r[i][e] *= f * w[e];

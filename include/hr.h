@@ -680,8 +680,8 @@ int32_t hr_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t ro
  *
  * C[m][n] = sum over blocks j of 2^(Ea[m][j] + Ew[n][j]) sum_k qa qw.  The
  * products are exact and the sums fp32: each sum of a matrix instruction (64
- * or 128 terms and the running sum) is within 2^-22 of its largest term of the
- * exact one, and terms below 2^-126 may count as 0.  Rounded once to dtype.  A
+ * or 128 terms and the running sum) is within 2^-20 of its largest term (for each
+ * 64 terms) of the exact one, and terms below 2^-126 may count as 0.  Rounded once to dtype.  A
  * scale byte of 255 makes its row (or column) of C NaN.
  *
  *   a_codes, a_scales  [M][K/2], [M][K/32];  w_codes, w_scales  [N][K/2],

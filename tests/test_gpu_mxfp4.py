@@ -9,10 +9,13 @@ border, and either neighbour is allowed where it does.
 
 Reading back: rounded once (half a step of the type) on top of the same bound.
 
-Product: a matrix instruction sums 64 or 128 exact products and the running sum,
-each at most 2^-22 of the largest off, so K / 64 instructions and 8 joins of
-waves are within (K / 64 + 8) 2^-22 of the sum of magnitudes, plus half a step
-of the output's type.  Rounding to nearest makes infinity of what is at least the
+Product: a matrix instruction sums 64 or 128 exact products and the running sum.
+Bits below 2^-26 of the leading bit of its largest term fall away from each; a
+product's mantissa is 1, 9/8 or 3/2, so that at most 3/4 of that is lost: 64 (128)
+terms lose at most 1.5 2^-21 (2^-20) of the largest, which is less than 2^-20 for each
+64 of K.  check_gemm holds random operands, whose terms are of like size, to (K / 64 + 8)
+2^-22 of the sum of magnitudes (8: joins of waves), plus half a step of the
+output's type; test_gemm_terms_far_apart reaches what is lost.  Rounding to nearest makes infinity of what is at least the
 type's largest number and half a step (65520 in fp16).
 """
 import numpy as np
@@ -441,6 +444,26 @@ def test_gemm_same_every_time_and_outside_untouched(m, n, k):
     assert (guard[0] == 7.0).all() and (guard[m + 1] == 7.0).all()
 
 
+@pytest.mark.parametrize("m,k", [(1, 128), (16, 4096), (20, 512), (200, 128), (300, 4096), (700, 1024)])
+def test_gemm_terms_far_apart(m, k):
+    """One large term and all others around the last bits that are kept beside it: less than 2^-20 of the largest
+    for each 64 terms, and an fp32 sum's half step for each join of 8 waves."""
+    for big in (5, 6, 7):
+        for small in (2, 3, 5, 11):
+            for s in range(18, 30):
+                codes, w = np.full((m, k), small, dtype=np.uint8), np.full((200, k), small & 7, dtype=np.uint8)
+                codes[:, :32] = 0
+                codes[:, 0], w[:, 0] = big, big
+                sa = np.full((m, k // 32), 127 - s, dtype=np.uint8)
+                sa[:, 0] = 127
+                a, b = (mxfp4.pack(codes), sa), (mxfp4.pack(w), np.full((200, k // 32), 127, dtype=np.uint8))
+                got = hr.mxfp4_gemm(*map(_t, a + b))
+                assert torch.equal(got, got[:1, :1].expand(m, 200))
+                want = mxfp4.gemm(a[0][:1], a[1][:1], b[0][:1], b[1][:1])[0][0, 0]
+                most = max(mxfp4.LEVELS[big] ** 2, abs(want))
+                assert abs(got[0, 0].item() - want) <= (k / 64 * 2.0 ** -20 + 8 * 2.0 ** -24) * most
+
+
 def test_gemm_no_rows():
     rng = _rng(1)
     a, w = _operand(rng, 4, 64), _operand(rng, 4, 64)
@@ -516,3 +539,52 @@ def test_two_streams():
                 got.append(hr.mxfp4_gemm(*hr.quant_mxfp4(x), *w))
     torch.cuda.synchronize()
     assert all(torch.equal(g, v) for g, v in zip(got, want))
+
+
+def test_two_host_threads_at_once():
+    """Calls of two threads on streams of their own, over each other in time."""
+    import threading
+
+    rng = _rng(31)
+    cases = []
+    for m in (5, 300):
+        x, w = _rows(rng, m, 1024, torch.bfloat16), _rows(rng, 700, 1024, torch.bfloat16)
+        q = hr.quant_mxfp4(w)
+        cases.append((x, q, hr.mxfp4_gemm(*hr.rotate_quant_mxfp4(x, 128), *q)))
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(x, q, want):
+        s = torch.cuda.Stream()
+        with torch.cuda.stream(s):
+            for _ in range(50):
+                got = hr.mxfp4_gemm(*hr.rotate_quant_mxfp4(x, 128), *q)
+                s.synchronize()
+                if not torch.equal(got, want):
+                    bad.append(x.shape)
+
+    threads = [threading.Thread(target=work, args=c) for c in cases]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("order", [0, 128])
+def test_as_many_elements_as_there_may_be(dtype, order):
+    """2^34 elements: rows of the last ones like those of the first, there and back."""
+    n, unit = 4096, 1 << 10
+    rows = (1 << 34) // n
+    some = _rows(_rng(41), unit, n, TYPES[dtype])
+    x = some.repeat(rows // unit, 1)
+    codes, scales = hr.rotate_quant_mxfp4(x, order) if order else hr.quant_mxfp4(x)
+    want = hr.rotate_quant_mxfp4(some, order) if order else hr.quant_mxfp4(some)
+    for at in (0, rows // 2 - unit, rows // 2, rows - unit):
+        assert torch.equal(codes[at:at + unit], want[0]) and torch.equal(scales[at:at + unit], want[1])
+    assert bool((codes.view(-1, unit * n // 2).view(torch.int64) == want[0].view(-1).view(torch.int64)).all())
+    back = hr.dequant_mxfp4(*want, order=order, dtype=TYPES[dtype])
+    hr.dequant_mxfp4(codes, scales, order=order, dtype=TYPES[dtype], out=x)
+    for at in (0, rows // 2 - unit, rows // 2, rows - unit):
+        assert torch.equal(x[at:at + unit], back)

@@ -290,3 +290,30 @@ def test_a_step_captured_and_replayed_in_place():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out[0], r) and torch.equal(out[1], h)
+
+
+def test_as_many_rows_as_there_may_be():
+    rows, n = 1 << 24, 3
+    rng = _rng(51)
+    some = _rows(rng, 1 << 12, n, torch.bfloat16), _rows(rng, 1 << 12, n, torch.bfloat16)
+    x, block = (v.repeat(rows >> 12, 1) for v in some)
+    want = hr.norm_residual(*some, post_norm=True)
+    got = hr.norm_residual(x, block, post_norm=True)
+    for g, w in zip(got, want):
+        assert bool((g.view(-1, (1 << 12) * n) == w.view(-1)).all())
+    with pytest.raises(hr.HRError):
+        hr.norm_residual(torch.zeros(((1 << 24) + 1, 1), dtype=torch.bfloat16, device=DEV))
+
+
+@pytest.mark.parametrize("n", [40, 2048, 20000])
+def test_no_epsilon(n):
+    """eps = 0: rows of zeros are 0 / 0, all others as ever."""
+    x = _rows(_rng(n), 5, n, torch.float32)
+    x[2] = 0.0
+    r, h = hr.norm_residual(x, eps=0.0)
+    assert torch.equal(r, x) and torch.isnan(h[2]).all()
+    keep = [0, 1, 3, 4]
+    v = x[keep].double()
+    want = v / v.square().mean(-1, keepdim=True).sqrt()
+    # the sum's additions, at most 40 one after another in a lane and over lanes, halved by the root; root, quotient, product
+    assert ((h[keep].double() - want).abs() <= 24 * 2.0 ** -24 * want.abs()).all()

@@ -240,6 +240,42 @@ def test_binding_refusals(error, call):
         call()
 
 
+@pytest.mark.parametrize("current", [0, 1])
+def test_calls_go_to_the_tensors_device(monkeypatch, current):
+    """Tensors on device 1: its stream, and device 1 the current one during the call."""
+    import contextlib
+
+    now, seen = [current], []
+
+    @contextlib.contextmanager
+    def device(index):
+        before, now[0] = now[0], index
+        yield
+        now[0] = before
+
+    def call(a, stream):
+        seen.append((a, stream, now[0]))
+        return 0
+
+    monkeypatch.setattr(hr, "_get_device", lambda: now[0])
+    monkeypatch.setattr(hr, "_raw_stream", lambda index: 100 + index)
+    monkeypatch.setattr(hr, "_stream", lambda index: 100 + index)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    hr._launch(1, call, 5)
+    assert seen == [(5, 101, 1)] and now[0] == current
+
+
+def test_a_call_that_fails_raises():
+    def hr_call(stream):
+        return hr.HR_EDEVICE
+
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(hr, "_get_device", lambda: 0)
+        m.setattr(hr, "_raw_stream", lambda index: 0)
+        with pytest.raises(hr.HRError):
+            hr._launch(0, hr_call)
+
+
 # ------------------------------------------------------------------ the oracle
 
 def test_levels_and_their_codes():
