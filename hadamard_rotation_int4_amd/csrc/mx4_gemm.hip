@@ -16,7 +16,10 @@
 // 2.5 to 1.5 GHz), the 16x16x128 one 5.7.  The 256 x 256 tile reaches 4.1 at 4096 x 4096
 // x 14336 and 3.9 at 8192 x 14336 x 4096 (242 us), where the matrix cores are busy 48% of
 // the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute unit) 3.6 PFLOP/s, 38 us,
-// 7 of them stores at the end and 3 the first loads.  What was tried on it made no
+// 7 of them stores at the end and 3 the first loads.  Of 119 us at 4096 x 4096 x 14336 the
+// copies into LDS cost 19 (where they come from hardly matters: always of one stage, 115)
+// and the reads out of it 14: 192 KB read and 64 written a stage and workgroup, 2048
+// cycles of LDS, which is also what the products take.  What was tried on it made no
 // difference: other orders of its LDS reads, copies and products, waves' priorities,
 // copies spread over the steps, 4 waves of 128 x 128 (116 against 118 us), bank
 // conflicts taken out (270 against 272 us), dies starting at other stages of K.
@@ -41,14 +44,34 @@ __device__ __forceinline__ void store_c(const Mx4GemmArgs& p, int64_t at, float 
   else reinterpret_cast<_Float16*>(p.c)[at] = (_Float16)v;
 }
 
-// Eight of them, 16-byte aligned; around the L2s where C is large.
+// Eight of them at any address; around the L2s where C is large.
+template <int DT, bool NT>
+__device__ __forceinline__ void store_octet_as(void* c, int64_t at, const float* v) {
+  typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(c) + at * (DT == kDtF32 ? 4 : 2));
+#pragma unroll
+  for (int i = 0; i < (DT == kDtF32 ? 2 : 1); ++i) {
+    u32x4_any x;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if (DT == kDtF32) x[e] = __float_as_uint(v[4 * i + e]);
+      else if (DT == kDtBf16) x[e] = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
+      else x[e] = __builtin_bit_cast(uint32_t, (half2v){(_Float16)v[2 * e], (_Float16)v[2 * e + 1]});
+    }
+    if (NT) __builtin_nontemporal_store(x, q + i);
+    else q[i] = x;
+  }
+}
+
 __device__ __forceinline__ void store_octet_c(const Mx4GemmArgs& p, int64_t at, const float* v) {
   if (p.stream) {
-    if (p.dtype == kDtF32) store_vec<kDtF32, 8, true>(reinterpret_cast<float*>(p.c) + at, v);
-    else if (p.dtype == kDtBf16) store_vec<kDtBf16, 8, true>(reinterpret_cast<uint16_t*>(p.c) + at, v);
-    else store_vec<kDtF16, 8, true>(reinterpret_cast<uint16_t*>(p.c) + at, v);
+    if (p.dtype == kDtF32) store_octet_as<kDtF32, true>(p.c, at, v);
+    else if (p.dtype == kDtBf16) store_octet_as<kDtBf16, true>(p.c, at, v);
+    else store_octet_as<kDtF16, true>(p.c, at, v);
   } else {
-    store_vec_any<8>(p.dtype, p.c, at, v);
+    if (p.dtype == kDtF32) store_octet_as<kDtF32, false>(p.c, at, v);
+    else if (p.dtype == kDtBf16) store_octet_as<kDtBf16, false>(p.c, at, v);
+    else store_octet_as<kDtF16, false>(p.c, at, v);
   }
 }
 
@@ -105,20 +128,23 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_gemm_rows_kernel(Mx4GemmArgs p
                                                                   (int)(x.as[t].v[s] >> (8 * kb)));
   };
   if (MT == 1) {
-    // the next run is under way while one is multiplied (one token, 4096 x 4096: 4.1 ->
-    // 3.7 us)
-    Run x, y;
-    int q = wave;
-    if (q < runs) load(q, x);
-    for (; q + WAVES < runs; q += 2 * WAVES) {
-      load(q + WAVES, y);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(x);
-      if (q + 2 * WAVES < runs) load(q + 2 * WAVES, x);
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(y);
+    // the next three runs are under way while one is multiplied (16 x 4096 x 14336, 3.5 runs
+    // a wave: 11.0 us, with one 11.9, two 11.1, four 10.9)
+    constexpr int AHEAD = 3;
+    Run x[AHEAD + 1];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i)
+      if (wave + i * WAVES < runs) load(wave + i * WAVES, x[i]);
+    for (int q = wave; q < runs; q += (AHEAD + 1) * WAVES) {
+#pragma unroll
+      for (int i = 0; i <= AHEAD; ++i) {
+        const int at = q + i * WAVES;
+        if (at >= runs) break;
+        if (at + AHEAD * WAVES < runs) load(at + AHEAD * WAVES, x[(i + AHEAD) % (AHEAD + 1)]);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(x[i]);
+      }
     }
-    if (q < runs) multiply(x);
   } else {
     for (int q = wave; q < runs; q += WAVES) {
       Run x;
@@ -176,7 +202,8 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // v_mfma_scale_f32_32x32x64_f8f6f4 a wave.
 //
 // A stage is 256 codes of K: 128 bytes of each row, copied from memory into LDS
-// (8 rows an instruction), two stages in LDS.  A lane of the instruction holds
+// (8 rows an instruction), D stages in LDS: a stage of a small tile takes less time than
+// its copies are under way, so that D - 1 of them are at a time.  A lane of the instruction holds
 // row l % 32 of its operand and 32 codes; half h = l / 32 takes blocks 4 h + s at
 // step s < 4 of a stage, so that one 4-byte word holds a lane's scales of the
 // stage and the step picks its byte.  In LDS the 16-byte chunk c of row r sits
@@ -191,11 +218,11 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // its own words.
 //
 // KG: teams of WM WN waves that take pairs of stages in turn, each with buffers of
-// its own; their sums are joined in LDS, in the teams' order.  A stage of a small
-// tile takes as long as its loads do, and KG teams have KG times as many under way.
+// its own; their sums are joined in LDS, in the teams' order.  For the smallest tiles,
+// of which a workgroup would else be one or two waves.
 enum { kOwn, kCopied, kBrought };
 
-template <int WM, int WN, int TM, int TN, int KG, int SM, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
   constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
   constexpr int ROWB = 128;                        // bytes of a row and stage
@@ -208,9 +235,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   constexpr int SPT = (BM + BN + 64 * WAVES - 1) / (64 * WAVES);   // rows of scales of a thread
   constexpr int BUF = (BM + BN) * ROWB;
   static_assert((QA + QW) % WAVES == 0 && DPW % 2 == 0 && QA % 2 == 0, "equal copies a wave, even and odd ones known");
+  // arrays of their own, so that a read is known not to wait for copies into others
   __shared__ __attribute__((aligned(16))) char sbuf0[KG * BUF];
   __shared__ __attribute__((aligned(16))) char sbuf1[KG * BUF];
-  __shared__ __attribute__((aligned(16))) char sscale[KG * 2 * SCB];
+  __shared__ __attribute__((aligned(16))) char sbuf2[D > 2 ? KG * BUF : 16];
+  __shared__ __attribute__((aligned(16))) char sbuf3[D > 2 ? KG * BUF : 16];
+  __shared__ __attribute__((aligned(16))) char sscale0[(D > 2 ? 1 : 2) * KG * SCB];
+  __shared__ __attribute__((aligned(16))) char sscale1[D > 2 ? KG * SCB : 16];
   const int lane = threadIdx.x & 63, l32 = lane & 31, h = lane >> 5;
   const int wave_all = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int team = KG == 1 ? 0 : wave_all / WAVES, wave = wave_all - team * WAVES;
@@ -245,8 +276,17 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     src_last[o] = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
   }
   auto buf = [&](auto b) -> char* {
-    if constexpr (decltype(b)::value == 0) return sbuf0 + team * BUF;
-    else return sbuf1 + team * BUF;
+    constexpr int B = decltype(b)::value;
+    if constexpr (B == 0) return sbuf0 + team * BUF;
+    else if constexpr (B == 1) return sbuf1 + team * BUF;
+    else if constexpr (B == 2) return sbuf2 + team * BUF;
+    else return sbuf3 + team * BUF;
+  };
+  // the scales of the team's stages 2 i and 2 i + 1 (i odd or even known where D > 2)
+  auto slot = [&](int i, auto odd) -> char* {
+    if constexpr (D == 2) return sscale0 + (i & 1) * (KG * SCB) + team * SCB;
+    else if constexpr (decltype(odd)::value == 0) return sscale0 + team * SCB;
+    else return sscale1 + team * SCB;
   };
   // the team's stage i as a stage of K
   auto place = [&](int i) { return KG == 1 ? i : 2 * (KG * (i >> 1) + team) + (i & 1); };
@@ -274,28 +314,28 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   struct __attribute__((packed, aligned(1))) Run { uint32_t v[4]; };
   const uint8_t* const sa = p.sa + m0 * blocks;
   const uint8_t* const sw = p.sw + n0 * blocks;
-  uint32_t sc[T], sn[SL ? 2 * T : T], srow[T];     // of this stage, of the next (SL: of two)
+  // of this stage; of the next (SL: of two; kOwn: of the stages under way)
+  uint32_t sc[T], sn[SL ? 1 : D][SL ? 2 * T : T], srow[T];
 #pragma unroll
   for (int i = 0; i < T; ++i) {
     const int r = i < TM ? wm + 32 * i + l32 : wn + 32 * (i - TM) + l32;
-    if (SL) srow[i] = (uint32_t)(i < TM ? r : (SM == kCopied ? 64 * SA : BM) + r) * 16 + team * 2 * SCB;
+    if (SL) srow[i] = (uint32_t)(i < TM ? r : (SM == kCopied ? 64 * SA : BM) + r) * 16;
     else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
   }
   // kCopied: of the team's stages 2 i and 2 i + 1; nothing is read behind the end of the
   // operand, what is read of the next row behind the end of a row is not used
-  auto copy_scales = [&](int i) {
+  auto copy_scales = [&](int i, auto odd) {
     const int q = KG * i + team;
     const int v = 2 * q < stages ? lane * blocks : kNowhere;
 #pragma unroll
     for (int j = 0; j < SPW; ++j) {
-      const int c = wave * SPW + j;
+      // where waves are more than copies some make the same one
+      const int c = (wave * SPW + j) % QS;
       const bool a = c < SA;
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(a ? sa : sw), 0, (a ? rows_a : rows_w) * blocks, 0x00020000);
-      if (QS % WAVES == 0 || c < QS)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs,
-                                                 (__attribute__((address_space(3))) void*)(sscale + (2 * team + (i & 1)) * SCB + 1024 * c),
-                                                 16, v, 64 * (a ? c : c - SA) * blocks + 16 * q, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(slot(i, odd) + 1024 * c), 16, v,
+                                               64 * (a ? c : c - SA) * blocks + 16 * q, 0, 0);
     }
   };
   // kBrought: a thread brings 16 bytes of its rows, of the team's stages 2 i and 2 i +
@@ -309,7 +349,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     for (int t = 0; t < SPT; ++t) {
       const int r = min((int)threadIdx.x - team * 64 * WAVES + t * 64 * WAVES, BM + BN - 1);     // the last again
       run_row[t] = r < BM ? sa + (int64_t)min(r, rows_a - 1) * blocks : sw + (int64_t)min(r - BM, rows_w - 1) * blocks;
-      run_at[t] = (uint32_t)r * 16 + team * 2 * SCB;
+      run_at[t] = (uint32_t)r * 16;
       // the last 16 of the row, shifted down to where the last run begins
       const int down = 16 * runs - blocks;
       const Run x = *reinterpret_cast<const Run*>(run_row[t] + blocks - 16);
@@ -328,22 +368,22 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       run[t] = (v4u){x.v[0], x.v[1], x.v[2], x.v[3]};
     }
   };
-  auto put_scales = [&](int i) {
+  auto put_scales = [&](int i, auto odd) {
     const int q = KG * i + team;
 #pragma unroll
     for (int t = 0; t < SPT; ++t) {
       v4u x;
 #pragma unroll
       for (int e = 0; e < 4; ++e) x[e] = q < runs - 1 ? run[t][e] : q < runs ? run_last[t][e] : 0u;
-      *reinterpret_cast<v4u*>(sscale + (i & 1) * SCB + run_at[t]) = x;
+      *reinterpret_cast<v4u*>(slot(i, odd) + run_at[t]) = x;
     }
   };
   // of the team's stage k; SL: of k, which is even, and k + 1, 16 bytes of a row at once
-  auto load_scales = [&](int k, uint32_t* v) {
+  auto load_scales = [&](int k, auto odd, uint32_t* v) {
     if constexpr (SL) {
 #pragma unroll
       for (int i = 0; i < T; ++i) {
-        const v4u x = *reinterpret_cast<const v4u*>(sscale + ((k >> 1) & 1) * SCB + srow[i]);
+        const v4u x = *reinterpret_cast<const v4u*>(slot(k >> 1, odd) + srow[i]);
         const uint32_t x0 = h ? x[1] : x[0], x1 = h ? x[3] : x[2];
         v[2 * i] = SM == kCopied && 8 * place(k) + 4 * h >= blocks ? 0u : x0;
         v[2 * i + 1] = SM == kCopied && 8 * place(k + 1) + 4 * h >= blocks ? 0u : x1;
@@ -402,10 +442,15 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   };
 
   uint4 f0[T], f1[T];
+  // Loads of this wave that may be under way when the next stage has landed: those of the
+  // D - 2 stages behind it, and of their scales (of every second stage; kOwn of every
+  // stage).
+  constexpr int AWAY = (D - 2) * DPW + (SM == kCopied ? (D - 2) / 2 * SPW : SM == kBrought ? (D - 2) / 2 * SPT : (D - 2) * T);
+  constexpr int WAIT = 0x0070 | (AWAY & 15) | (AWAY >> 4) << 14;      // vmcnt(AWAY) lgkmcnt(0)
   // the team's stage k from buffer B: the fragments of its first step are in f0
   auto stage = [&](int k, auto b) {
-    constexpr int B = decltype(b)::value;
-    if (!SL) load_scales(k + 1, sn);
+    constexpr int B = decltype(b)::value, NEXT = (B + 1) % D;
+    if (!SL) load_scales(k + D - 1, MxC<0>{}, sn[SL ? 0 : (B + D - 1) % D]);
     read(b, 1, f1);
     multiply(MxC<0>{}, f0);
     interleave();
@@ -416,46 +461,74 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     multiply(MxC<2>{}, f0);
     interleave();
     // every read of this buffer is done and the next stage has landed, in every wave
-    __builtin_amdgcn_s_waitcnt(0x0070);            // vmcnt(0) lgkmcnt(0)
+    __builtin_amdgcn_s_waitcnt(WAIT);
     mx_barrier();
-    if (SL && B == 1) load_scales(k + 1, sn);
-    read(MxC<1 - B>{}, 0, f0);                     // behind the last stage: nothing uses it
-    if (SM == kBrought && B == 0) {
+    if (SL && B % 2 == 1) load_scales(k + 1, MxC<NEXT / 2 % 2>{}, sn[0]);
+    read(MxC<NEXT>{}, 0, f0);                      // behind the last stage: nothing uses it
+    if (SM == kBrought && B % 2 == 0) {
       // where the scales lay that were read behind the barrier of stage k - 3
-      put_scales((k >> 1) + 1);
+      put_scales((k >> 1) + 1, MxC<(B / 2 + 1) % 2>{});
       bring_scales((k >> 1) + 2);
     }
-    copy(place(k + 2), b);
-    if (SM == kCopied && B == 0) copy_scales((k >> 1) + 1);
+    copy(place(k + D), b);
+    // where the scales lay that were read behind the barrier of stage k - 1 (D = 2: k - 3)
+    if (SM == kCopied && B % 2 == 0) copy_scales((k >> 1) + D / 2, MxC<(B + D) / 2 % 2>{});
     multiply(MxC<3>{}, f1);
     interleave();
-    use_scales(k + 1, MxC<1 - B>{}, sn);
+    use_scales(k + 1, MxC<NEXT % 2>{}, sn[SL ? 0 : NEXT]);
   };
 
+  // In the order that AWAY counts.
+  auto fence = [&]() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if constexpr (!SL) load_scales(0, MxC<0>{}, sn[0]);
   copy(place(0), MxC<0>{});
   if constexpr (SM == kCopied) {
-    copy_scales(0);
+    copy_scales(0, MxC<0>{});
   } else if constexpr (SM == kBrought) {
     bring_scales(0);
-    put_scales(0);
-    bring_scales(1);
-  } else {
-    load_scales(0, sn);
+    put_scales(0, MxC<0>{});
   }
   copy(place(1), MxC<1>{});
-  __builtin_amdgcn_s_waitcnt(0x0070);
+  fence();
+  if constexpr (SM == kBrought) bring_scales(1);
+  if constexpr (D > 2) {
+    if constexpr (SM == kOwn) load_scales(1, MxC<0>{}, sn[1]);
+    fence();
+    copy(place(2), MxC<2>{});
+    if constexpr (SM == kCopied) copy_scales(1, MxC<1>{});
+    if constexpr (SM == kOwn) load_scales(2, MxC<0>{}, sn[2]);
+    fence();
+    copy(place(3), MxC<3>{});
+    fence();
+  }
+  // the first stage, of those that come in before the second one
+  constexpr int AWAY0 = D > 2 ? AWAY + DPW : 0;
+  __builtin_amdgcn_s_waitcnt(0x0070 | (AWAY0 & 15) | (AWAY0 >> 4) << 14);
   mx_barrier();
-  if (SL) load_scales(0, sn);
-  use_scales(0, MxC<0>{}, sn);
+  if (SL) load_scales(0, MxC<0>{}, sn[0]);
+  use_scales(0, MxC<0>{}, sn[0]);
   read(MxC<0>{}, 0, f0);
   // every team runs the same number: behind the end of K under zero scales
   const int turns = KG == 1 ? stages : (stages + 2 * KG - 1) / (2 * KG) * 2;
   int k = 0;
-  for (; k + 2 <= turns; k += 2) {
+  for (; k + D <= turns; k += D) {
     stage(k, MxC<0>{});
     stage(k + 1, MxC<1>{});
+    if constexpr (D > 2) {
+      stage(k + 2, MxC<2>{});
+      stage(k + 3, MxC<3>{});
+    }
   }
-  if (k < turns) stage(k, MxC<0>{});
+  if (k < turns) {
+    stage(k, MxC<0>{});
+    if constexpr (D > 2) {
+      if (k + 1 < turns) stage(k + 1, MxC<1>{});
+      if (k + 2 < turns) stage(k + 2, MxC<2>{});
+    }
+  }
   // no copy is left when LDS is written again or goes to another workgroup
   __builtin_amdgcn_s_waitcnt(0x0070);
   mx_barrier();
@@ -503,7 +576,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   constexpr int HALF = SKIP1 ? 0 : (KG * BUF - LEFT0) / (32 * PITCH);      // waves whose part fits in the first buffer
   static_assert(HALF >= WAVES || SKIP1 + (WAVES - HALF) * 32 * PITCH <= KG * BUF, "fits where the stages were");
   char* const part = wave < HALF ? sbuf0 + LEFT0 + wave * (32 * PITCH) : sbuf1 + SKIP1 + (wave - HALF) * (32 * PITCH);
-  const bool octets = p.N % 8 == 0;
 #pragma unroll
   for (int i = 0; i < TM; ++i) {
 #pragma unroll
@@ -513,34 +585,32 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
         *reinterpret_cast<v4f*>(part + l32 * PITCH + 16 * ((8 * j + 2 * q + h) ^ (l32 & 7))) =
             (v4f){acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
-    if (octets) {
-      constexpr int LPR = CW / 8;                  // lanes of a row
+    constexpr int LPR = CW / 8;                    // lanes of a row
 #pragma unroll
-      for (int r = 0; r < 32; r += 64 / LPR) {
-        const int rr = r + lane / LPR, n = 8 * (lane % LPR), m = wm + 32 * i + rr;
-        const v4f x = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4) ^ (rr & 7)));
-        const v4f y = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4 + 1) ^ (rr & 7)));
-        const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-        if (m < rows_a && wn + n < rows_w) store_octet_c(p, (m0 + m) * p.N + n0 + wn + n, v);
+    for (int r = 0; r < 32; r += 64 / LPR) {
+      const int rr = r + lane / LPR, n = 8 * (lane % LPR), m = wm + 32 * i + rr;
+      const v4f x = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4) ^ (rr & 7)));
+      const v4f y = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4 + 1) ^ (rr & 7)));
+      const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      const int64_t to = (m0 + m) * p.N + n0 + wn + n;
+      const int left = m < rows_a ? rows_w - wn - n : 0;
+      if (left >= 8) {
+        store_octet_c(p, to, v);
+      } else {
+#pragma unroll 1
+        for (int e = 0; e < left; ++e)
+          store_c(p, to + e, *reinterpret_cast<const float*>(part + rr * PITCH + 16 * (((n + e) / 4) ^ (rr & 7)) + 4 * (e % 4)));
       }
-    } else {
-      for (int r = 0; r < 32; ++r)
-#pragma unroll
-        for (int n = 0; n < CW; n += 64) {
-          const int m = wm + 32 * i + r, c = n + lane;
-          if ((CW % 64 == 0 || c < CW) && m < rows_a && wn + c < rows_w)
-            store_c(p, (m0 + m) * p.N + n0 + wn + c, *reinterpret_cast<const float*>(part + r * PITCH + 16 * ((c / 4) ^ (r & 7)) + 4 * (c % 4)));
-        }
     }
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int WM, int WN, int TM, int TN, int KG, int SM, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC>
 static void launch_tile(const Mx4GemmArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   const int tm = (int)((a.M + BM - 1) / BM), tn = (int)((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, SM, OCC>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, D, SM, OCC>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN * KG), 0, s, a, tm, tn);
 }
 
@@ -550,49 +620,63 @@ static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
                      dim3(64 * WAVES), 0, s, a);
 }
 
-// Which tile, by how many of them there are for the 256 compute units: the largest
-// of which there is about one for each (kEnough), a few stragglers costing less than
-// smaller tiles' traffic; fewer of the small ones get teams.  bf16, us, chosen |
-// next smaller | next larger:
-//   256 x 256  1024 x 14336 x 4096 (224 tiles) 34 | 42 | -;   3000 x 5120 x 5120 (240) 43 | 52 | -
-//   128 x 128  512 x 14336 x 4096 (448) 24 | 32 | 30;         1536 x 4096 x 4096 (384) 21 | 27 | 28
-//   64 x 64    512 x 4096 x 4096 (512) 12.2 | 12.4 in teams of 2 | 15.7
-//   in teams   256 x 4096 x 4096 (256) 9.6 | 13.3 | 10.9 alone, 15.4 (128 x 128)
-//   32 x 64    128 x 4096 x 14336 (256), teams of 4, 18 | - | 26
-//   32 x 32    64 x 4096 x 14336 (256), teams of 4, 13 | - | 17
-constexpr int kEnough = 180;
+// Which tile, by how many of them there are for the 256 compute units: the largest of
+// which there is about one for each (kEnough), a few idle units costing less than
+// smaller tiles' traffic.  Up to one for each keeps four stages in LDS; more share the
+// units, two and more at a time, and keep two.  bf16, us, chosen | next smaller | next
+// larger:
+//   256 x 256  1024 x 14336 x 4096 (224) 34 | 42 | -;         3000 x 5120 x 5120 (240) 43 | 52 | -
+//   128 x 128  512 x 8192 x 8192 (256) 31 | 44 | 64;          512 x 14336 x 4096 (448) 30 | 43 | 37
+//   128 x 64   512 x 4096 x 4096 (256) 11.7 | 13.1 | 14.5;    600 x 4096 x 4096 (320) 14.4 | 17.1 | 15.9
+//   64 x 64    256 x 4096 x 4096 (256) 7.9 | 9.6 | 10.7;      40 x 10000 x 4096 (157) 10.4 | 12.3 | 11.2
+//   32 x 64    128 x 4096 x 4096 (256) 6.9 | 7.1 | 7.7
+//   32 x 32    64 x 4096 x 4096 (256) 5.5 | - | 6.7
+// Four stages in LDS against two: 512 x 8192 x 8192 31 against 38, 256 x 4096 x 4096 7.9
+// against 11.4; two with more than one tile a unit: 512 x 14336 x 4096 30 against 35.
+constexpr int kCus = 256;
+constexpr int kEnough = 180, kEnough64 = 140;
 
 // Scales of rows that are not whole words: through LDS where stages are many and
-// tiles large (4096 x 4096 x 4128 52 us against 65), each lane its own where not (64 x
-// 4096 x 4128 7.6 against 8.7).
-template <int WM, int WN, int TM, int TN, int KG, int OCC>
+// waves share them (4096 x 4096 x 4128 54 us against 65, 850 x 900 x 4128 10.9 against
+// 11.5), each lane its own where not (850 x 900 x 544 5.0 against 5.3, 64 x 4096 x 4128 in
+// teams 7.0 against 7.6).
+template <int WM, int WN, int TM, int TN, int KG, int D, int OCC>
 static void launch_scales(const Mx4GemmArgs& a, hipStream_t s) {
   const bool words = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.sa) | reinterpret_cast<uintptr_t>(a.sw)) & 3u) == 0;
-  if (words) launch_tile<WM, WN, TM, TN, KG, kCopied, OCC>(a, s);
-  else if (KG <= 2 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, KG <= 2 ? kBrought : kOwn, OCC>(a, s);
-  else launch_tile<WM, WN, TM, TN, KG, kOwn, OCC>(a, s);
+  if (words) launch_tile<WM, WN, TM, TN, KG, D, kCopied, OCC>(a, s);
+  else if (KG == 1 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, D, KG == 1 ? kBrought : kOwn, OCC>(a, s);
+  else launch_tile<WM, WN, TM, TN, KG, D, kOwn, OCC>(a, s);
 }
 
 static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
+  auto count = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   // enough of them, and more than half of one filled either way
-  auto fit = [&](int bm, int bn, int enough) {
-    return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn) >= enough && 2 * a.M > bm && 2 * a.N > bn;
-  };
-  if (fit(256, 256, kEnough)) launch_scales<4, 2, 2, 4, 1, 1>(a, s);
-  else if (fit(128, 128, kEnough)) launch_scales<2, 2, 2, 2, 1, 2>(a, s);
-  else if (fit(64, 64, 2 * kEnough)) launch_scales<2, 2, 1, 1, 1, 4>(a, s);
-  else if (fit(64, 64, kEnough)) launch_scales<2, 2, 1, 1, 2, 2>(a, s);
-  else if (fit(32, 64, kEnough)) launch_scales<1, 2, 1, 1, 4, 1>(a, s);
-  else launch_scales<1, 1, 1, 1, 4, 1>(a, s);
+  auto fit = [&](int bm, int bn, int enough) { return count(bm, bn) >= enough && 2 * a.M > bm && 2 * a.N > bn; };
+  if (fit(256, 256, kEnough)) {
+    launch_scales<4, 2, 2, 4, 1, 2, 1>(a, s);
+  } else if (fit(128, 128, kEnough)) {
+    if (count(128, 128) <= kCus) launch_scales<2, 2, 2, 2, 1, 4, 1>(a, s);
+    else launch_scales<2, 2, 2, 2, 1, 2, 2>(a, s);
+  } else if (fit(128, 64, kEnough)) {
+    if (count(128, 64) <= kCus) launch_scales<2, 2, 2, 1, 1, 4, 1>(a, s);
+    else launch_scales<2, 2, 2, 1, 1, 2, 2>(a, s);
+  } else if (fit(64, 64, kEnough64)) {
+    launch_scales<2, 2, 1, 1, 1, 4, 2>(a, s);
+  } else if (count(32, 64) >= kEnough && 2 * a.N > 64) {
+    if (count(32, 64) <= kCus) launch_scales<1, 2, 1, 1, 2, 4, 1>(a, s);
+    else launch_scales<1, 2, 1, 1, 1, 4, 1>(a, s);
+  } else {
+    launch_scales<1, 1, 1, 1, 2, 4, 1>(a, s);
+  }
 }
 
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
   Mx4GemmArgs a = args;
   a.stream = a.M * a.N * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
   // A few rows are bound by the weights' bytes, which go straight to registers while
-  // there is a workgroup for each compute unit: 16 x 4096 x 14336 9.5 us (32 x 64 tiles
-  // 15), one row 7.3.  With more columns tiles read the rows of A less often: 16 x 8192 x
-  // 8192 9.6 us in 32 x 32 tiles, 13.7 in rows.  Tiles need four blocks of K.
+  // there is a workgroup for each compute unit: 16 x 4096 x 14336 11.0 us (32 x 32 tiles
+  // 12.8), one row 8.9.  With more columns tiles read the rows of A less often: 16 x 8192 x
+  // 8192 10.2 us in 32 x 32 tiles, 14.4 in rows.  Tiles need four blocks of K.
   if (a.K < 128) launch_rows<4, 8>(a, s);
   else if (a.M <= 16 && a.N <= 4096) launch_rows<1, 8>(a, s);
   else launch_tiles(a, s);

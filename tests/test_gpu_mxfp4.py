@@ -334,6 +334,24 @@ def test_gemm_every_tile(m, n, k):
     check_gemm(got[:, torch.from_numpy(at).to(DEV)], *a, w[0][at], w[1][at], torch.bfloat16)
 
 
+@pytest.mark.parametrize("m,n", [(3400, 3601), (2200, 2113), (1793, 1700), (1500, 1703), (1300, 1201), (1100, 1111), (850, 901),
+                                 (447, 1201), (400, 1000), (100, 100), (9000, 5)])
+@pytest.mark.parametrize("k", [128, 160, 256, 288, 384, 544, 640, 800, 992, 1056, 1152, 1312, 1504, 1568, 1792, 2048, 2080])
+def test_gemm_every_number_of_stages(m, n, k):
+    """One to nine stages of K in each tile, one round of it or more, and each way of the scales; what lies before
+    and behind C stays."""
+    rng = _rng(m + n + k)
+    a, w = _operand(rng, m, k), _operand(rng, n, k)
+    dtype = [torch.bfloat16, torch.float16, torch.float32][k // 32 % 3]
+    room = torch.full((m * n + 256,), 77.0, dtype=dtype, device=DEV)
+    got = hr.mxfp4_gemm(*map(_t, a + w), dtype=dtype, out=room[128:128 + m * n].view(m, n))
+    assert (room[:128] == 77).all() and (room[128 + m * n:] == 77).all()
+    at = np.unique(np.concatenate([np.arange(5), np.arange(m - 5, m), rng.integers(0, m, 100)]))
+    check_gemm(got[torch.from_numpy(at).to(DEV)], a[0][at], a[1][at], *w, dtype)
+    at = np.unique(np.concatenate([np.arange(5), np.arange(n - 5, n), rng.integers(0, n, 100)]))
+    check_gemm(got[:, torch.from_numpy(at).to(DEV)], *a, w[0][at], w[1][at], dtype)
+
+
 @pytest.mark.parametrize("m", [1, 16, 100, 300])
 def test_gemm_long_rows(m):
     rng = _rng(m)
