@@ -265,6 +265,19 @@ def test_calls_go_to_the_tensors_device(monkeypatch, current):
     assert seen == [(5, 101, 1)] and now[0] == current
 
 
+@pytest.mark.parametrize("current,fast", [(0, True), (1, True), (0, False)])
+def test_outputs_are_made_on_the_tensors_device(monkeypatch, current, fast):
+    made = []
+    monkeypatch.setattr(hr, "_get_device", lambda: current)
+    monkeypatch.setattr(hr, "_empty_cuda", (lambda *a: made.append(("fast", *a))) if fast else None)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append(("empty", *a, k)))
+    hr._new(0, 3, 5, torch.uint8)
+    if fast and current == 0:
+        assert made == [("fast", (3, 5), (5, 1), torch.uint8)]
+    else:
+        assert made == [("empty", (3, 5), {"dtype": torch.uint8, "device": torch.device("cuda", 0)})]
+
+
 def test_a_call_that_fails_raises():
     def hr_call(stream):
         return hr.HR_EDEVICE
