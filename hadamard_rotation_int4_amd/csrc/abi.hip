@@ -840,8 +840,8 @@ int32_t hr_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uin
   if (!kv4_dtype(dtype)) return fail(HR_EINVAL, "%s: dtype must be HR_F32, HR_BF16 or HR_F16", fn);
   if (K <= 0 || K % hr::kMxBlock || K > hr::kMxMaxN)
     return fail(HR_EUNSUPPORTED, "%s: K=%lld is not a multiple of 32 in [32, 2^18]", fn, (long long)K);
-  // what one launch holds: 2^20 tiles of 256 x 256, and of 64 x 16 where K is less than a tile needs
-  if (M > (1 << 21) || N > (1 << 21) || M * N > int64_t(1) << (K < 128 ? 30 : 36))
+  // what one launch holds: 2^20 tiles of 256 x 256 (K below 128: 2^22 of 128 x 128)
+  if (M > (1 << 21) || N > (1 << 21) || M * N > int64_t(1) << 36)
     return fail(HR_EUNSUPPORTED, "%s: M=%lld, N=%lld too large", fn, (long long)M, (long long)N);
   const bool some = M > 0 && N > 0;
   if (some && (!a_codes || !a_scales || !w_codes || !w_scales || !c))

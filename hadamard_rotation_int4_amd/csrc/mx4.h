@@ -46,7 +46,6 @@ struct Mx4GemmArgs {
   int K;
   int dtype;             // of c
   void* c;               // [M][N]
-  int stream;            // set by the launcher: nontemporal stores of c
 };
 
 // r = x + scale gate (block or its norm), h = weight r / rms(r), after host

@@ -44,35 +44,21 @@ __device__ __forceinline__ void store_c(const Mx4GemmArgs& p, int64_t at, float 
   else reinterpret_cast<_Float16*>(p.c)[at] = (_Float16)v;
 }
 
-// Eight of them at any address; around the L2s where C is large.
-template <int DT, bool NT>
-__device__ __forceinline__ void store_octet_as(void* c, int64_t at, const float* v) {
+// 16 bytes of a row of C at any address: four elements in 32 bits, eight in 16; around
+// the L2s with NT.
+template <bool NT>
+__device__ __forceinline__ void store_unit_c(const Mx4GemmArgs& p, int64_t at, const float* v) {
   typedef uint32_t u32x4_any __attribute__((ext_vector_type(4), aligned(2)));
-  u32x4_any* q = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(c) + at * (DT == kDtF32 ? 4 : 2));
+  u32x4_any x;
 #pragma unroll
-  for (int i = 0; i < (DT == kDtF32 ? 2 : 1); ++i) {
-    u32x4_any x;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if (DT == kDtF32) x[e] = __float_as_uint(v[4 * i + e]);
-      else if (DT == kDtBf16) x[e] = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
-      else x[e] = __builtin_bit_cast(uint32_t, (half2v){(_Float16)v[2 * e], (_Float16)v[2 * e + 1]});
-    }
-    if (NT) __builtin_nontemporal_store(x, q + i);
-    else q[i] = x;
+  for (int e = 0; e < 4; ++e) {
+    if (p.dtype == kDtF32) x[e] = __float_as_uint(v[e]);
+    else if (p.dtype == kDtBf16) x[e] = __builtin_bit_cast(uint32_t, (bf16x2){(__bf16)v[2 * e], (__bf16)v[2 * e + 1]});
+    else x[e] = __builtin_bit_cast(uint32_t, (half2v){(_Float16)v[2 * e], (_Float16)v[2 * e + 1]});
   }
-}
-
-__device__ __forceinline__ void store_octet_c(const Mx4GemmArgs& p, int64_t at, const float* v) {
-  if (p.stream) {
-    if (p.dtype == kDtF32) store_octet_as<kDtF32, true>(p.c, at, v);
-    else if (p.dtype == kDtBf16) store_octet_as<kDtBf16, true>(p.c, at, v);
-    else store_octet_as<kDtF16, true>(p.c, at, v);
-  } else {
-    if (p.dtype == kDtF32) store_octet_as<kDtF32, false>(p.c, at, v);
-    else if (p.dtype == kDtBf16) store_octet_as<kDtBf16, false>(p.c, at, v);
-    else store_octet_as<kDtF16, false>(p.c, at, v);
-  }
+  u32x4_any* q = reinterpret_cast<u32x4_any*>(reinterpret_cast<char*>(p.c) + at * (p.dtype == kDtF32 ? 4 : 2));
+  if (NT) __builtin_nontemporal_store(x, q);
+  else *q = x;
 }
 
 // 16 columns and 16 MT rows of C a workgroup.  K goes in runs of 512 codes (four
@@ -215,20 +201,20 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // SM, how a lane gets its scales.  kCopied: copied into LDS, 16 bytes of each row
 // every second stage, where each row's are whole words.  kBrought: the same
 // through registers, at any alignment, for K of at least 512.  kOwn: each lane loads
-// its own words.
+// its own words, for K of at least 128.  kFew: its own bytes, for fewer than four blocks.
 //
 // KG: teams of WM WN waves that take pairs of stages in turn, each with buffers of
 // its own; their sums are joined in LDS, in the teams' order.  For the smallest tiles,
 // of which a workgroup would else be one or two waves.
-enum { kOwn, kCopied, kBrought };
+enum { kOwn, kCopied, kBrought, kFew };
 
-template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC, bool NT>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
   constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
   constexpr int ROWB = 128;                        // bytes of a row and stage
   constexpr int QA = BM / 8, QW = BN / 8;          // copies of 1 KB of a stage
   constexpr int DPW = (QA + QW) / WAVES;
-  constexpr bool SL = SM != kOwn;                  // through LDS
+  constexpr bool SL = SM == kCopied || SM == kBrought;             // through LDS
   constexpr int SA = (BM + 63) / 64, QS = SA + (BN + 63) / 64;     // copies of 64 rows' scales of two stages
   constexpr int SCB = SM == kCopied ? QS * 1024 : SL ? (BM + BN) * 16 : 16;      // bytes of them
   constexpr int SPW = (QS + WAVES - 1) / WAVES;    // copies of a wave
@@ -388,6 +374,13 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
         v[2 * i] = SM == kCopied && 8 * place(k) + 4 * h >= blocks ? 0u : x0;
         v[2 * i + 1] = SM == kCopied && 8 * place(k + 1) + 4 * h >= blocks ? 0u : x1;
       }
+    } else if constexpr (SM == kFew) {
+#pragma unroll
+      for (int i = 0; i < T; ++i) {
+        const uint8_t* s = (i < TM ? sa : sw) + srow[i];
+        const uint32_t b0 = s[0], b1 = s[min(1, blocks - 1)], b2 = s[blocks - 1];
+        v[i] = place(k) > 0 || h ? 0u : b0 | (blocks > 1 ? b1 << 8 : 0u) | (blocks > 2 ? b2 << 16 : 0u);
+      }
     } else {
       // past the end of a row its last word, shifted by use_scales
       const uint32_t from = min(8 * place(k) + 4 * h, blocks - 4);
@@ -399,6 +392,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     if constexpr (SL) {
 #pragma unroll
       for (int i = 0; i < T; ++i) sc[i] = v[2 * i + decltype(odd)::value];
+    } else if constexpr (SM == kFew) {
+#pragma unroll
+      for (int i = 0; i < T; ++i) sc[i] = v[i];
     } else {
       const int half = 4 * min(max(8 * place(k) + 4 * h - (blocks - 4), 0), 4);      // in two shifts: they may be 32 together
 #pragma unroll
@@ -585,32 +581,40 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
         *reinterpret_cast<v4f*>(part + l32 * PITCH + 16 * ((8 * j + 2 * q + h) ^ (l32 & 7))) =
             (v4f){acc[j][i][4 * q], acc[j][i][4 * q + 1], acc[j][i][4 * q + 2], acc[j][i][4 * q + 3]};
     __builtin_amdgcn_wave_barrier();
-    constexpr int LPR = CW / 8;                    // lanes of a row
+    auto store_rows = [&](auto unit) {
+      constexpr int U = decltype(unit)::value, LPR = CW / U;       // elements of a lane, lanes of a row
 #pragma unroll
-    for (int r = 0; r < 32; r += 64 / LPR) {
-      const int rr = r + lane / LPR, n = 8 * (lane % LPR), m = wm + 32 * i + rr;
-      const v4f x = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4) ^ (rr & 7)));
-      const v4f y = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4 + 1) ^ (rr & 7)));
-      const float v[8] = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
-      const int64_t to = (m0 + m) * p.N + n0 + wn + n;
-      const int left = m < rows_a ? rows_w - wn - n : 0;
-      if (left >= 8) {
-        store_octet_c(p, to, v);
-      } else {
+      for (int r = 0; r < 32; r += 64 / LPR) {
+        const int rr = r + lane / LPR, n = U * (lane % LPR), m = wm + 32 * i + rr;
+        float v[8];
+#pragma unroll
+        for (int q = 0; q < U / 4; ++q) {
+          const v4f x = *reinterpret_cast<const v4f*>(part + rr * PITCH + 16 * ((n / 4 + q) ^ (rr & 7)));
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[4 * q + e] = x[e];
+        }
+        const int64_t to = (m0 + m) * p.N + n0 + wn + n;
+        const int left = m < rows_a ? rows_w - wn - n : 0;
+        if (left >= U) {
+          store_unit_c<NT>(p, to, v);
+        } else {
 #pragma unroll 1
-        for (int e = 0; e < left; ++e)
-          store_c(p, to + e, *reinterpret_cast<const float*>(part + rr * PITCH + 16 * (((n + e) / 4) ^ (rr & 7)) + 4 * (e % 4)));
+          for (int e = 0; e < left; ++e)
+            store_c(p, to + e, *reinterpret_cast<const float*>(part + rr * PITCH + 16 * (((n + e) / 4) ^ (rr & 7)) + 4 * (e % 4)));
+        }
       }
-    }
+    };
+    if (p.dtype == kDtF32) store_rows(MxC<4>{});
+    else store_rows(MxC<8>{});
     __builtin_amdgcn_wave_barrier();
   }
 }
 
-template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC, bool NT = false>
 static void launch_tile(const Mx4GemmArgs& a, hipStream_t s) {
   constexpr int BM = 32 * WM * TM, BN = 32 * WN * TN;
   const int tm = (int)((a.M + BM - 1) / BM), tn = (int)((a.N + BN - 1) / BN);
-  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, D, SM, OCC>), dim3((unsigned)(tm * tn)),
+  hipLaunchKernelGGL((mx4_gemm_tile_kernel<WM, WN, TM, TN, KG, D, SM, OCC, NT>), dim3((unsigned)(tm * tn)),
                      dim3(64 * WM * WN * KG), 0, s, a, tm, tn);
 }
 
@@ -640,20 +644,32 @@ constexpr int kEnough = 180, kEnough64 = 140;
 // waves share them (4096 x 4096 x 4128 54 us against 65, 850 x 900 x 4128 10.9 against
 // 11.5), each lane its own where not (850 x 900 x 544 5.0 against 5.3, 64 x 4096 x 4128 in
 // teams 7.0 against 7.6).
-template <int WM, int WN, int TM, int TN, int KG, int D, int OCC>
+template <int WM, int WN, int TM, int TN, int KG, int D, int OCC, bool NT = false>
 static void launch_scales(const Mx4GemmArgs& a, hipStream_t s) {
   const bool words = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.sa) | reinterpret_cast<uintptr_t>(a.sw)) & 3u) == 0;
-  if (words) launch_tile<WM, WN, TM, TN, KG, D, kCopied, OCC>(a, s);
-  else if (KG == 1 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, D, KG == 1 ? kBrought : kOwn, OCC>(a, s);
-  else launch_tile<WM, WN, TM, TN, KG, D, kOwn, OCC>(a, s);
+  if (words) launch_tile<WM, WN, TM, TN, KG, D, kCopied, OCC, NT>(a, s);
+  else if (KG == 1 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, D, KG == 1 ? kBrought : kOwn, OCC, NT>(a, s);
+  else launch_tile<WM, WN, TM, TN, KG, D, kOwn, OCC, NT>(a, s);
 }
 
 static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
   auto count = [&](int bm, int bn) { return ((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
   // enough of them, and more than half of one filled either way
   auto fit = [&](int bm, int bn, int enough) { return count(bm, bn) >= enough && 2 * a.M > bm && 2 * a.N > bn; };
+  if (a.K < 128) {
+    if (fit(128, 128, kEnough)) launch_tile<2, 2, 2, 2, 1, 2, kFew, 2>(a, s);
+    else if (fit(64, 64, kEnough64)) launch_tile<2, 2, 1, 1, 1, 2, kFew, 4>(a, s);
+    else launch_rows<4, 8>(a, s);
+    return;
+  }
   if (fit(256, 256, kEnough)) {
-    launch_scales<4, 2, 2, 4, 1, 2, 1>(a, s);
+    // a large C in 16 bits around the L2s, where the operands are read for long and rows
+    // are whole lines: 8192 x 14336 x 4096 265 us against 271 (x 128 69 against 61; in 32 bits
+    // 4096 x 8192 x 4096 95 against 87; rows of 14335 x 256 109 against 77)
+    if (a.dtype != kDtF32 && a.M * a.N * 2 >= kStreamBytes && a.K >= 2048 && a.N % 64 == 0)
+      launch_scales<4, 2, 2, 4, 1, 2, 1, true>(a, s);
+    else
+      launch_scales<4, 2, 2, 4, 1, 2, 1>(a, s);
   } else if (fit(128, 128, kEnough)) {
     if (count(128, 128) <= kCus) launch_scales<2, 2, 2, 2, 1, 4, 1>(a, s);
     else launch_scales<2, 2, 2, 2, 1, 2, 2>(a, s);
@@ -670,15 +686,12 @@ static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
   }
 }
 
-hipError_t launch_mx4_gemm(const Mx4GemmArgs& args, hipStream_t s) {
-  Mx4GemmArgs a = args;
-  a.stream = a.M * a.N * (a.dtype == kDtF32 ? 4 : 2) >= kStreamBytes;
+hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t s) {
   // A few rows are bound by the weights' bytes, which go straight to registers while
   // there is a workgroup for each compute unit: 16 x 4096 x 14336 11.0 us (32 x 32 tiles
   // 12.8), one row 8.9.  With more columns tiles read the rows of A less often: 16 x 8192 x
-  // 8192 10.2 us in 32 x 32 tiles, 14.4 in rows.  Tiles need four blocks of K.
-  if (a.K < 128) launch_rows<4, 8>(a, s);
-  else if (a.M <= 16 && a.N <= 4096) launch_rows<1, 8>(a, s);
+  // 8192 10.2 us in 32 x 32 tiles, 14.4 in rows.
+  if (a.M <= 16 && a.N <= 4096) launch_rows<1, 8>(a, s);
   else launch_tiles(a, s);
   return hipGetLastError();
 }

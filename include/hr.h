@@ -687,7 +687,7 @@ int32_t hr_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, int64_t ro
  *   a_codes, a_scales  [M][K/2], [M][K/32];  w_codes, w_scales  [N][K/2],
  *             [N][K/32].
  *   K         a multiple of 32, at most 2^18;  M and N at most 2^21, M * N at
- *             most 2^36 (2^30 with K below 128).
+ *             most 2^36.
  *   c         [M][N] of dtype (HR_F32, HR_BF16 or HR_F16).
  */
 int32_t hr_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uint8_t* w_codes,

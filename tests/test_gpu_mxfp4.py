@@ -317,7 +317,7 @@ def test_gemm_tiles(m, n, k, dtype):
 
 @pytest.mark.parametrize("m,n,k", [(3400, 3601, 256), (3333, 3600, 288), (1700, 1801, 512), (1793, 1700, 544),
                                    (1400, 1150, 384), (1300, 1201, 416), (832, 1024, 640), (833, 1023, 672),
-                                   (12, 8200, 512), (16, 9001, 160), (12, 12000, 1152),
+                                   (12, 8200, 512), (16, 9001, 160), (12, 12000, 1152), (6000, 6016, 2048), (5999, 6016, 2080),
                                    # odd numbers of blocks past the first run of each kind
                                    (3400, 3601, 1056), (3333, 3600, 2080), (1700, 1801, 1120), (1793, 1700, 1088),
                                    (1400, 1150, 1184), (1300, 1201, 1504), (832, 1024, 1248), (833, 1023, 1376),
@@ -336,9 +336,9 @@ def test_gemm_every_tile(m, n, k):
 
 @pytest.mark.parametrize("m,n", [(3400, 3601), (2200, 2113), (1793, 1700), (1500, 1703), (1300, 1201), (1100, 1111), (850, 901),
                                  (447, 1201), (400, 1000), (100, 100), (9000, 5)])
-@pytest.mark.parametrize("k", [128, 160, 256, 288, 384, 544, 640, 800, 992, 1056, 1152, 1312, 1504, 1568, 1792, 2048, 2080])
+@pytest.mark.parametrize("k", [32, 64, 96, 128, 160, 256, 288, 384, 544, 640, 800, 992, 1056, 1152, 1312, 1504, 1568, 1792, 2048, 2080])
 def test_gemm_every_number_of_stages(m, n, k):
-    """One to nine stages of K in each tile, one round of it or more, and each way of the scales; what lies before
+    """Fewer blocks than a step takes, and one to nine stages of K in each tile, one round of it or more, and each way of the scales; what lies before
     and behind C stays."""
     rng = _rng(m + n + k)
     a, w = _operand(rng, m, k), _operand(rng, n, k)

@@ -107,7 +107,7 @@ def _gemm(**kw):
     (dict(M=(1 << 21) + 1), hr.HR_EUNSUPPORTED),
     (dict(N=1 << 40), hr.HR_EUNSUPPORTED),
     (dict(M=1 << 21, N=1 << 16, K=128), hr.HR_EUNSUPPORTED),
-    (dict(M=1 << 20, N=1 << 11), hr.HR_EUNSUPPORTED),
+    (dict(M=1 << 21, N=1 << 16), hr.HR_EUNSUPPORTED),
     (dict(M=0, a=None, sa=None, c=None), hr.HR_OK),
     (dict(N=0, w=None, sw=None, c=None), hr.HR_OK),
 ])
