@@ -14,9 +14,9 @@
 // rotated go through the matrix cores instead (mx4_rotate.hip).
 //
 // Bound by memory when there are many rows: without a rotation bf16 65536 x 2048 takes
-// 57 us to the format and 57 back (339 MB each, 5.9 TB/s, where a large copy reaches
-// 5.3 and one operand negated 6.1), fp32 1237 x 5120 6.2 and 6.6.  Bound by the launch
-// when there are few: one row of 4096 1.8 us.
+// 57 us to the format and 57 back, each over and over (339 MB, 5.9 TB/s, where a large
+// copy reaches 5.3 and one operand negated 6.1), fp32 1237 x 5120 6.8 and 6.9.  Bound by
+// the launch when there are few: one row of 4096 1.8 us.
 #include "mx4_device.h"
 
 namespace hr {

@@ -13,10 +13,11 @@
 // of H_32 are given to the instruction in the order in which its results come out
 // (v = 0 .. 15 of half h), so that a lane gets back elements 16 h + v: 8 bytes of codes.
 //
-// Bound by memory: bf16 65536 x 2048, order 128, takes 57 us to the format and 60 back
-// (339 MB each, 5.9 and 5.7 TB/s, where a large copy reaches 5.3 and one operand negated
-// 6.1).  With butterflies on the vector units, 17 instructions an element, it was
-// their issue (there and back 190 us); this takes 6 an element.
+// Bound by memory: bf16 65536 x 2048, order 128, takes 57 us to the format and 60 back,
+// each over and over (339 MB, 5.9 and 5.7 TB/s, where a large copy reaches 5.3 and one
+// operand negated 6.1); in turn 79 and 61, the rows read back still on their way to memory
+// when the next call's are asked for.  With butterflies on the vector units, 17
+// instructions an element, it was their issue (there and back 190 us); this takes 6.
 #include "mx4_device.h"
 
 namespace hr {
