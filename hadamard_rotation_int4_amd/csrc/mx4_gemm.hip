@@ -14,9 +14,9 @@
 // Rates on random codes: the 32x32x64 instruction alone, nothing loaded, reaches 6.4
 // PFLOP/s on the whole card (9.0 on zeros: the clock falls with the power drawn, from
 // 2.5 to 1.5 GHz), the 16x16x128 one 5.7.  The 256 x 256 tile reaches 4.1 at 4096 x 4096
-// x 14336 and 3.9 at 8192 x 14336 x 4096 (242 us), where the matrix cores are busy 48% of
-// the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute unit) 3.6 PFLOP/s, 38 us,
-// 7 of them stores at the end and 3 the first loads.  Of 119 us at 4096 x 4096 x 14336 the
+// x 14336 and 3.6 to 3.9 at 8192 x 14336 x 4096 (242 to 265 us), where the matrix cores are
+// busy 46% of the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute unit) 3.4 to 3.6
+// PFLOP/s, 38 to 41 us, 7 of them stores at the end and 3 the first loads.  Of 119 us at 4096 x 4096 x 14336 the
 // copies into LDS cost 19 (where they come from hardly matters: always of one stage, 115)
 // and the reads out of it 14: 192 KB read and 64 written a stage and workgroup, 2048
 // cycles of LDS, which is also what the products take.  What was tried on it made no
