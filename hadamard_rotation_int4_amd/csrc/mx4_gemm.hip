@@ -662,7 +662,9 @@ static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
     else launch_rows<4, 8>(a, s);
     return;
   }
-  if (fit(256, 256, kEnough)) {
+  // also where 128 x 128 tiles would begin a third round (two a unit): 1400 x 7000 x 4096 (168)
+  // 37 us against 45, 1100 x 7680 x 4096 (150) 36 against 39
+  if (fit(256, 256, kEnough) || (count(128, 128) > 2 * kCus && fit(256, 256, kCus / 2))) {
     // a large C in 16 bits around the L2s, where the operands are read for long and rows
     // are whole lines: 8192 x 14336 x 4096 265 us against 271 (x 128 69 against 61; in 32 bits
     // 4096 x 8192 x 4096 95 against 87; rows of 14335 x 256 109 against 77)

@@ -317,7 +317,7 @@ def test_gemm_tiles(m, n, k, dtype):
 
 @pytest.mark.parametrize("m,n,k", [(3400, 3601, 256), (3333, 3600, 288), (1700, 1801, 512), (1793, 1700, 544),
                                    (1400, 1150, 384), (1300, 1201, 416), (832, 1024, 640), (833, 1023, 672),
-                                   (12, 8200, 512), (16, 9001, 160), (12, 12000, 1152), (6000, 6016, 2048), (5999, 6016, 2080),
+                                   (12, 8200, 512), (16, 9001, 160), (12, 12000, 1152), (1100, 7680, 288), (1101, 7681, 1024), (6000, 6016, 2048), (5999, 6016, 2080),
                                    # odd numbers of blocks past the first run of each kind
                                    (3400, 3601, 1056), (3333, 3600, 2080), (1700, 1801, 1120), (1793, 1700, 1088),
                                    (1400, 1150, 1184), (1300, 1201, 1504), (832, 1024, 1248), (833, 1023, 1376),
