@@ -21,8 +21,9 @@
 // and the reads out of it 14: 192 KB read and 64 written a stage and workgroup, 2048
 // cycles of LDS, which is also what the products take.  What was tried on it made no
 // difference: other orders of its LDS reads, copies and products, waves' priorities,
-// copies spread over the steps, 4 waves of 128 x 128 (116 against 118 us), bank
-// conflicts taken out (270 against 272 us), dies starting at other stages of K.
+// copies spread over the steps, bank conflicts taken out (270 against 272 us), dies starting
+// at other stages of K; waves of 64 x 128 instead of 128 x 64 are 1% slower, 4 waves of
+// 128 x 128, alone on their SIMDs, 133 against 121 us.
 #include "mx4_device.h"
 
 namespace hr {
@@ -669,9 +670,9 @@ static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
     // are whole lines: 8192 x 14336 x 4096 265 us against 271 (x 128 69 against 61; in 32 bits
     // 4096 x 8192 x 4096 95 against 87; rows of 14335 x 256 109 against 77)
     if (a.dtype != kDtF32 && a.M * a.N * 2 >= kStreamBytes && a.K >= 2048 && a.N % 64 == 0)
-      launch_scales<4, 2, 2, 4, 1, 2, 1, true>(a, s);
+      launch_scales<2, 4, 4, 2, 1, 2, 1, true>(a, s);
     else
-      launch_scales<4, 2, 2, 4, 1, 2, 1>(a, s);
+      launch_scales<2, 4, 4, 2, 1, 2, 1>(a, s);
   } else if (fit(128, 128, kEnough)) {
     if (count(128, 128) <= kCus) launch_scales<2, 2, 2, 2, 1, 4, 1>(a, s);
     else launch_scales<2, 2, 2, 2, 1, 2, 2>(a, s);
