@@ -24,6 +24,7 @@
 // copies spread over the steps, bank conflicts taken out (270 against 272 us), dies starting
 // at other stages of K; waves of 64 x 128 instead of 128 x 64 are 1% slower, 4 waves of
 // 128 x 128, alone on their SIMDs, 133 against 121 us.
+#include "mx4_copy.h"
 #include "mx4_device.h"
 
 namespace hr {
@@ -182,7 +183,6 @@ __global__ __launch_bounds__(64 * WAVES) void mx4_gemm_rows_kernel(Mx4GemmArgs p
 template <int V>
 struct MxC { static constexpr int value = V; };
 
-constexpr int kNowhere = 0x40000000;     // past the end of every panel of an operand
 constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 
 // (32 WM TM) x (32 WN TN) outputs a workgroup of WM WN waves, TM x TN tiles of
@@ -200,7 +200,7 @@ constexpr int kSchedMfma = 0x8, kSchedDsRead = 0x100;
 // is permuted, within the row's 128 bytes.
 //
 // SM, how a lane gets its scales.  kCopied: copied into LDS, 16 bytes of each row
-// every second stage, where each row's are whole words.  kBrought: the same
+// every second stage, where each row's are whole runs of 16.  kBrought: the same
 // through registers, at any alignment, for K of at least 512.  kOwn: each lane loads
 // its own words, for K of at least 128.  kFew: its own bytes, for fewer than four blocks.
 //
@@ -212,7 +212,7 @@ enum { kOwn, kCopied, kBrought, kFew };
 template <int WM, int WN, int TM, int TN, int KG, int D, int SM, int OCC, bool NT>
 __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(Mx4GemmArgs p, int tiles_m, int tiles_n) {
   constexpr int WAVES = WM * WN, BM = 32 * WM * TM, BN = 32 * WN * TN, T = TM + TN;
-  constexpr int ROWB = 128;                        // bytes of a row and stage
+  constexpr int ROWB = kMxStageBytes;              // bytes of a row and stage
   constexpr int QA = BM / 8, QW = BN / 8;          // copies of 1 KB of a stage
   constexpr int DPW = (QA + QW) / WAVES;
   constexpr bool SL = SM == kCopied || SM == kBrought;             // through LDS
@@ -243,10 +243,10 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   const int high = min(8, tiles_m - 8 * group);
   const int64_t m0 = (int64_t)(8 * group + in % high) * BM, n0 = (int64_t)(in / high) * BN;
 
-  const int blocks = p.K / kMxBlock, stages = (blocks + 7) / 8, stride = p.K / 2;
+  const int blocks = p.K / kMxBlock, stages = mx4_stages(blocks), stride = p.K / 2;
   const int rows_a = (int)(p.M - m0 < BM ? p.M - m0 : BM), rows_w = (int)(p.N - n0 < BN ? p.N - n0 : BN);
-  // rows past the end lie past the buffer's end: nothing is read there, and what
-  // LDS holds for them (codes are finite whatever they are) goes into outputs
+  // rows past the end lie past the buffer's end (mx4_copy.h): nothing is read there, and
+  // what LDS holds for them (codes are finite whatever they are) goes into outputs
   // that are not stored
   const __amdgpu_buffer_rsrc_t ra =
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.a + m0 * stride), 0, rows_a * stride, 0x00020000);
@@ -254,13 +254,11 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       __builtin_amdgcn_make_buffer_rsrc((void*)(p.w + n0 * stride), 0, rows_w * stride, 0x00020000);
   // of even and odd copies; in the last stage chunks past the end take the row's last
   // one (under zero scales)
-  const int last = 8 * (stages - 1);
   int src[2], src_last[2];
 #pragma unroll
   for (int o = 0; o < 2; ++o) {
-    const int chunk = (lane & 7) ^ ((lane >> 4) + 4 * o);
-    src[o] = (lane >> 3) * stride + 16 * chunk;
-    src_last[o] = (lane >> 3) * stride + 16 * min(chunk, blocks - 1 - last);
+    src[o] = mx4_lane_offset(lane, o, blocks);
+    src_last[o] = mx4_lane_offset_last(lane, o, blocks);
   }
   auto buf = [&](auto b) -> char* {
     constexpr int B = decltype(b)::value;
@@ -283,14 +281,14 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     char* dst = buf(b);
     int v[2];
 #pragma unroll
-    for (int o = 0; o < 2; ++o) v[o] = s < stages - 1 ? src[o] : s < stages ? src_last[o] : kNowhere;
+    for (int o = 0; o < 2; ++o) v[o] = mx4_stage_offset(s, stages, src[o], src_last[o]);
 #pragma unroll
     for (int j = 0; j < DPW; ++j) {
       const int q = wave * DPW + j;
       const bool a = q < QA;
       __builtin_amdgcn_raw_ptr_buffer_load_lds(a ? ra : rw,
-                                               (__attribute__((address_space(3))) void*)(dst + 1024 * q), 16, v[j & 1],
-                                               8 * (a ? q : q - QA) * stride + s * ROWB, 0, 0);
+                                               (__attribute__((address_space(3))) void*)(dst + 1024 * q), 16,
+                                               mx4_copy_offset(v[j & 1], 8 * (a ? q : q - QA), blocks), s * ROWB, 0, 0);
     }
   };
 
@@ -310,10 +308,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     else srow[i] = (uint32_t)min(r, (i < TM ? rows_a : rows_w) - 1) * blocks;
   }
   // kCopied: of the team's stages 2 i and 2 i + 1; nothing is read behind the end of the
-  // operand, what is read of the next row behind the end of a row is not used
+  // operand or of K
   auto copy_scales = [&](int i, auto odd) {
     const int q = KG * i + team;
-    const int v = 2 * q < stages ? lane * blocks : kNowhere;
 #pragma unroll
     for (int j = 0; j < SPW; ++j) {
       // where waves are more than copies some make the same one
@@ -321,8 +318,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
       const bool a = c < SA;
       const __amdgpu_buffer_rsrc_t rs = __builtin_amdgcn_make_buffer_rsrc(
           (void*)(a ? sa : sw), 0, (a ? rows_a : rows_w) * blocks, 0x00020000);
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(slot(i, odd) + 1024 * c), 16, v,
-                                               64 * (a ? c : c - SA) * blocks + 16 * q, 0, 0);
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, (__attribute__((address_space(3))) void*)(slot(i, odd) + 1024 * c), 16,
+                                               mx4_scale_offset(lane, 64 * (a ? c : c - SA), q, blocks), 16 * q, 0, 0);
     }
   };
   // kBrought: a thread brings 16 bytes of its rows, of the team's stages 2 i and 2 i +
@@ -641,14 +638,17 @@ static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
 constexpr int kCus = 256;
 constexpr int kEnough = 180, kEnough64 = 140;
 
-// Scales of rows that are not whole words: through LDS where stages are many and
-// waves share them (4096 x 4096 x 4128 54 us against 65, 850 x 900 x 4128 10.9 against
-// 11.5), each lane its own where not (850 x 900 x 544 5.0 against 5.3, 64 x 4096 x 4128 in
-// teams 7.0 against 7.6).
+// Scales of rows that are not whole runs of 16: through registers into LDS where stages
+// are many and waves share them (4096 x 4096 x 4128 54 us against 65, 850 x 900 x 4128
+// 10.9 against 11.5), each lane its own where not (850 x 900 x 544 5.0 against 5.3, 64 x
+// 4096 x 4128 in teams 7.0 against 7.6).  Whole words could be copied as well, but the
+// last 16 bytes would pass the operand's end (4096 x 4096 x 4224 48.9 us instead of 51.0,
+// 512 x 4096 x 1152 7.2 instead of 7.6, 512 x 4096 x 640 the same 6.2).
 template <int WM, int WN, int TM, int TN, int KG, int D, int OCC, bool NT = false>
 static void launch_scales(const Mx4GemmArgs& a, hipStream_t s) {
-  const bool words = a.K % 128 == 0 && ((reinterpret_cast<uintptr_t>(a.sa) | reinterpret_cast<uintptr_t>(a.sw)) & 3u) == 0;
-  if (words) launch_tile<WM, WN, TM, TN, KG, D, kCopied, OCC, NT>(a, s);
+  // (copies of 16 bytes begin at whole words)
+  const bool whole = a.K % 512 == 0 && ((reinterpret_cast<uintptr_t>(a.sa) | reinterpret_cast<uintptr_t>(a.sw)) & 3u) == 0;
+  if (whole) launch_tile<WM, WN, TM, TN, KG, D, kCopied, OCC, NT>(a, s);
   else if (KG == 1 && a.K >= 1024) launch_tile<WM, WN, TM, TN, KG, D, KG == 1 ? kBrought : kOwn, OCC, NT>(a, s);
   else launch_tile<WM, WN, TM, TN, KG, D, kOwn, OCC, NT>(a, s);
 }
