@@ -436,10 +436,9 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
   };
 
   uint4 f0[T], f1[T];
-  // Loads of this wave that may be under way when the next stage has landed: those of the
-  // D - 2 stages behind it, and of their scales (of every second stage; kOwn of every
-  // stage).
-  constexpr int AWAY = (D - 2) * DPW + (SM == kCopied ? (D - 2) / 2 * SPW : SM == kBrought ? (D - 2) / 2 * SPT : (D - 2) * T);
+  // Copies of this wave that may be under way when the next stage has landed.
+  constexpr int AWAY = mx4_away(D, DPW, SM == kCopied ? SPW : 0), AWAY0 = mx4_away_first(D, DPW, SM == kCopied ? SPW : 0);
+  static_assert(AWAY0 < 64, "vmcnt's six bits");
   constexpr int WAIT = 0x0070 | (AWAY & 15) | (AWAY >> 4) << 14;      // vmcnt(AWAY) lgkmcnt(0)
   // the team's stage k from buffer B: the fragments of its first step are in f0
   auto stage = [&](int k, auto b) {
@@ -472,7 +471,8 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     use_scales(k + 1, MxC<NEXT % 2>{}, sn[SL ? 0 : NEXT]);
   };
 
-  // In the order that AWAY counts.
+  // Copies go out in the order in which stages take them: the waits count on it, and nothing
+  // else would keep the compiler to it, as they write arrays of their own.
   auto fence = [&]() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
@@ -485,6 +485,7 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     bring_scales(0);
     put_scales(0, MxC<0>{});
   }
+  fence();
   copy(place(1), MxC<1>{});
   fence();
   if constexpr (SM == kBrought) bring_scales(1);
@@ -498,8 +499,6 @@ __global__ __launch_bounds__(64 * WM * WN * KG, OCC) void mx4_gemm_tile_kernel(M
     copy(place(3), MxC<3>{});
     fence();
   }
-  // the first stage, of those that come in before the second one
-  constexpr int AWAY0 = D > 2 ? AWAY + DPW : 0;
   __builtin_amdgcn_s_waitcnt(0x0070 | (AWAY0 & 15) | (AWAY0 >> 4) << 14);
   mx_barrier();
   if (SL) load_scales(0, MxC<0>{}, sn[0]);

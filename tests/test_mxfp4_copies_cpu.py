@@ -4,6 +4,10 @@ A buffer's range check is sure to see a lane's vector offset; whether it counts 
 scalar offset too is not relied on.  So for rows 0 .. rows - 1 of `size` bytes each in a
 buffer of rows * size bytes, a lane's 16 bytes must be either nowhere (vector offset
 at or past the buffer's size) or inside one row, vector and scalar offset together.
+
+A stage waits until at most so many loads are under way.  Loads complete in order; the
+copies are certain to be among them, the compiler's plain loads are not, so the wait has
+to cover the next stage whether those are there or not.
 """
 import os
 import shutil
@@ -83,3 +87,57 @@ def test_copies_stay_in_their_rows(tmp_path, tile):
     blocks = [*range(1, 41), 64, 95, 96, 100, 256] + ([8190, 8192] if tile < 256 else [8192])
     r = subprocess.run([str(exe), str(tile), *map(str, blocks)], capture_output=True, text=True)
     assert r.returncode == 0, r.stdout
+
+
+WAITS = r"""
+#include <cstdio>
+#include <cstdlib>
+#include <vector>
+#include "mx4_copy.h"
+using namespace hr;
+
+int main(int argc, char** argv) {
+  const int depth = std::atoi(argv[1]), codes = std::atoi(argv[2]), scales = std::atoi(argv[3]), plain = std::atoi(argv[4]);
+  // loads in the order in which a wave issues them: stage s as s, scales of stages 2 i and
+  // 2 i + 1 as 1000 + i, plain loads as -1
+  std::vector<int> sent;
+  auto load = [&](int what, int n) { sent.insert(sent.end(), n, what); };
+  auto landed = [&](int away, int what) {
+    for (size_t i = sent.size() > (size_t)away ? sent.size() - away : 0; i < sent.size(); ++i)
+      if (sent[i] == what) { std::printf("%d is under way\n", what); std::exit(1); }
+  };
+  load(-1, plain);
+  load(0, codes);
+  load(1000, scales);
+  for (int s = 1; s < depth; ++s) {
+    load(s, codes);
+    load(-1, plain);
+    if (s % 2 == 0) load(1000 + s / 2, scales);
+  }
+  landed(mx4_away_first(depth, codes, scales), 0);
+  landed(mx4_away_first(depth, codes, scales), 1000);
+  for (int k = 0; k < 40; ++k) {
+    load(-1, plain);
+    const int away = mx4_away(depth, codes, scales);
+    landed(away, k + 1);
+    if (k % 2 == 1) landed(away, 1000 + (k + 1) / 2);
+    load(-1, plain);
+    load(k + depth, codes);
+    if (k % 2 == 0) load(1000 + k / 2 + depth / 2, scales);
+  }
+  return 0;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_waits_cover_the_next_stage(tmp_path):
+    src, exe = tmp_path / "waits.cpp", tmp_path / "waits"
+    src.write_text(WAITS)
+    subprocess.run(["g++", "-std=c++17", "-O2", "-I", CSRC, str(src), "-o", str(exe)], check=True)
+    for depth in (2, 4):
+        for codes in (2, 4, 6, 8, 12):
+            for scales in (0, 1, 2, 4):
+                for plain in (0, 1, 3, 8):
+                    r = subprocess.run([str(exe), *map(str, (depth, codes, scales, plain))], capture_output=True, text=True)
+                    assert r.returncode == 0, (depth, codes, scales, plain, r.stdout)
