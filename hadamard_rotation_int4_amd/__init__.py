@@ -951,7 +951,13 @@ def _strided(t, name: str, dtypes):
     return rows, n, step if rows > 1 else n, dtype
 
 
+def _row_length(n: int) -> None:
+    if n > _I32_MAX:          # ctypes would cut off what does not fit
+        raise ValueError(f"rows of {n} elements: at most {_I32_MAX}")
+
+
 def _mx_order(order, n: int, signs) -> int:
+    _row_length(n)
     if n <= 0 or n % 32:
         raise ValueError(f"rows of {n} elements are not whole blocks of 32")
     if not order:
@@ -1098,6 +1104,7 @@ def _norm(x, block_out, weight, post_norm, post_weight, gate, scale, eps, dtype,
     rows, n, step, xt = _strided(x, "x", _KV4_TYPES)
     if n < 1:
         raise ValueError("x: rows of no elements")
+    _row_length(n)
     if dtype is None:
         dtype = xt if block_out is None else getattr(block_out, "dtype", None)
     if dtype not in _KV4_TYPES:
