@@ -894,7 +894,8 @@ _MX_RULES = {"floor": 0, "ceil": 1}
 _MX_ORDERS = (32, 64, 128, 256)
 _U8, _F32 = torch.uint8, torch.float32
 _get_device = getattr(torch._C, "_cuda_getDevice", None)
-# torch.empty without its dispatch, 0.7 us instead of 1.5: a call of one token takes 6
+# torch.empty without its dispatch, 0.7 us instead of 1.5: a call of one token takes 6.  Not
+# a public function: where it is not there, or takes other arguments, torch.empty is taken.
 _empty_cuda = getattr(getattr(getattr(torch._C, "_dynamo", None), "guards", None), "_empty_strided_cuda", None)
 
 
@@ -911,8 +912,12 @@ def _launch(index: int, fn, *args) -> None:
 
 def _new(index: int, rows: int, n: int, dtype) -> torch.Tensor:
     """An output [rows][n] on device `index`."""
+    global _empty_cuda
     if _empty_cuda is not None and _get_device is not None and _get_device() == index:
-        return _empty_cuda((rows, n), (n, 1), dtype)
+        try:
+            return _empty_cuda((rows, n), (n, 1), dtype)
+        except TypeError:
+            _empty_cuda = None
     return torch.empty((rows, n), dtype=dtype, device=torch.device("cuda", index))
 
 

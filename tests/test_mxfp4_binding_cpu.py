@@ -31,3 +31,27 @@ def test_rows_past_the_c_type_are_refused(call, n):
     """Not cut to it: 2^32 + 64 elements would run as 64."""
     with pytest.raises(ValueError, match=f"rows of {n} elements"):
         call(n)
+
+
+def test_outputs_where_the_quick_way_takes_other_arguments(monkeypatch):
+    """A private function of torch that has changed is left alone from then on; running
+    out of memory is not that."""
+    calls, made = [], []
+
+    def other(size, stride, dtype, device):
+        calls.append(size)
+
+    def full(*a):
+        raise torch.OutOfMemoryError("out of memory")
+
+    monkeypatch.setattr(hr, "_get_device", lambda: 0)
+    monkeypatch.setattr(hr, "_empty_cuda", full)
+    with pytest.raises(torch.OutOfMemoryError):
+        hr._new(0, 3, 5, torch.uint8)
+    assert hr._empty_cuda is full
+    monkeypatch.setattr(hr, "_empty_cuda", other)
+    monkeypatch.setattr(torch, "empty", lambda *a, **k: made.append((a, k)))
+    for _ in range(2):
+        hr._new(0, 3, 5, torch.uint8)
+    want = (((3, 5),), {"dtype": torch.uint8, "device": torch.device("cuda", 0)})
+    assert made == [want, want] and hr._empty_cuda is None and not calls
