@@ -650,8 +650,10 @@ int32_t hr_quant_mxfp4(const void* x, int32_t x_dtype, int64_t x_stride, int64_t
  * Method; the sign diagonal of HARP's incoherence processing), block by block.
  * Both operands of a product rotated alike leave it as it is.
  *
- * The transform is computed in fp32 (1/sqrt(p) rounded to it); a value that is
- * not finite reaches every element of its Hadamard block.
+ * The transform is computed in fp32 (1/sqrt(p) rounded to it), its sums before
+ * the factor 1/sqrt(p); a value that is not finite reaches every element of its
+ * Hadamard block, and so does a sum past fp32's range (none where magnitudes
+ * are below 2^128 / p).  The same holds for reading back.
  *
  *   order   p in {32, 64, 128, 256}, dividing n.
  *   signs   [n] int8 +-1, 16-byte aligned, or NULL (all +1).
@@ -699,7 +701,9 @@ int32_t hr_mxfp4_gemm(const uint8_t* a_codes, const uint8_t* a_scales, const uin
  *   r = x + scale * gate * u       (the new residual stream)
  *   h = weight * r / sqrt(mean(r^2) + eps)
  * in fp32; h follows from r as computed, before it is rounded to be stored.
- * Without block_out, r = x, and h is the plain norm of x.
+ * Without block_out, r = x, and h is the plain norm of x.  Sums of squares are
+ * fp32 too: a row whose sum passes its range (magnitudes from 2^64 / sqrt(n) on
+ * may) counts as of infinite size, so that its finite elements' norm is 0.
  *
  *   x          [rows] rows of n elements of x_dtype, x_stride apart.
  *   block_out  the block's output o, [rows] rows of dtype, block_stride

@@ -177,3 +177,18 @@ def test_the_same_every_time():
         assert all(torch.equal(g, w) for g, w in zip(got, want))
         assert torch.equal(hr.dequant_mxfp4(*got[1:], order=64, signs=signs, dtype=torch.bfloat16), back)
         assert all(torch.equal(g, w) for g, w in zip(hr.rotate_quant_mxfp4(x, 128, signs), there))
+
+
+@pytest.mark.parametrize("n", [96, 2048, 20000])
+def test_magnitudes_up_to_what_sums_of_squares_hold(n):
+    """Below 2^64 / sqrt(n) as ever; a row whose sum passes fp32's range has infinite size."""
+    for stream, dtype in (("bf16", "bf16"), ("f32", "f32"), ("f32", "bf16")):
+        rng = _rng(n)
+        x = rng.uniform(-1, 1, (4, n)) * 2.0 ** 64 / np.sqrt(n) * 0.99
+        a = {"x": _t(x.astype(np.float32)).to(TYPES[stream]), "block_out": None, "weight": None, "post_norm": False,
+             "post_weight": None, "gate": None, "scale": 1.0, "eps": EPS}
+        got = hr.norm_residual(**a, dtype=TYPES[dtype])
+        check_each(a, got, TYPES[dtype])
+        a["x"] = a["x"] * 2.0 ** 30
+        r, h = hr.norm_residual(**a, dtype=TYPES[dtype])
+        assert r is a["x"] and not h.any()
