@@ -13,13 +13,15 @@
 //
 // Rates on random codes: the 32x32x64 instruction alone, nothing loaded, reaches 6.4
 // PFLOP/s on the whole card (9.0 on zeros: the clock falls with the power drawn, from
-// 2.5 to 1.5 GHz), the 16x16x128 one 5.7.  The 256 x 256 tile reaches 4.1 at 4096 x 4096
-// x 14336 and 3.6 to 3.9 at 8192 x 14336 x 4096 (242 to 265 us), where the matrix cores are
-// busy 46% of the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute unit) 3.4 to 3.6
-// PFLOP/s, 38 to 41 us, 7 of them stores at the end and 3 the first loads.  Of 119 us at 4096 x 4096 x 14336 the
-// copies into LDS cost 19 (where they come from hardly matters: always of one stage, 115)
-// and the reads out of it 14: 192 KB read and 64 written a stage and workgroup, 2048
-// cycles of LDS, which is also what the products take.  What was tried on it made no
+// 2.5 to 1.5 GHz), the 16x16x128 one 5.5.  The 256 x 256 tile reaches 3.9 to 4.1 at 4096 x
+// 4096 x 14336 and 3.5 to 3.9 at 8192 x 14336 x 4096 (247 to 272 us by the card), where the
+// matrix cores are busy 46% of the clocks, at 1.9 GHz; at 4096^3 (256 tiles, one a compute
+// unit) 3.2 to 3.7 PFLOP/s, 38 to 43 us, 7 of them stores at the end and 3 the first loads.
+// Of 119 us at 4096 x 4096 x 14336 products alone take 86, the copies into LDS cost 19 (where
+// they come from hardly matters: always of one stage, 115) and the reads out of it 14, one
+// after another: 192 KB read and 64 written a stage and workgroup are 2048 cycles of LDS, as
+// many as its products take, but a stage takes some 4400, for all waves meet at one barrier
+// a stage, then read and multiply together.  What was tried on it made no
 // difference: other orders of its LDS reads, copies and products, waves' priorities,
 // copies spread over the steps, bank conflicts taken out (270 against 272 us), dies starting
 // at other stages of K; waves of 64 x 128 instead of 128 x 64 are 1% slower, 4 waves of
@@ -623,9 +625,13 @@ static void launch_rows(const Mx4GemmArgs& a, hipStream_t s) {
 
 // Which tile, by how many of them there are for the 256 compute units: the largest of
 // which there is about one for each (kEnough), a few idle units costing less than
-// smaller tiles' traffic.  Up to one for each keeps four stages in LDS; more share the
-// units, two and more at a time, and keep two.  bf16, us, chosen | next smaller | next
-// larger:
+// smaller tiles' traffic.  Up to one for each keeps four stages in LDS; more of the larger
+// tiles share the units, two and more at a time, and keep two.  64 x 64 and 32 x 64 keep
+// four however many they are: two of them share a unit all the same, and long rows gain
+// what short ones lose (64 x 64, 1100 x 1111 (324) x 4096 12.6 against 13.1 with two, x
+// 1024 7.2 against 6.9; 32 x 64, 30 x 20000 (313) x 4096 15.6 against 17.1, x 1024 6.2 against
+// 6.0).  Past one for each 32 x 64 has one team, whose waves alone are enough (two teams
+// 17.4, x 1024 8.5).  bf16, us, chosen | next smaller | next larger:
 //   256 x 256  1024 x 14336 x 4096 (224) 34 | 42 | -;         3000 x 5120 x 5120 (240) 43 | 52 | -
 //   128 x 128  512 x 8192 x 8192 (256) 31 | 44 | 64;          512 x 14336 x 4096 (448) 30 | 43 | 37
 //   128 x 64   512 x 4096 x 4096 (256) 11.7 | 13.1 | 14.5;    600 x 4096 x 4096 (320) 14.4 | 17.1 | 15.9
@@ -691,8 +697,9 @@ static void launch_tiles(const Mx4GemmArgs& a, hipStream_t s) {
 hipError_t launch_mx4_gemm(const Mx4GemmArgs& a, hipStream_t s) {
   // A few rows are bound by the weights' bytes, which go straight to registers while
   // there is a workgroup for each compute unit: 16 x 4096 x 14336 11.0 us (32 x 32 tiles
-  // 12.8), one row 8.9.  With more columns tiles read the rows of A less often: 16 x 8192 x
-  // 8192 10.2 us in 32 x 32 tiles, 14.4 in rows.
+  // 12.8), one row 8.9, operands past the caches.  With more columns tiles read the rows of
+  // A less often: 16 x 8192 x 8192 10.2 us in 32 x 32 tiles, 14.4 in rows (one row of more
+  // columns was not measured both ways: 1 x 14336 x 4096 9.9 us in tiles).
   if (a.M <= 16 && a.N <= 4096) launch_rows<1, 8>(a, s);
   else launch_tiles(a, s);
   return hipGetLastError();

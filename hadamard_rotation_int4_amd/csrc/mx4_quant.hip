@@ -15,8 +15,10 @@
 //
 // Bound by memory when there are many rows: without a rotation bf16 65536 x 2048 takes
 // 57 us to the format and 57 back, each over and over (339 MB, 5.9 TB/s, where a large
-// copy reaches 5.3 and one operand negated 6.1), fp32 1237 x 5120 6.8 and 6.9.  Bound by
-// the launch when there are few: one row of 4096 1.8 us.
+// copy reaches 5.3 and one operand negated 6.1), fp32 1237 x 5120 6.8 and 6.9.  fp32 rows
+// through a rotation of order 128, operands past the caches: 65536 x 2048 113 us to the format
+// and 172 back (608 MB, 5.4 and 3.5 TB/s; back, a lane's two stores are 32 bytes apart),
+// 1237 x 5120 8.4 and 11.1.  Bound by the launch when there are few: one row of 4096 1.8 us.
 #include "mx4_device.h"
 
 namespace hr {

@@ -9,15 +9,25 @@
 // h is rounded once to its type, or goes to MXFP4 (mx4_quant.hip) unrounded,
 // rotated on the way if asked.
 //
-// A row is held in registers by a workgroup, or by 8 to 64 lanes of a wave where it is
-// short, an octet of 8 elements a lane and turn, so that every operand is read once.
-// Workgroups stay for many rows: weights are read once, and a row's operands are
-// asked for before the sums of the row before it, whose waits they then hide.
+// A row is held by a workgroup, or by 8 to 64 lanes of a wave where it is short, an octet
+// of 8 elements a lane and turn, so that every operand is read once.  Workgroups stay for
+// many rows: weights are read once up to 8192 elements (for each row past them), and a
+// row's operands are asked for before the sums of the row before it, whose waits they
+// then hide.
+//
+// All of a row is in registers up to 8192 elements, and up to 16384 where the result is not
+// MXFP4 and stream and block are not both fp32.  Past 8192 a workgroup has 1024 threads of
+// 128 registers; what does not fit goes through scratch: up to 16384 elements 8 to 31
+// registers, past them 126 to 186, with an fp32 stream and block 513 to 643.
 //
 // Bound by memory when there are many rows: bf16 16384 x 4096 with a block, its norm
 // and a gate takes 92 us (537 MB, 5.8 TB/s, where a large copy reaches 5.3 and one
 // operand negated 6.1), to MXFP4 through a rotation 75 (438 MB).  Bound by the launch
-// and two sums over the row when there are few: one row of 4096 3.2 us.
+// and two sums over the row when there are few: one row of 4096 3.2 us.  By waves, of which
+// more than 128 registers leave 3 a SIMD, to MXFP4 at 4097 to 8192 elements: 16384 x 5120
+// 205 us where bf16 results take 118.  By rows at odd addresses: 32768 x 2047 205 us where
+// 2048 take 96.  By scratch past 16384: 1024 x 32768 119 us (bf16, 268 MB), in fp32 222
+// (537 MB).
 #pragma once
 
 #include "mx4_device.h"
@@ -302,8 +312,8 @@ static void launch_rows(const NormArgs& a, hipStream_t s) {
   const int64_t turns = (a.rows + ROWS - 1) / ROWS, most = 256 * 1024 / THREADS;
   const dim3 grid((unsigned)(turns < 4 * most ? turns : most)), threads(THREADS);
   // large streams of aligned rows: 16384 x 4096 bf16 95 us against 102 without the hint, to
-  // MXFP4 78 against 88; of rows that share lines, 16384 x 4094 124 against 113, fp32 16384 x
-  // 4095 182 against 163
+  // MXFP4 78 against 88; of rows that share lines, 16384 x 4094 bf16 126 against 116, 16384 x
+  // 4095 of an fp32 stream and a bf16 block 186 against 168, of an fp32 block 288 against 264
   const bool nt = a.rows * a.n * (XT == kDtF32 ? 4 : 2) >= kStreamBytes && a.n % 8 == 0;
   if (a.codes) {
     if (nt) hipLaunchKernelGGL((norm_kernel<XT, DT, LANES, CH, true, true>), grid, threads, 0, s, a);
