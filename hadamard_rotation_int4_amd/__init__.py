@@ -170,6 +170,14 @@ def _ptrs(*args):
     return out
 
 
+_I32_MAX, _I64_MAX = 2 ** 31 - 1, 2 ** 63 - 1
+
+
+def _row_length(n: int) -> None:
+    if n > _I32_MAX:          # ctypes would cut off what does not fit
+        raise ValueError(f"rows of {n} elements: at most {_I32_MAX}")
+
+
 def _rows_of(x, name: str, dtypes):
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor, got {type(x).__name__}")
@@ -177,6 +185,7 @@ def _rows_of(x, name: str, dtypes):
         raise ValueError(f"{name}: expected a 2-D [rows][n] tensor, got shape {tuple(x.shape)}")
     if x.dtype not in dtypes:
         raise TypeError(f"{name}: dtype {x.dtype} not in {[_DT_NAME[d] for d in dtypes]}")
+    _row_length(int(x.shape[1]))
     return int(x.shape[0]), int(x.shape[1])
 
 
@@ -725,9 +734,6 @@ def _kv4_ptr(cache, t, name: str) -> int:
     return t.data_ptr()
 
 
-_I32_MAX, _I64_MAX = 2 ** 31 - 1, 2 ** 63 - 1
-
-
 def _kv4_size(v, name: str, most: int) -> int:
     """An integer of the C call's range: ctypes would cut off what does not fit."""
     try:
@@ -954,11 +960,6 @@ def _strided(t, name: str, dtypes):
     if (last != 1 and n > 1) or (rows > 1 and step < n):
         raise ValueError(f"{name}: the elements of a row must be contiguous and rows must not overlap")
     return rows, n, step if rows > 1 else n, dtype
-
-
-def _row_length(n: int) -> None:
-    if n > _I32_MAX:          # ctypes would cut off what does not fit
-        raise ValueError(f"rows of {n} elements: at most {_I32_MAX}")
 
 
 def _mx_order(order, n: int, signs) -> int:
